@@ -35,8 +35,8 @@
  *    argument returns its error code and enqueues nothing.  Thread-local
  *    detail is available from w8_last_error().
  *  - Kernels never trap.  A GEMM whose internal pipeline wait runs past its
- *    deadline (2 s), or an ln_modulate_quant block whose row-buffer wait
- *    does, stops, records W8_ERR_TIMEOUT in a device error word and
+ *    deadline (2 s), a cross_attention block or an ln_modulate_quant block
+ *    whose wait does, stops, records W8_ERR_TIMEOUT in a device error word and
  *    returns; w8_poll_device_error() reports and clears it.
  */
 #ifndef W8LIN_H
@@ -87,7 +87,7 @@ const char* w8_last_error(void);
 w8_status w8_device_check(void);
 
 /* Synchronises `stream`, then returns W8_ERR_TIMEOUT (and clears the word)
- * if any GEMM launched so far on the current device recorded a pipeline
+ * if any kernel launched so far on the current device recorded a pipeline
  * timeout, else W8_OK. */
 w8_status w8_poll_device_error(void* stream);
 
@@ -405,6 +405,98 @@ w8_status bf16_gate_up_swiglu_ex(const uint16_t* x, int64_t M, int64_t K, const 
 w8_status ln_modulate_quant(const uint16_t* x, int64_t M, int64_t K, const uint16_t* shift,
                             const uint16_t* scale, int64_t rows_per_sample, float eps,
                             const float* s_in, uint8_t* q, uint16_t* h, void* stream);
+
+/*
+ * add_rms_norm_quant — the residual's addition, the root-mean-square norm and
+ * the quantization that stand between two linear sites, in one pass.  Per row:
+ *   r = fl32(x + res)                     (r = x without a residual)
+ *   i = 1 / sqrt(mean(r^2) + eps)         (binary32, reciprocal root within 2 ulps)
+ *   h = fl32(fl32(r * w) * i)
+ *   s = *s_in, or with s_tok this row's max(fl32(max|h| / 448), 2^-126)
+ *   q = E4M3_satRNE( fl32(h * fl32(1/s)) )
+ * r is not rounded before the norm nor h before the quantization.  A row with
+ * a NaN has a NaN scale and NaN codes; a zero row has zero codes.
+ *   x, res, w   [M, K], [M, K], [K] of dtype (W8_DTYPE_BF16 or W8_DTYPE_F16),
+ *               device; res may be NULL; 8 <= K <= 16384, K % 8 == 0
+ *   eps         finite and >= 0 (0 on a zero row gives NaN, as the formula does)
+ *   s_in        device float scalar, a calibrated scale; or NULL with s_tok
+ *   s_tok       [M] floats, device, written: each token's own scale; or NULL
+ *   q           E4M3 [M, K], device, written; NULL (with s_in and s_tok NULL):
+ *               h only
+ *   h           [M, K] of dtype, device, written: round16(h); may be NULL
+ *   res_out     [M, K] of dtype, device, written: round16(r); may be NULL, and
+ *               may be res or x itself
+ * Arrays 16-byte aligned (s_in, s_tok: 4).  M == 0 launches nothing.
+ * Errors: DTYPE, SHAPE, PARAM (eps; s_in and s_tok both given), NULL (x, w,
+ * both outputs, q without a scale or a scale without q, res_out without res),
+ * ALIGN, ARCH, CUDA.
+ */
+w8_status add_rms_norm_quant(const void* x, const void* res, int32_t dtype, int64_t M, int64_t K, const void* w,
+                             float eps, const float* s_in, float* s_tok, uint8_t* q, void* h, void* res_out,
+                             void* stream);
+
+/*
+ * fp8_linear_w8a8_pertoken — G (1..3) E4M3 linears that share an activation
+ * whose tokens have scales of their own (add_rms_norm_quant's s_tok), on
+ * weights with a scale for each output channel:
+ *   y_g[m,n] = bf16_RNE( fl32( fl32(s_tok[m] * acc) * s_ch_g[n] ) ),
+ *   acc = sum_k dec(qx[m,k]) * dec(w_g[n,k])   (F32 on the tensor cores).
+ *   qx     E4M3 [M, K], device;  s_tok  [M] floats, device
+ *   w      HOST array of G device pointers, E4M3 [N_g, K];  N  HOST array
+ *   s_ch   HOST array of G device pointers, [N_g] floats, 16-byte aligned
+ *   y      HOST array of G device pointers, bf16 [M, N_g], written
+ * The order of the sum depends on M, N, K and G alone: equal calls give equal
+ * bits.  Errors: SHAPE (group size, K % 16, N % 16), NULL, ALIGN, ARCH, CUDA.
+ */
+w8_status fp8_linear_w8a8_pertoken(const uint8_t* qx, int64_t M, int64_t K, const float* s_tok, int32_t G,
+                                   const uint8_t* const* w, const int64_t* N, const float* const* s_ch,
+                                   uint16_t* const* y, void* stream);
+
+/* Sizes and layout of a cross attention.  Strides are in elements, in the
+ * order (sample, position, head); the head's dimensions are contiguous.  Each
+ * is a positive multiple of 8 (dimensions of one entry aside); the sample's
+ * stride of q, k or v may be 0 where all samples share one array. */
+typedef struct {
+  int64_t B, Lq, Lk;     /* samples, queries, keys; any may be 0 */
+  int64_t Hq, Hkv, D;    /* heads; Hq a multiple of Hkv, at most 128 times it; 8 <= D <= 128, D % 8 == 0 */
+  int64_t q_stride[3], k_stride[3], v_stride[3], o_stride[3];
+  int64_t mask_stride;   /* bytes between the samples of kv_mask (0: one for all) */
+  int32_t dtype;         /* of q, k, v: W8_DTYPE_BF16 or W8_DTYPE_F16 */
+  float scale;           /* of the scores, finite and > 0 (usually 1 / sqrt(D)) */
+} w8_attention_desc;
+
+/*
+ * cross_attention — softmax attention of Lq queries over the Lk keys and
+ * values of an encoder, for each sample b and query head h, with key head
+ * h / (Hq / Hkv):
+ *   o[b,l,h] = sum_j p_j v[b,j] / sum_j p_j,  p_j = exp(scale * q[b,l,h] . k[b,j] - max)
+ * over the keys j that count: j < kv_len[b] and kv_mask[b,j] != 0.  A row for
+ * which no key counts is 0.  What K and V hold at keys that do not count (NaN
+ * included) has no effect.  Scores, sums and the accumulator are binary32, p
+ * is rounded to dtype for the product with V.
+ *   desc     host struct, read during the call only
+ *   q        [B, Lq, Hq, D], k, v [B, Lk, Hkv, D] of dtype, device
+ *   kv_len   [B] int32, device (clamped to 0 .. Lk), or NULL
+ *   kv_mask  [B, Lk] bytes, device, nonzero where a key counts, or NULL
+ *   s_out    NULL: out is of dtype, round16(o).  Device float scalar: out is
+ *            E4M3_satRNE( fl32(o * fl32(1/s_out)) ), the codes that an
+ *            out-projection with that input scale reads
+ *   out      [B, Lq, Hq, D] by o_stride, device, written
+ *   ws       ws_floats floats, device, of which cross_attention_workspace()
+ *            says how many the call needs (none when it says 0: may be NULL);
+ *            its contents need no set-up and mean nothing afterwards
+ * Equal calls give equal bits.  B == 0 or Lq == 0 launches nothing; Lk == 0
+ * writes zeros.
+ * Errors: NULL, SHAPE (sizes, workspace too small), STRIDE, DTYPE, PARAM
+ * (scale), ALIGN (16 bytes; kv_len and s_out 4), ARCH, CUDA.
+ */
+w8_status cross_attention(const w8_attention_desc* desc, const void* q, const void* k, const void* v,
+                          const int32_t* kv_len, const uint8_t* kv_mask, const float* s_out, void* out, float* ws,
+                          int64_t ws_floats, void* stream);
+
+/* Floats of workspace that cross_attention needs for these sizes on the
+ * current device (it splits few queries along the keys).  Errors as above. */
+w8_status cross_attention_workspace(const w8_attention_desc* desc, int64_t* floats);
 
 /*
  * step_policy_dispatch — host-only, pure function of (policy, step, num_steps).

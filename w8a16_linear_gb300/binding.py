@@ -40,6 +40,13 @@ class SwigluParams(ctypes.Structure):
                 ("beta", ctypes.c_float)]
 
 
+class AttentionDesc(ctypes.Structure):
+    """Mirror of ``w8_attention_desc``."""
+    _fields_ = [("B", _i64), ("Lq", _i64), ("Lk", _i64), ("Hq", _i64), ("Hkv", _i64), ("D", _i64),
+                ("q_stride", _i64 * 3), ("k_stride", _i64 * 3), ("v_stride", _i64 * 3), ("o_stride", _i64 * 3),
+                ("mask_stride", _i64), ("dtype", _i32), ("scale", ctypes.c_float)]
+
+
 SIGNATURES = {
     "w8_abi_version": (ctypes.c_int, []),
     "w8_last_error": (ctypes.c_char_p, []),
@@ -84,6 +91,14 @@ SIGNATURES = {
                                               ctypes.POINTER(SwigluParams), _c_void_p, _c_void_p]),
     "ln_modulate_quant": (ctypes.c_int, [_c_void_p, _i64, _i64, _c_void_p, _c_void_p, _i64, ctypes.c_float,
                                          _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
+    "add_rms_norm_quant": (ctypes.c_int, [_c_void_p, _c_void_p, _i32, _i64, _i64, _c_void_p, ctypes.c_float, _c_void_p,
+                                          _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
+    "fp8_linear_w8a8_pertoken": (ctypes.c_int, [_c_void_p, _i64, _i64, _c_void_p, _i32, ctypes.POINTER(_c_void_p),
+                                                ctypes.POINTER(_i64), ctypes.POINTER(_c_void_p),
+                                                ctypes.POINTER(_c_void_p), _c_void_p]),
+    "cross_attention": (ctypes.c_int, [ctypes.POINTER(AttentionDesc), _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                       _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p]),
+    "cross_attention_workspace": (ctypes.c_int, [ctypes.POINTER(AttentionDesc), ctypes.POINTER(_i64)]),
     "step_policy_dispatch": (ctypes.c_int, [_c_void_p, _i32, _i32, ctypes.POINTER(_i32)]),
     "w8_check_group_scales": (ctypes.c_int, [ctypes.POINTER(_c_void_p), _i32]),
     "w8_step_policy_parse": (ctypes.c_int, [ctypes.c_char_p, ctypes.POINTER(StepPolicy),
@@ -550,6 +565,172 @@ def swiglu_2in_ex_16(gate, up, limit=None, alpha=1.0, beta=0.0, out=None, stream
         raise W8Error(5, "out must have the inputs' dtype")
     prm = _swiglu_params(limit, alpha, beta)
     _check(lib().swiglu_2in_ex_16(_ptr(g), _ptr(u), dt, M, I, ctypes.byref(prm), _ptr(o), _stream(stream)))
+    return out
+
+
+def _vector(t, n, name):
+    _dense(t, name)
+    if t.dtype != torch.float32 or t.numel() != n:
+        raise W8Error(5, f"{name}: expected {n} float32 values on the device")
+    return t
+
+
+def add_rms_norm_quant(x, residual, weight, eps=1e-6, s_in=None, out=None, s_tok=None, res_out=None, h_out=None,
+                       stream=None):
+    """E4M3 codes of the root-mean-square norm of ``x + residual`` (bfloat16 or
+    float16; ``residual`` may be None), with the static scale ``s_in`` or, without
+    one, a scale for each token.  Returns ``(codes, s_tok, res_out)``: the
+    tokens' scales (None with ``s_in``) and the sum in 16 bits (None without a
+    residual).  ``res_out`` may be ``residual`` itself; ``h_out`` receives the
+    norm in 16 bits when given."""
+    x, dt = _as_16(x, "x")
+    K = x.shape[-1]
+    M = x.numel() // K if K else 0
+
+    def like_x(t, name):
+        t, d = _as_16(t, name)
+        if d != dt or t.shape != x.shape:
+            raise W8Error(5, f"{name}: expected {x.dtype} of shape {tuple(x.shape)}")
+        return t
+
+    weight, dw = _as_16(weight, "weight")
+    if dw != dt or weight.numel() != K:
+        raise W8Error(5, f"weight: expected {K} values of {x.dtype}")
+    if residual is not None:
+        like_x(residual, "residual")
+        res_out = torch.empty_like(x) if res_out is None else like_x(res_out, "res_out")
+    elif res_out is not None:
+        raise W8Error(1, "res_out without a residual")
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+    q = _as_u8(out, "out")
+    if q.shape != x.shape:
+        raise W8Error(2, f"out: shape {tuple(q.shape)} differs from x {tuple(x.shape)}")
+    if s_in is not None:
+        if s_tok is not None:
+            raise W8Error(11, "s_in and s_tok: one of them")
+        _scalar(s_in, "s_in")
+    else:
+        s_tok = torch.empty((M,), dtype=torch.float32, device=x.device) if s_tok is None else _vector(s_tok, M, "s_tok")
+    if h_out is not None:
+        like_x(h_out, "h_out")
+    _check(lib().add_rms_norm_quant(_ptr(x), _ptr(residual), dt, M, K, _ptr(weight), float(eps), _ptr(s_in),
+                                    _ptr(s_tok), _ptr(q), _ptr(h_out), _ptr(res_out), _stream(stream)))
+    return out, s_tok, res_out
+
+
+def fp8_linear_w8a8_pertoken_group(qx, s_tok, weights, channel_scales, outs=None, stream=None):
+    """G W8A8 projections of an activation whose tokens have scales of their own
+    (``s_tok``, one float32 a token), on weights with one scale for each output
+    channel."""
+    q = _as_u8(qx, "qx")
+    K = q.shape[-1]
+    M = q.numel() // K if K else 0
+    G = len(weights)
+    ws_q = [_as_u8(w, f"w[{i}]") for i, w in enumerate(weights)]
+    for i, w in enumerate(ws_q):
+        if w.dim() != 2 or w.shape[1] != K:
+            raise W8Error(2, f"w[{i}]: expected [N, {K}], got {tuple(w.shape)}")
+    if len(channel_scales) != G:
+        raise W8Error(2, f"{G} weights, {len(channel_scales)} sets of channel scales")
+    if outs is None:
+        outs = [torch.empty(*qx.shape[:-1], w.shape[0], dtype=torch.bfloat16, device=qx.device) for w in ws_q]
+    for i, (o, w) in enumerate(zip(outs, ws_q)):
+        if _as_bf16(o, f"y[{i}]").numel() != M * w.shape[0]:
+            raise W8Error(2, f"y[{i}]: expected {M} x {w.shape[0]} values")
+    arr_w = (ctypes.c_void_p * G)(*[w.data_ptr() for w in ws_q])
+    arr_n = (ctypes.c_int64 * G)(*[w.shape[0] for w in ws_q])
+    arr_s = (ctypes.c_void_p * G)(*[_vector(s, w.shape[0], f"s_ch[{i}]").data_ptr()
+                                    for i, (s, w) in enumerate(zip(channel_scales, ws_q))])
+    arr_y = (ctypes.c_void_p * G)(*[o.data_ptr() for o in outs])
+    _check(lib().fp8_linear_w8a8_pertoken(_ptr(q), M, K, _ptr(_vector(s_tok, M, "s_tok")), G, arr_w, arr_n, arr_s,
+                                          arr_y, _stream(stream)))
+    return outs
+
+
+def fp8_linear_w8a8_pertoken(qx, s_tok, w, s_ch, out=None, stream=None):
+    """W8A8 linear with a scale for each token and one for each output channel."""
+    return fp8_linear_w8a8_pertoken_group(qx, s_tok, [w], [s_ch], outs=None if out is None else [out],
+                                          stream=stream)[0]
+
+
+def _heads(t, name, dtype, device):
+    if t.dim() != 4:
+        raise W8Error(2, f"{name}: expected [samples, positions, heads, D], got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise W8Error(5, f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != device or not t.is_cuda:
+        raise W8Error(1, f"{name}: must be a CUDA tensor on q's device")
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise W8Error(4, f"{name}: the head's dimensions must be contiguous")
+    return t
+
+
+def _attention_desc(q, k, v, out, kv_mask, scale):
+    B, Lq, Hq, D = q.shape
+    return AttentionDesc(B, Lq, k.shape[1], Hq, k.shape[2], D, q.stride()[:3], k.stride()[:3], v.stride()[:3],
+                         out.stride()[:3], kv_mask.stride(0) if kv_mask is not None else 0,
+                         DTYPE_F16 if q.dtype == torch.float16 else DTYPE_BF16,
+                         D ** -0.5 if scale is None else float(scale))
+
+
+def cross_attention_workspace(q, k, v):
+    """float32 scratch for cross_attention(q, k, v, ..., ws=...) of these shapes
+    (caller-side allocation; empty when none is needed)."""
+    n = ctypes.c_int64(0)
+    _check(lib().cross_attention_workspace(ctypes.byref(_attention_desc(q, k, v, q, None, None)), ctypes.byref(n)))
+    return torch.empty((n.value,), dtype=torch.float32, device=q.device)
+
+
+def cross_attention(q, k, v, kv_len=None, kv_mask=None, scale=None, s_out=None, out=None, ws=None, stream=None):
+    """Softmax attention of ``q`` [B, Lq, Hq, D] over an encoder's ``k`` and ``v``
+    [B, Lk, Hkv, D] (bfloat16 or float16; any strides that are multiples of 8
+    with contiguous D; Hq a multiple of Hkv).  ``kv_len`` (int32 [B]) and
+    ``kv_mask`` (bool or uint8 [B, Lk], true where a key counts) limit the keys;
+    a row without keys is 0.  ``scale`` defaults to D ** -0.5.  Returns [B, Lq, Hq, D]
+    in q's dtype, or with ``s_out`` E4M3 codes."""
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise W8Error(5, f"q: expected bfloat16 or float16, got {q.dtype}")
+    _heads(q, "q", q.dtype, q.device)
+    _heads(k, "k", q.dtype, q.device)
+    _heads(v, "v", q.dtype, q.device)
+    B, Lq, Hq, D = q.shape
+    Lk = k.shape[1]
+    if k.shape != v.shape or k.shape[0] != B or k.shape[3] != D:
+        raise W8Error(2, f"q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)} do not fit together")
+    if kv_len is not None:
+        _dense(kv_len, "kv_len")
+        if kv_len.dtype != torch.int32 or kv_len.numel() != B:
+            raise W8Error(5, f"kv_len: expected {B} int32 values")
+    if kv_mask is not None:
+        if kv_mask.dtype not in (torch.bool, torch.uint8) or kv_mask.shape != (B, Lk):
+            raise W8Error(5, f"kv_mask: expected bool or uint8 [{B}, {Lk}]")
+        if not kv_mask.is_cuda:
+            raise W8Error(1, "kv_mask: must be a CUDA tensor")
+        if Lk > 1 and kv_mask.stride(1) != 1:
+            raise W8Error(4, "kv_mask: a sample's keys must be contiguous")
+    if out is None:
+        out = torch.empty((B, Lq, Hq, D), dtype=q.dtype if s_out is None else torch.uint8, device=q.device)
+    if out.shape != q.shape:
+        raise W8Error(2, f"out: shape {tuple(out.shape)} differs from q {tuple(q.shape)}")
+    if s_out is None:
+        _heads(out, "out", q.dtype, q.device)
+    else:
+        _scalar(s_out, "s_out")
+        if out.dtype not in (torch.uint8, getattr(torch, "float8_e4m3fn", None)):
+            raise W8Error(5, f"out: expected E4M3 codes (uint8 or float8_e4m3fn), got {out.dtype}")
+        _heads(out, "out", out.dtype, q.device)
+    desc = _attention_desc(q, k, v, out, kv_mask, scale)
+    if ws is None:
+        n = ctypes.c_int64(0)
+        _check(lib().cross_attention_workspace(ctypes.byref(desc), ctypes.byref(n)))
+        if n.value:
+            ws = torch.empty((n.value,), dtype=torch.float32, device=q.device)
+    elif _dense(ws, "ws").dtype != torch.float32:
+        raise W8Error(5, f"ws: expected float32, got {ws.dtype}")
+    _check(lib().cross_attention(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(kv_len), _ptr(kv_mask),
+                                 _ptr(s_out), _ptr(out), _ptr(ws), ws.numel() if ws is not None else 0,
+                                 _stream(stream)))
     return out
 
 

@@ -106,12 +106,14 @@ w8_status w8_device_check(void) {
 }
 
 w8_status w8_poll_device_error(void* stream) {
-  uint32_t err = 0, err2 = 0;
+  uint32_t err = 0, err2 = 0, err3 = 0;
   cudaError_t e = w8::gemm_read_error(static_cast<cudaStream_t>(stream), &err);
   if (e == cudaSuccess) e = w8::elementwise_read_error(static_cast<cudaStream_t>(stream), &err2);
+  if (e == cudaSuccess) e = w8::attention_read_error(static_cast<cudaStream_t>(stream), &err3);
   if (e != cudaSuccess) return fail(W8_ERR_CUDA, "reading device error word: %s", cudaGetErrorString(e));
   if (err & w8::kErrTimeout) return fail(W8_ERR_TIMEOUT, "a GEMM pipeline wait timed out");
   if (err2 & w8::kErrTimeout) return fail(W8_ERR_TIMEOUT, "a row-buffer wait of ln_modulate_quant timed out");
+  if (err3 & w8::kErrTimeout) return fail(W8_ERR_TIMEOUT, "a pipeline wait of cross_attention timed out");
   return ok();
 }
 
@@ -605,6 +607,162 @@ w8_status ln_modulate_quant(const uint16_t* x, int64_t M, int64_t K, const uint1
   return cuda_status(w8::launch_ln_modulate_quant(x, M, (int)K, shift, scale, rows_per_sample, eps, s_in, q, h,
                                                   sms, static_cast<cudaStream_t>(stream)),
                      "ln_modulate_quant launch");
+}
+
+w8_status add_rms_norm_quant(const void* x, const void* res, int32_t dtype, int64_t M, int64_t K, const void* w,
+                             float eps, const float* s_in, float* s_tok, uint8_t* q, void* h, void* res_out,
+                             void* stream) {
+  if (dtype != W8_DTYPE_BF16 && dtype != W8_DTYPE_F16)
+    return fail(W8_ERR_DTYPE, "add_rms_norm_quant: dtype %d is neither bf16 nor f16", dtype);
+  if (M < 0 || K < 8 || K > 16384 || K % 8)
+    return fail(W8_ERR_SHAPE, "add_rms_norm_quant: M=%lld K=%lld (need 8 <= K <= 16384, K %% 8 == 0)", (long long)M,
+                (long long)K);
+  if (!std::isfinite(eps) || eps < 0.0f) return fail(W8_ERR_PARAM, "add_rms_norm_quant: eps=%g", (double)eps);
+  if (M == 0) return ok();
+  if (!x || !w) return fail(W8_ERR_NULL, "add_rms_norm_quant: NULL input");
+  if (!q && !h) return fail(W8_ERR_NULL, "add_rms_norm_quant: neither q nor h given");
+  if (q && !s_in == !s_tok)
+    return fail(s_in ? W8_ERR_PARAM : W8_ERR_NULL, "add_rms_norm_quant: q needs s_in or s_tok, and not both");
+  if (!q && (s_in || s_tok)) return fail(W8_ERR_NULL, "add_rms_norm_quant: a scale without q");
+  if (res_out && !res) return fail(W8_ERR_NULL, "add_rms_norm_quant: res_out without a residual");
+  if (!aligned16(x) || !aligned16(w) || !aligned16(res) || !aligned16(q) || !aligned16(h) || !aligned16(res_out) ||
+      (reinterpret_cast<uintptr_t>(s_in) & 3u) || (reinterpret_cast<uintptr_t>(s_tok) & 3u))
+    return fail(W8_ERR_ALIGN, "add_rms_norm_quant: arrays must be 16-byte aligned");
+  int sms = 0;
+  w8_status st = device_info(&sms);
+  if (st != W8_OK) return st;
+  return cuda_status(w8::launch_add_rms_norm_quant(x, res, dtype == W8_DTYPE_F16, M, (int)K, w, eps, s_in, s_tok, q, h,
+                                                   res_out, sms, static_cast<cudaStream_t>(stream)),
+                     "add_rms_norm_quant launch");
+}
+
+w8_status fp8_linear_w8a8_pertoken(const uint8_t* qx, int64_t M, int64_t K, const float* s_tok, int32_t G,
+                                   const uint8_t* const* w, const int64_t* N, const float* const* s_ch,
+                                   uint16_t* const* y, void* stream) {
+  if (G < 1 || G > w8::kMaxGroup)
+    return fail(W8_ERR_SHAPE, "fp8_linear_w8a8_pertoken: group size %d outside 1..3", G);
+  if (!w || !N || !s_ch || !y) return fail(W8_ERR_NULL, "fp8_linear_w8a8_pertoken: NULL host array");
+  for (int g = 0; g < G; ++g) {
+    w8_status st = check_linear_common("fp8_linear_w8a8_pertoken", qx, M, K, w[g], N[g], s_ch[g], y[g]);
+    if (st != W8_OK) return st;
+    if (M > 0 && !aligned16(s_ch[g]))
+      return fail(W8_ERR_ALIGN, "fp8_linear_w8a8_pertoken: s_ch[%d] must be 16-byte aligned", g);
+  }
+  if (M == 0) return ok();
+  if (!s_tok) return fail(W8_ERR_NULL, "fp8_linear_w8a8_pertoken: NULL s_tok");
+  if (reinterpret_cast<uintptr_t>(s_tok) & 3u)
+    return fail(W8_ERR_ALIGN, "fp8_linear_w8a8_pertoken: s_tok must be 4-byte aligned");
+  int sms = 0;
+  w8_status st = device_info(&sms);
+  if (st != W8_OK) return st;
+  w8::GemmProblem p{};
+  p.M = M;
+  p.K = K;
+  p.G = G;
+  p.x = qx;
+  p.s_in = s_tok;
+  for (int g = 0; g < G; ++g) {
+    p.w[g] = w[g];
+    p.N[g] = N[g];
+    p.s_w[g] = s_ch[g];
+    p.y[g] = y[g];
+  }
+  int terr = 0;
+  cudaError_t e = w8::launch_gemm_w8a8_token(p, sms, static_cast<cudaStream_t>(stream), &terr);
+  if (terr) return fail(W8_ERR_ALIGN, "fp8_linear_w8a8_pertoken: tensor map encoding rejected the operands");
+  return cuda_status(e, "fp8_linear_w8a8_pertoken: GEMM launch");
+}
+
+// Sizes, strides and scalars of a cross attention, without its pointers.
+static w8_status check_attention(const char* fn, const w8_attention_desc* d, w8::AttnProblem* p) {
+  if (!d) return fail(W8_ERR_NULL, "%s: NULL descriptor", fn);
+  if (d->dtype != W8_DTYPE_BF16 && d->dtype != W8_DTYPE_F16)
+    return fail(W8_ERR_DTYPE, "%s: dtype %d is neither bf16 nor f16", fn, d->dtype);
+  const int64_t sizes[6] = {d->B, d->Lq, d->Lk, d->Hq, d->Hkv, d->D};
+  for (int64_t v : sizes)
+    if (v < 0 || v > INT32_MAX / 2) return fail(W8_ERR_SHAPE, "%s: size %lld", fn, (long long)v);
+  if (d->D < 8 || d->D > 128 || d->D % 8)
+    return fail(W8_ERR_SHAPE, "%s: D=%lld (need 8 <= D <= 128, D %% 8 == 0)", fn, (long long)d->D);
+  if (d->Hq < 1 || d->Hkv < 1 || d->Hq % d->Hkv || d->Hq / d->Hkv > 128)
+    return fail(W8_ERR_SHAPE, "%s: Hq=%lld Hkv=%lld (need Hq a multiple of Hkv, at most 128 times it)", fn,
+                (long long)d->Hq, (long long)d->Hkv);
+  // work items and joined rows are counted in 32 bits
+  const double rows = (double)d->B * (double)d->Hq * (double)d->Lq;
+  if (rows > (double)(1ll << 32)) return fail(W8_ERR_SHAPE, "%s: B * Hq * Lq = %.0f is above 2^32", fn, rows);
+  if (!std::isfinite(d->scale) || !(d->scale > 0.0f)) return fail(W8_ERR_PARAM, "%s: scale=%g", fn, (double)d->scale);
+  const int64_t* strides[4] = {d->q_stride, d->k_stride, d->v_stride, d->o_stride};
+  for (int t = 0; t < 4; ++t) {
+    const int64_t ext[3] = {d->B, t == 0 || t == 3 ? d->Lq : d->Lk, t == 0 || t == 3 ? d->Hq : d->Hkv};
+    for (int i = 0; i < 3; ++i) {
+      // the sample's stride of an input may be 0: one array for all samples
+      const bool shared = i == 0 && t < 3 && strides[t][i] == 0;
+      if (ext[i] > 1 && !shared && (strides[t][i] < 8 || strides[t][i] % 8 || strides[t][i] >= (1ll << 38)))
+        return fail(W8_ERR_STRIDE, "%s: stride %lld of %s (need a positive multiple of 8 elements)", fn,
+                    (long long)strides[t][i], t == 0 ? "q" : t == 1 ? "k" : t == 2 ? "v" : "out");
+    }
+  }
+  if (d->mask_stride < 0) return fail(W8_ERR_STRIDE, "%s: mask_stride=%lld", fn, (long long)d->mask_stride);
+  std::memset(p, 0, sizeof(*p));
+  p->B = (int)d->B;
+  p->Lq = (int)d->Lq;
+  p->Lk = (int)d->Lk;
+  p->Hq = (int)d->Hq;
+  p->Hkv = (int)d->Hkv;
+  p->D = (int)d->D;
+  for (int i = 0; i < 3; ++i) {
+    p->qs[i] = d->q_stride[i];
+    p->ks[i] = d->k_stride[i];
+    p->vs[i] = d->v_stride[i];
+    p->os[i] = d->o_stride[i];
+  }
+  p->f16 = d->dtype == W8_DTYPE_F16;
+  p->scale = d->scale;
+  p->mask_stride = d->mask_stride;
+  return W8_OK;
+}
+
+w8_status cross_attention_workspace(const w8_attention_desc* desc, int64_t* floats) {
+  if (!floats) return fail(W8_ERR_NULL, "cross_attention_workspace: NULL result");
+  w8::AttnProblem p;
+  w8_status st = check_attention("cross_attention_workspace", desc, &p);
+  if (st != W8_OK) return st;
+  *floats = 0;
+  if (p.B == 0 || p.Lq == 0) return ok();
+  int sms = 0;
+  if ((st = device_info(&sms)) != W8_OK) return st;
+  *floats = w8::cross_attention_ws_floats(p, sms);
+  return ok();
+}
+
+w8_status cross_attention(const w8_attention_desc* desc, const void* q, const void* k, const void* v,
+                          const int32_t* kv_len, const uint8_t* kv_mask, const float* s_out, void* out, float* ws,
+                          int64_t ws_floats, void* stream) {
+  w8::AttnProblem p;
+  w8_status st = check_attention("cross_attention", desc, &p);
+  if (st != W8_OK) return st;
+  if (p.B == 0 || p.Lq == 0) return ok();
+  if (!q || !out || (p.Lk > 0 && (!k || !v))) return fail(W8_ERR_NULL, "cross_attention: NULL pointer");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(ws) ||
+      (reinterpret_cast<uintptr_t>(kv_len) & 3u) || (reinterpret_cast<uintptr_t>(s_out) & 3u))
+    return fail(W8_ERR_ALIGN, "cross_attention: q, k, v, out and ws must be 16-byte aligned");
+  int sms = 0;
+  if ((st = device_info(&sms)) != W8_OK) return st;
+  const int64_t need = w8::cross_attention_ws_floats(p, sms);
+  if (need > 0 && !ws) return fail(W8_ERR_NULL, "cross_attention: needs a workspace of %lld floats", (long long)need);
+  if (ws_floats < need)
+    return fail(W8_ERR_SHAPE, "cross_attention: workspace of %lld floats, %lld needed", (long long)ws_floats, (long long)need);
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.kv_len = kv_len;
+  p.kv_mask = p.Lk > 0 ? kv_mask : nullptr;
+  p.s_out = s_out;
+  p.out = out;
+  p.ws = ws;
+  int terr = 0;
+  cudaError_t e = w8::launch_cross_attention(p, sms, static_cast<cudaStream_t>(stream), &terr);
+  if (terr) return fail(W8_ERR_ALIGN, "cross_attention: tensor map encoding rejected the operands");
+  return cuda_status(e, "cross_attention launch");
 }
 
 w8_status step_policy_dispatch(const w8_step_policy* policy, int32_t step, int32_t num_steps,

@@ -30,6 +30,12 @@
 //        TensorRT-LLM PR #17476, section Test Coverage) in the epilogue -- the
 //        values swiglu_2in_ex_fp8 / swiglu_2in_ex_16 would produce from the
 //        same bf16 gate and up.
+//  W8A8T (kind::f8f6f4): W8A8 with a scale for each token and one for each
+//        output channel: y = bf16( fl32( fl32( s_tok[m] * acc ) * s_ch[n] ) ).
+//        The scales are constant over k, so they stay in the epilogue, where a
+//        thread holds one token's row of the tile: its token scale is one
+//        register, the channel scales of a 64-column chunk are broadcast
+//        loads that L1 serves.
 //  W8A16 (kind::f16, gemm_a16t_kernel below): the same product with the
 //        dequantized weight formed in TMEM inside the GEMM, for calls that
 //        provide no workspace.
@@ -75,7 +81,7 @@ constexpr uint32_t kAccCols = 256;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per wait
 constexpr int kEpiBufBytes = 32 * 128;            // W8A8 staging: 32 rows x 64 bf16
 
-enum class Mode { W8A8, GLU, BF16, GLU16, GLUX, GLU16X };
+enum class Mode { W8A8, GLU, BF16, GLU16, GLUX, GLU16X, W8A8T };
 
 template <Mode MODE, int CG>
 struct Cfg {
@@ -83,6 +89,7 @@ struct Cfg {
   // in the epilogue; separate kernels, so that the plain forms keep theirs.
   static constexpr bool kEx = (MODE == Mode::GLUX || MODE == Mode::GLU16X);
   static constexpr bool kGlu = (MODE == Mode::GLU || MODE == Mode::GLU16 || kEx);
+  static constexpr bool kTok = (MODE == Mode::W8A8T);       // s_in [M], s_w[g] [N_g]
   // BF16: the W8A16 product on an already dequantized weight (bf16 x bf16,
   // kind::f16): the same tiles and pipeline (a 128-byte swizzle atom holds
   // 64 K-values instead of 128) and an unscaled epilogue.  GLU16: the gate/up pair of a 16-bit
@@ -444,7 +451,7 @@ __global__ void __launch_bounds__(Layout<MODE, CG>::kThreads, 1)
       decode_unit(args, t, BM * CG, C::kBN, m0, g, n0, width);
       float alpha = 1.0f, alpha_u = 1.0f;
       // BF16: the scale is already in the dequantized weight; y = bf16(acc).
-      if constexpr (!C::kBf16) alpha = __fmul_rn(__ldg(args.s_in), __ldg(scale_w(args, kGlu ? 0 : g)));
+      if constexpr (!C::kBf16 && !C::kTok) alpha = __fmul_rn(__ldg(args.s_in), __ldg(scale_w(args, kGlu ? 0 : g)));
       if constexpr (kGlu && !C::kBf16) alpha_u = __fmul_rn(__ldg(args.s_in), __ldg(args.s_w[1]));
       // Warp-uniform wait: the TMEM loads below are .sync.aligned.
       if (!mbar_wait_warp(tfull_bar(acc), acc_ph, abort, kWaitLimitNs)) {
@@ -454,6 +461,7 @@ __global__ void __launch_bounds__(Layout<MODE, CG>::kThreads, 1)
       tc_fence_after();
       const int row0 = m0 + (int)rank * BM + wq * 32;
       const int ng = args.N[g];
+      if constexpr (C::kTok) alpha = __ldg(args.s_in + min(row0 + lane, args.M - 1));
       const uint32_t tbase = tmem_base + ((uint32_t)(wq * 32) << 16) + (uint32_t)(acc * kAccCols);
       if constexpr (!kGlu) {
         const int chunks = width / 64;
@@ -472,14 +480,30 @@ __global__ void __launch_bounds__(Layout<MODE, CG>::kThreads, 1)
             }
           }
           uint32_t packed[32];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            packed[j] = cvt_bf16x2(__fmul_rn(__uint_as_float(r0[2 * j]), alpha),
-                                   __fmul_rn(__uint_as_float(r0[2 * j + 1]), alpha));
-            packed[16 + j] = cvt_bf16x2(__fmul_rn(__uint_as_float(r1[2 * j]), alpha),
-                                        __fmul_rn(__uint_as_float(r1[2 * j + 1]), alpha));
-          }
           const int col0 = n0 + c * 64;
+          if constexpr (C::kTok) {
+            // N_g is a multiple of 16: a group of four is in range or past the end,
+            // where the last one's scales stand in for columns that are not stored
+            const float* ch = scale_w(args, g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float4 a4 = __ldg(reinterpret_cast<const float4*>(ch + min(col0 + 4 * j, ng - 4)));
+              const float4 b4 = __ldg(reinterpret_cast<const float4*>(ch + min(col0 + 32 + 4 * j, ng - 4)));
+              auto val = [&](uint32_t acc, float s) { return __fmul_rn(__fmul_rn(__uint_as_float(acc), alpha), s); };
+              packed[2 * j] = cvt_bf16x2(val(r0[4 * j], a4.x), val(r0[4 * j + 1], a4.y));
+              packed[2 * j + 1] = cvt_bf16x2(val(r0[4 * j + 2], a4.z), val(r0[4 * j + 3], a4.w));
+              packed[16 + 2 * j] = cvt_bf16x2(val(r1[4 * j], b4.x), val(r1[4 * j + 1], b4.y));
+              packed[17 + 2 * j] = cvt_bf16x2(val(r1[4 * j + 2], b4.z), val(r1[4 * j + 3], b4.w));
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              packed[j] = cvt_bf16x2(__fmul_rn(__uint_as_float(r0[2 * j]), alpha),
+                                     __fmul_rn(__uint_as_float(r0[2 * j + 1]), alpha));
+              packed[16 + j] = cvt_bf16x2(__fmul_rn(__uint_as_float(r1[2 * j]), alpha),
+                                          __fmul_rn(__uint_as_float(r1[2 * j + 1]), alpha));
+            }
+          }
           if (col0 >= ng || row0 >= args.M) continue;  // nothing of this chunk is in range
           // The store issued two chunks ago from this buffer must have read it.
           if (lane == 0) tma_store_wait_read<1>();
@@ -1127,6 +1151,11 @@ __global__ void selftest_timeout_kernel(uint64_t limit_ns) {
 cudaError_t launch_gemm_w8a8(const GemmProblem& p, int sms, cudaStream_t st, int* tmap_err) {
   return use_pair(p) ? launch<Mode::W8A8, 2>(p, sms, st, tmap_err)
                      : launch<Mode::W8A8, 1>(p, sms, st, tmap_err);
+}
+
+cudaError_t launch_gemm_w8a8_token(const GemmProblem& p, int sms, cudaStream_t st, int* tmap_err) {
+  return use_pair(p) ? launch<Mode::W8A8T, 2>(p, sms, st, tmap_err)
+                     : launch<Mode::W8A8T, 1>(p, sms, st, tmap_err);
 }
 
 cudaError_t launch_gemm_bf16(const GemmProblem& p, int sms, cudaStream_t st, int* tmap_err) {

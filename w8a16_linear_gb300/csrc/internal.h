@@ -37,6 +37,14 @@ cudaError_t launch_ln_modulate_quant(const uint16_t* x, int64_t M, int K, const 
                                      const uint16_t* scale, int64_t rows_per_sample, float eps,
                                      const float* s_in, uint8_t* q, uint16_t* h, int sms, cudaStream_t st);
 
+// ---- residual + root-mean-square norm + quantization (rmsnorm.cu)
+// One row of K values at a time (8 <= K <= 16384, K % 8 == 0); res, h and
+// res_out may be null, q too if h is given; the scale of q is *s_in, or each
+// row's own, written to s_tok.
+cudaError_t launch_add_rms_norm_quant(const void* x, const void* res, bool f16, int64_t M, int K, const void* w,
+                                      float eps, const float* s_in, float* s_tok, uint8_t* q, void* h, void* res_out,
+                                      int sms, cudaStream_t st);
+
 struct SwigluExArgs {            // validated by the caller
   bool has_limit;
   float limit, alpha, beta;
@@ -64,6 +72,8 @@ struct GemmProblem {
 // Returns cudaSuccess or the CUDA error; *tmap_err is set non-zero when a
 // tensor map could not be encoded.
 cudaError_t launch_gemm_w8a8(const GemmProblem& p, int sms, cudaStream_t st, int* tmap_err);
+// W8A8 with a scale for each token (s_in: [M]) and output channel (s_w[g]: [N_g], 16-byte aligned).
+cudaError_t launch_gemm_w8a8_token(const GemmProblem& p, int sms, cudaStream_t st, int* tmap_err);
 cudaError_t launch_gemm_w8a16(const GemmProblem& p, int sms, cudaStream_t st, int* tmap_err);
 // Gate/up W8A8 GEMMs with the SwiGLU-to-E4M3 epilogue: x E4M3 [M,K], w[0] gate
 // and w[1] up [I,K] with s_w[0], s_w[1]; N[0] = I; y[0] E4M3 [M,I]; s_out.
@@ -74,6 +84,25 @@ cudaError_t launch_gemm_bf16(const GemmProblem& p, int sms, cudaStream_t st, int
 // and w[1] (up), [I, K] each, with h = SwiGLU written as bf16 into y[0] [M, I].
 cudaError_t launch_gemm_glu16(const GemmProblem& p, int sms, cudaStream_t st, int* tmap_err);
 cudaError_t launch_gemm_glu(const GemmProblem& p, int sms, cudaStream_t st, int* tmap_err);
+
+// ---- cross attention (attention.cu)
+struct AttnProblem {             // validated by the caller
+  int B, Lq, Lk, Hq, Hkv, D;
+  int64_t qs[3], ks[3], vs[3], os[3];   // element strides: sample, position, head
+  bool f16;
+  float scale;
+  const void *q, *k, *v;
+  const int32_t* kv_len;         // [B], or null
+  const uint8_t* kv_mask;        // [B, Lk], rows mask_stride apart, or null
+  int64_t mask_stride;
+  const float* s_out;            // not null: E4M3 output
+  void* out;
+  float* ws;                     // cross_attention_ws_floats() floats
+};
+int64_t cross_attention_ws_floats(const AttnProblem& p, int sms);
+cudaError_t launch_cross_attention(const AttnProblem& p, int sms, cudaStream_t st, int* tmap_err);
+// Reads and clears the attention kernels' device error word (synchronises `st`).
+cudaError_t attention_read_error(cudaStream_t st, uint32_t* err);
 
 // Launches a one-thread kernel whose mbarrier wait times out (0.2 s).
 cudaError_t launch_selftest_timeout(cudaStream_t st);
