@@ -26,8 +26,8 @@
 // results that a second kernel joins.
 //
 // Roles: warps 0-3 and 4-7 softmax of slot 0 / 1 (a thread per row, so row
-// maxima and sums need no shuffles), 8-11 epilogue, 12 MMA issue, 13 TMA
-// loads, 14 clearing of masked V rows (0 * NaN would spoil the products).
+// maxima and sums need no shuffles), 8-11 epilogue, 12 and 15 MMA issue of slot 0 / 1,
+// 13 TMA loads, 14 clearing of masked V rows (0 * NaN would spoil the products).
 //
 // Roundings below 32 bits: P to the inputs' 16-bit type (the tensor core takes
 // no wider operand beside 16-bit V; its sum l is taken before the rounding,
@@ -66,11 +66,12 @@ struct Cfg {
   static constexpr int kStages = DP == 128 ? 4 : 6;
   static constexpr int kQ = 0;
   static constexpr int kRing = kQ + 2 * kTile;
-  static constexpr int kSum = kRing + kStages * kTile;   // l[2][128], m[2][128]
+  static constexpr int kOut = kRing + kStages * kTile;   // 32 rows of 128 bytes for each epilogue warp
+  static constexpr int kSum = kOut + 4 * 32 * 128;       // l[2][128], m[2][128]
   static constexpr int kBar = kSum + 4 * kRows * 4;
   // full[S], empty[S], clean[S], q_full[2], q_empty[2], s_full[2], p_full[2],
-  // o_full[2], l_full[2], o_free[2], drain
-  static constexpr int kNumBars = 3 * kStages + 15;
+  // o_full[2], l_full[2], o_free[2], p_half[2], drain[2]
+  static constexpr int kNumBars = 3 * kStages + 18;
   static constexpr int kTmemSlot = kBar + kNumBars * 8;
   static constexpr int kAbort = kTmemSlot + 4;
   static constexpr int kAlloc = kAbort + 4 + 1024;       // slack for 1024-byte alignment
@@ -120,16 +121,38 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
       : "memory");
+}
+
+// Waits for this thread's TMEM loads; naming the registers keeps their uses
+// behind the wait while other loads are still under way.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+// mbar_wait_warp with every lane asking first: no broadcast on the way of a
+// phase that is complete or about to be.
+__device__ __forceinline__ bool mbar_wait_lanes(uint32_t bar, uint32_t parity, volatile int* abort) {
+  bool done = false;
+#pragma unroll 1
+  for (int k = 0; k < 64 && !done; ++k) done = mbar_try_wait(bar, parity);
+  done = __all_sync(0xFFFFFFFFu, done);
+  if (!done) done = mbar_wait_warp(bar, parity, abort, kWaitLimitNs);
+  __syncwarp();   // the TMEM instructions that follow want the warp together
+  return done;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -160,6 +183,26 @@ struct Item {
   __device__ __forceinline__ int n() const { return t1 - t0; }
 };
 
+// kLens / kMask: which of the two limits a kernel has.  Each form is compiled
+// by itself, without tests of optional pointers, and what limits the keys is read
+// by plain volatile loads: an earlier kernel may have written it just before.
+__device__ __forceinline__ int load_len(const int32_t* p) {
+  int v;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float load_scale(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ bool load_mask(const uint8_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v != 0;
+}
+
+template <bool kLens>
 __device__ __forceinline__ Item decode(const AttnArgs& a, int it) {
   Item x;
   x.blk = it % a.blocks;
@@ -169,7 +212,7 @@ __device__ __forceinline__ Item decode(const AttnArgs& a, int it) {
   x.hk = it % a.Hkv;
   x.b = it / a.Hkv;
   x.len = a.Lk;
-  if (a.kv_len) x.len = min(max(__ldg(a.kv_len + x.b), 0), a.Lk);
+  if constexpr (kLens) x.len = min(max(load_len(a.kv_len + x.b), 0), a.Lk);
   const int tiles = (x.len + kKeys - 1) / kKeys;
   x.t0 = (int)((int64_t)tiles * x.split / a.splits);
   x.t1 = (int)((int64_t)tiles * (x.split + 1) / a.splits);
@@ -183,11 +226,12 @@ __device__ __forceinline__ void record_timeout(volatile int* abort) {
 
 // kShared: both slots work on the same key tiles (256 query rows); otherwise
 // they take the even and odd tiles of the same 128 rows.
-template <int DP, bool kF16, bool kMask, bool kShared>
+template <int DP, bool kF16, bool kLens, bool kMask, bool kShared>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_attention_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ AttnArgs a) {
   using C = Cfg<DP>;
   constexpr int S = C::kStages;
+  constexpr bool kClean = kLens || kMask;
   constexpr uint32_t kIdescS = make_idesc(kF16 ? 0 : 1, kF16 ? 0 : 1, kRows, kKeys);
   constexpr uint32_t kIdescO = make_idesc(kF16 ? 0 : 1, kF16 ? 0 : 1, kRows, DP) | (1u << 16);  // B is MN-major
 
@@ -206,7 +250,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto o_full = [&](int i) { return bar(3 * S + 8 + i); };
   auto l_full = [&](int i) { return bar(3 * S + 10 + i); };
   auto o_free = [&](int i) { return bar(3 * S + 12 + i); };
-  const uint32_t drain_bar = bar(3 * S + 14);
+  auto p_half = [&](int i) { return bar(3 * S + 14 + i); };
+  auto drain_bar = [&](int i) { return bar(3 * S + 16 + i); };
   volatile int* abort = reinterpret_cast<volatile int*>(smem + C::kAbort);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kTmemSlot);
   float* sum_l = reinterpret_cast<float*>(smem + C::kSum);
@@ -218,19 +263,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), 1);
+      mbar_init(empty_bar(s), kShared ? 2 : 1);   // the slots that read the tile
       mbar_init(clean_bar(s), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full(i), 1);
-      mbar_init(q_empty(i), 1);
+      mbar_init(q_empty(i), kShared ? 1 : 2);     // the slots that read Q
       mbar_init(s_full(i), 1);
+      mbar_init(p_half(i), 4);
       mbar_init(p_full(i), 4);
       mbar_init(o_full(i), 1);
       mbar_init(l_full(i), 4);
       mbar_init(o_free(i), 4);
     }
-    mbar_init(drain_bar, 1);
+    mbar_init(drain_bar(0), 1);
+    mbar_init(drain_bar(1), 1);
     *abort = 0;
     fence_mbar_init();
     prefetch_tensormap(&maps.q);
@@ -286,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
-        const Item x = decode(a, it);
+        const Item x = decode<kLens>(a, it);
         if (x.n() == 0) continue;
         bool first = true;
         ok = load_q(x, 0);
@@ -319,148 +366,88 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (qcount[i] > 0 && !mbar_wait(q_full(i), (qcount[i] - 1) & 1, &never, kWaitLimitNs))
           atomicOr(&g_attn_err, kErrTimeout);
     }
-  } else if (warp == 12) {
+  } else if (warp == 12 || warp == 15) {
     // ---------------------------------------------------------------- MMA issue
+    // One thread for each slot: issuing an MMA takes about as long as the
+    // tensor core takes to run it, so one thread for both left it idle half of
+    // the time.  A slot's MMAs run in the order of their issue: the scores
+    // of tile j + 1 may be written over P of tile j, and when they are complete
+    // so is the product of tile j.
     if (lane == 0) {
-      int st = 0;
-      uint32_t ph = 0;
-      uint32_t qcount = 0;                       // items whose Q has been waited for
-      uint32_t pcount[2] = {0, 0};               // tiles of each slot whose P has been waited for
-      uint32_t ocount[2] = {0, 0};               // items of each slot whose O has been started
+      const int i = warp == 12 ? 0 : 1;
+      uint32_t base = 0;                         // entries of the ring before this item
+      uint32_t qcount = 0, pcount = 0, icount = 0;
       bool ok = true;
-      // Waits for the stage at the ring's head, and takes it.  With masks the
+      // Waits for entry e of the ring; returns its stage.  With limits the
       // cleaning warp passes every stage first, K's too: a stage can then not
       // be refilled before that warp has seen it.
-      auto take = [&](int& s) {
-        s = st;
-        ok = ok && mbar_wait(kMask ? clean_bar(st) : full_bar(st), ph, abort, kWaitLimitNs);
-        if (++st == S) {
-          st = 0;
-          ph ^= 1;
-        }
+      auto take = [&](uint32_t e) {
+        const int st = (int)(e % S);
+        ok = ok && mbar_wait(kClean ? clean_bar(st) : full_bar(st), (e / S) & 1, abort, kWaitLimitNs);
         tc_fence_after();
+        return st;
       };
-      auto qk = [&](int i, int s) {
-        const uint32_t qa = sbase + C::kQ + (kShared ? i : 0) * C::kTile, ka = sbase + C::kRing + s * C::kTile;
+      for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
+        const int n = decode<kLens>(a, it).n();
+        if (n == 0) continue;
+        if (slot_tiles(n, i) > 0) {
+          ok = mbar_wait(q_full(kShared ? i : 0), qcount & 1, abort, kWaitLimitNs);
+          tc_fence_after();
+        }
+        for (int j = kShared ? 0 : i; ok && j < n; j += kShared ? 1 : 2) {
+          const bool first = j == (kShared ? 0 : i), last = j + (kShared ? 1 : 2) >= n;
+          // where `walk` puts K and V of tile j
+          const uint32_t ek = kShared ? 2 * j : j < 2 ? j : 2 * j - 1, ev = kShared ? 2 * j + 1 : j == n - 1 ? 2 * n - 1 : 2 * j + 2;
+          int st = take(base + ek);
+          if (!ok) break;
+          const uint64_t qd = sw128_kmajor_desc(sbase + C::kQ + (kShared ? i : 0) * C::kTile);
+          const uint64_t kd = sw128_kmajor_desc(sbase + C::kRing + st * C::kTile);
 #pragma unroll
-        for (int k = 0; k < DP / 16; ++k)
-          mma_f16(s_col(i), sw128_kmajor_desc(qa + (k >> 2) * kAtom + 32 * (k & 3)),
-                  sw128_kmajor_desc(ka + (k >> 2) * kAtom + 32 * (k & 3)), kIdescS, k != 0);
-        mma_commit(s_full(i));
-      };
-      auto pv = [&](int i, int s, bool first) {
-        const uint32_t va = sbase + C::kRing + s * C::kTile;
-        ok = ok && mbar_wait(p_full(i), pcount[i] & 1, abort, kWaitLimitNs);
-        ++pcount[i];
-        if (first) {   // the epilogue has read the accumulator's previous item
-          ok = ok && mbar_wait(o_free(i), (ocount[i] & 1) ^ 1, abort, kWaitLimitNs);
-          ++ocount[i];
-        }
-        if (!ok) return;
-        tc_fence_after();
+          for (int k = 0; k < DP / 16; ++k) {   // descriptors count in 16 bytes
+            const uint64_t at = ((k >> 2) * kAtom + 32 * (k & 3)) >> 4;
+            mma_f16(s_col(i), qd + at, kd + at, kIdescS, k != 0);
+          }
+          mma_commit(s_full(i));
+          mma_commit(empty_bar(st));
+          if (last) mma_commit(q_empty(kShared ? i : 0));
+
+          st = take(base + ev);
+          if (first) ok = ok && mbar_wait(o_free(i), (icount++ & 1) ^ 1, abort, kWaitLimitNs);   // the epilogue has read O_i
+          const uint64_t vd = sw128_mnmajor_desc(sbase + C::kRing + st * C::kTile);
 #pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
-          mma_f16_tmem_a(o_col(i), s_col(i) + 8 * k, sw128_mnmajor_desc(va + 2048 * k), kIdescO, !first || k != 0);
-      };
-      auto wait_q = [&](int i, uint32_t count) {
-        ok = ok && mbar_wait(q_full(i), count & 1, abort, kWaitLimitNs);
-        tc_fence_after();
-      };
-      auto next_item = [&](int it) {             // the next item with any keys, or items
-        for (it += gridDim.x; it < a.items; it += gridDim.x)
-          if (decode(a, it).n() > 0) break;
-        return min(it, a.items);
-      };
-      int it = next_item((int)blockIdx.x - (int)gridDim.x);
-      if constexpr (kShared) {
-        // The scores of the next tile -- of the next item after an item's last
-        // tile -- are issued behind each slot's product with V, so that the
-        // tensor core has the other slot's work while a softmax runs.
-        bool have = false;
-        int s = 0;
-        while (ok && it < a.items) {
-          const int n = decode(a, it).n();
-          const int nx = next_item(it);
-          const int n_next = nx < a.items ? decode(a, nx).n() : 0;
-          if (!have) {
-            take(s);
-            for (int i = 0; i < 2 && ok; ++i) {
-              wait_q(i, qcount);
-              if (!ok) break;
-              qk(i, s);
-              if (n == 1) mma_commit(q_empty(i));
-            }
-            mma_commit(empty_bar(s));
+          for (int h = 0; h < 2; ++h) {          // 64 keys at a time, as the softmax hands them over
+            ok = ok && mbar_wait(h ? p_full(i) : p_half(i), pcount & 1, abort, kWaitLimitNs);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = h * kKeys / 32; k < (h + 1) * kKeys / 32; ++k)
+              mma_f16_tmem_a(o_col(i), s_col(i) + 8 * k, vd + (2048 * k >> 4), kIdescO, !first || k != 0);
           }
-          for (int j = 0; j < n && ok; ++j) {
-            const bool more = j + 1 < n;
-            int vs, ks = 0;
-            take(vs);
-            for (int i = 0; i < 2 && ok; ++i) {
-              pv(i, vs, j == 0);
-              if (!ok) break;
-              if (i == 1) mma_commit(empty_bar(vs));
-              if (!more) mma_commit(o_full(i));
-              if (more || n_next > 0) {
-                if (i == 0) take(ks);
-                if (!more) wait_q(i, qcount + 1);
-                if (!ok) break;
-                qk(i, ks);
-                if (more ? j + 2 == n : n_next == 1) mma_commit(q_empty(i));
-                if (i == 1) mma_commit(empty_bar(ks));
-              }
-            }
-          }
-          ++qcount;
-          have = n_next > 0;
-          it = nx;
+          ++pcount;
+          if (!ok) break;
+          mma_commit(empty_bar(st));
+          if (last) mma_commit(o_full(i));
         }
-      } else {
-        while (ok && it < a.items) {
-          const int n = decode(a, it).n();
-          int s = 0;
-          wait_q(0, qcount);
-          ++qcount;
-          for (int j = 0; j < 2 && j < n && ok; ++j) {
-            take(s);
-            if (!ok) break;
-            qk(j, s);
-            mma_commit(empty_bar(s));
-          }
-          for (int j = 0; j < n && ok; ++j) {
-            take(s);
-            if (!ok) break;
-            pv(j & 1, s, j < 2);
-            if (!ok) break;
-            mma_commit(empty_bar(s));
-            if (j + 2 >= n) mma_commit(o_full(j & 1));
-            if (j + 2 < n) {
-              take(s);
-              if (!ok) break;
-              qk(j & 1, s);
-              mma_commit(empty_bar(s));
-            }
-          }
-          mma_commit(q_empty(0));
-          it = next_item(it);
-        }
+        if (!kShared && i == 1 && n == 1) mma_commit(q_empty(0));   // no tile of this item: its word on Q all the same
+        base += 2 * (uint32_t)n;
+        ++qcount;
       }
       if (!ok) record_timeout(abort);
       // All MMAs complete before TMEM is freed.
-      mma_commit(drain_bar);
+      mma_commit(drain_bar(i));
       volatile int never = 0;
-      if (!mbar_wait(drain_bar, 0, &never, kWaitLimitNs)) atomicOr(&g_attn_err, kErrTimeout);
+      if (!mbar_wait(drain_bar(i), 0, &never, kWaitLimitNs)) atomicOr(&g_attn_err, kErrTimeout);
     }
   } else if (warp == 14) {
     // ---------------------------------------------------------------- masked V rows
     // Keys that do not count have P = 0, but their V may be anything, NaN and
     // infinities included: those rows are cleared before the product.
-    if constexpr (kMask) {
+    if constexpr (kClean) {
       int st = 0;
       uint32_t ph = 0;
       bool ok = true;
       for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
-        const Item x = decode(a, it);
+        const Item x = decode<kLens>(a, it);
         ok = walk(x, [&](bool is_v, int tile) {
           if (!mbar_wait_warp(full_bar(st), ph, abort, kWaitLimitNs)) return false;
           if (is_v) {
@@ -469,7 +456,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int r = lane; r < kKeys; r += 32) {
               const int j = tile * kKeys + r;
               // beyond the array the copy has written zeros
-              if (j >= a.Lk || (j < x.len && (!a.kv_mask || a.kv_mask[x.b * a.mask_stride + j]))) continue;
+              if (j >= a.Lk) continue;
+              bool on = j < x.len;
+              if constexpr (kMask)
+                if (on) on = load_mask(a.kv_mask + x.b * a.mask_stride + j);
+              if (on) continue;
               wrote = true;
               for (int at = 0; at < C::kAtoms; ++at)
 #pragma unroll
@@ -497,45 +488,53 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t scount = 0, icount = 0;
     bool ok = true;
     for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
-      const Item x = decode(a, it);
+      const Item x = decode<kLens>(a, it);
       const int n = slot_tiles(x.n(), i);
       if (n == 0) continue;
       float m = -INFINITY, l = 0.0f;             // m in powers of two: scaled scores
       for (int j = 0; j < n; ++j) {
         const int key0 = (x.t0 + (kShared ? j : 2 * j + i)) * kKeys;
         // Bit lane of word e: key 4 lane + e of the tile counts.
-        bool masked = false;
-        uint32_t word[4] = {~0u, ~0u, ~0u, ~0u};
-        if (kMask || key0 + kKeys > x.len) {
-          masked = true;
+        const bool masked = kMask || key0 + kKeys > x.len;
+        uint32_t word[4];
+        if (masked) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int key = key0 + 4 * lane + e;
             bool on = key < x.len;
-            if (kMask && a.kv_mask && on) on = a.kv_mask[x.b * a.mask_stride + key] != 0;
+            if constexpr (kMask)
+              if (on) on = load_mask(a.kv_mask + x.b * a.mask_stride + key);
             word[e] = __ballot_sync(0xFFFFFFFFu, on);
           }
+          __syncwarp();   // lanes past the last key took another path
         }
-        if (!mbar_wait_warp(s_full(i), scount & 1, abort, kWaitLimitNs)) {
+        if (!mbar_wait_lanes(s_full(i), scount & 1, abort)) {
           ok = false;
           break;
         }
         ++scount;
         tc_fence_after();
-        float top = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(s_col(i) + quad + c * 32, r);
-          tmem_ld_wait();
+        // Two passes over the row's scores in TMEM, 32 columns at a time with the
+        // next 32 on their way: 128 registers a thread hold no whole row.
+        uint32_t r[2][32];
+        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        tmem_ld_32x32b_x32(s_col(i) + quad, r[0]);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float v = __uint_as_float(r[e]);
-            if (masked && !((word[e & 3] >> (8 * c + (e >> 2))) & 1)) v = -INFINITY;
-            top = fmaxf(top, v);
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld_wait_for(r[c & 1]);
+          tmem_ld_32x32b_x32(s_col(i) + quad + (c + 1) % 4 * 32, r[(c + 1) & 1]);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float v0 = __uint_as_float(r[c & 1][e]), v1 = __uint_as_float(r[c & 1][e + 1]);
+            if (masked) {
+              if (!((word[e & 3] >> (8 * c + (e >> 2))) & 1)) v0 = -INFINITY;
+              if (!((word[(e + 1) & 3] >> (8 * c + (e >> 2))) & 1)) v1 = -INFINITY;
+            }
+            tops[(e >> 1) & 3] = fmaxf(fmaxf(tops[(e >> 1) & 3], v0), v1);
           }
         }
-        top *= a.scale_log2;
+        tmem_ld_wait_for(r[0]);   // columns 0 - 31 again
+        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * a.scale_log2;
         // Scores of slot i are complete, so its product with the previous tile
         // is too (issued before them): O_i may be rescaled here.
         const bool grow = top > m + kLazyMax || (m == -INFINITY && top > m);
@@ -545,45 +544,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float f = m_new == -INFINITY ? 1.0f : ex2(m - m_new);
             l *= f;
 #pragma unroll 1
-            for (int c = 0; c < DP / 32; ++c) {
-              uint32_t r[32];
-              tmem_ld_32x32b_x32(o_col(i) + quad + c * 32, r);
+            for (int c = 0; c < DP / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld_32x32b_x16(o_col(i) + quad + c * 16, o);
               tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-              tmem_st_32x32b_x32(o_col(i) + quad + c * 32, r);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st_32x32b_x16(o_col(i) + quad + c * 16, o);
             }
           }
           m = m_new;
         }
-        const float ms = m == -INFINITY ? 0.0f : m;
-        float l0 = 0.0f, l1 = 0.0f;
-#pragma unroll 1
+        const F2 scale = splat(a.scale_log2), minus_m = splat(m == -INFINITY ? 0.0f : -m);
+        F2 sums[2] = {splat(0.0f), splat(0.0f)};
+#pragma unroll
         for (int c = 0; c < 4; ++c) {
-          uint32_t r[32], p[16];
-          tmem_ld_32x32b_x32(s_col(i) + quad + c * 32, r);
-          tmem_ld_wait();
+          uint32_t p[16];
+          if (c > 0) tmem_ld_wait_for(r[c & 1]);
+          if (c < 3) tmem_ld_32x32b_x32(s_col(i) + quad + (c + 1) * 32, r[(c + 1) & 1]);
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            float p0 = ex2(fmaf(__uint_as_float(r[e]), a.scale_log2, -ms));
-            float p1 = ex2(fmaf(__uint_as_float(r[e + 1]), a.scale_log2, -ms));
+            const F2 t = fma2(F2{__uint_as_float(r[c & 1][e]), __uint_as_float(r[c & 1][e + 1])}, scale, minus_m);
+            F2 w = F2{ex2(t.x), ex2(t.y)};
             if (masked) {
-              if (!((word[e & 3] >> (8 * c + (e >> 2))) & 1)) p0 = 0.0f;
-              if (!((word[(e + 1) & 3] >> (8 * c + (e >> 2))) & 1)) p1 = 0.0f;
+              if (!((word[e & 3] >> (8 * c + (e >> 2))) & 1)) w.x = 0.0f;
+              if (!((word[(e + 1) & 3] >> (8 * c + (e >> 2))) & 1)) w.y = 0.0f;
             }
-            l0 += p0;
-            l1 += p1;
-            p[e >> 1] = cvt16x2(kF16, p0, p1);
+            sums[(e >> 1) & 1] = add2(sums[(e >> 1) & 1], w);
+            p[e >> 1] = cvt16x2(kF16, w.x, w.y);
           }
-          // 32 scores leave 16 columns of P over the first half of S_i; chunk
-          // c's are read before: columns 16 c .. 16 c + 15 lie at or below 32 c
+          // P takes the first half of S_i's columns: chunk c's 16 lie at or below
+          // the first column of the scores that are still to be read
           tmem_st_32x32b_x16(s_col(i) + quad + c * 16, p);
+          if (c & 1) {   // 64 keys of P: the product with V may start on them
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(c == 1 ? p_half(i) : p_full(i));
+          }
         }
-        l += l0 + l1;
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(i));
+        sums[0] = add2(sums[0], sums[1]);
+        l += sums[0].x + sums[0].y;
       }
       if (!ok) break;
       // the epilogue has read the previous item's sums
@@ -604,37 +605,71 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t quad = (uint32_t)((warp & 3) * 32) << 16;
     const int pos = row / a.G, g = row - pos * a.G;
     float inv_s = 1.0f;
-    if (a.s_out) inv_s = __frcp_rn(__ldg(a.s_out));
+    if (a.s_out) inv_s = __frcp_rn(load_scale(a.s_out));
     uint32_t icount[2] = {0, 0};
     bool ok = true;
 
-    // 32 columns of this thread's row, scaled, to the output or the partials.
-    auto put = [&](const Item& x, int l, int c, const float (&v)[32]) {
-      if (pos >= a.rows_l || l >= a.Lq) return;
-      const int d0 = 32 * c;
-      if (a.splits > 1) {
-        const int64_t at = (((int64_t)x.split * a.B + x.b) * a.Hkv + x.hk) * ((int64_t)a.Lq * a.G) + (int64_t)l * a.G + g;
-        float4* dst = reinterpret_cast<float4*>(a.part + at * DP + d0);
+    // A warp's 32 rows leave through 4 KB of shared memory, 128 bytes of each at
+    // a time (32 columns of binary32 partials, 64 of 16 bits, 128 codes), so
+    // that whole sectors of a row are written together: 16-byte stores from the
+    // rows' own threads took 1.2 times as long over a short key side.
+    uint8_t* stage = smem + C::kOut + (warp & 3) * 32 * 128;
+    const int kind = a.splits > 1 ? 2 : a.s_out ? 0 : 1;             // log2 of a value's bytes
+    auto out_row = [&](const Item& x, int l) -> int64_t {            // element offset, or -1
+      if (pos >= a.rows_l || l >= a.Lq) return -1;
+      if (kind == 2)
+        return ((((int64_t)x.split * a.B + x.b) * a.Hkv + x.hk) * ((int64_t)a.Lq * a.G) + (int64_t)l * a.G + g) * DP;
+      return x.b * a.o_b + l * a.o_l + (int64_t)(x.hk * a.G + g) * a.o_h;
+    };
+    uint8_t* const out_base = static_cast<uint8_t*>(kind == 2 ? static_cast<void*>(a.part) : a.out);
+    // 16 columns (chunk c) of this thread's row; the store of the span follows
+    // when its 128 bytes (or the row) are complete.
+    auto put = [&](int64_t off, int c, const float (&v)[16]) {
+      const int span = 128 >> kind;                                  // columns of 128 bytes
+      const int u0 = (16 * c % span << kind) >> 4;                   // first 16-byte unit of the chunk
+      uint8_t* mine = stage + lane * 128;
+      auto unit = [&](int u, uint4 w) { *reinterpret_cast<uint4*>(mine + ((u ^ (lane & 7)) << 4)) = w; };
+      if (kind == 0) {
+        uint32_t w[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-        return;
+        for (int k = 0; k < 8; ++k) w[k] = cvt_e4m3x2(v[2 * k] * inv_s, v[2 * k + 1] * inv_s);
+        unit(u0, make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16)));
+      } else if (kind == 1) {
+        uint32_t w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = cvt16x2(kF16, v[2 * k], v[2 * k + 1]);
+        unit(u0, make_uint4(w[0], w[1], w[2], w[3]));
+        unit(u0 + 1, make_uint4(w[4], w[5], w[6], w[7]));
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          unit(u0 + k, make_uint4(__float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]), __float_as_uint(v[4 * k + 2]),
+                                  __float_as_uint(v[4 * k + 3])));
       }
-      const int64_t off = x.b * a.o_b + l * a.o_l + (int64_t)(x.hk * a.G + g) * a.o_h + d0;
-#pragma unroll
-      for (int e = 0; e < 32; e += 8) {
-        if (d0 + e >= a.D) break;
-        if (a.s_out) {
-          uint32_t w[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = cvt_e4m3x2(v[e + 2 * k] * inv_s, v[e + 2 * k + 1] * inv_s);
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + off + e) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-        } else {
-          uint32_t w[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = cvt16x2(kF16, v[e + 2 * k], v[e + 2 * k + 1]);
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + off + e) = make_uint4(w[0], w[1], w[2], w[3]);
+      const int end = 16 * (c + 1);
+      if (end % span != 0 && end != DP) return;
+      __syncwarp();
+      const int d0 = (end - 1) / span * span;
+      const int width = kind == 2 ? DP : a.D;                        // partial rows are DP wide
+      if (kind == 0) {                                               // a row of codes is 8-byte aligned
+#pragma unroll 4
+        for (int k = 0; k < 16; ++k) {
+          const int row = 2 * k + (lane >> 4), u = lane & 15;
+          const int64_t o = __shfl_sync(0xFFFFFFFFu, off, row);
+          const uint2 w = *reinterpret_cast<const uint2*>(stage + row * 128 + ((u >> 1 ^ (row & 7)) << 4) + 8 * (u & 1));
+          if (o >= 0 && d0 + 8 * u < width) *reinterpret_cast<uint2*>(out_base + o + d0 + 8 * u) = w;
+        }
+      } else {
+#pragma unroll 4
+        for (int k = 0; k < 8; ++k) {
+          const int row = 4 * k + (lane >> 3), u = lane & 7;
+          const int64_t o = __shfl_sync(0xFFFFFFFFu, off, row);
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + row * 128 + ((u ^ (row & 7)) << 4));
+          if (o >= 0 && d0 + (16 >> kind) * u < width)
+            *reinterpret_cast<uint4*>(out_base + ((o + d0) << kind) + 16 * u) = w;
         }
       }
+      __syncwarp();
     };
     auto put_lse = [&](const Item& x, int l, float m, float sum) {
       if (a.splits == 1 || pos >= a.rows_l || l >= a.Lq) return;
@@ -643,14 +678,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
-      const Item x = decode(a, it);
+      const Item x = decode<kLens>(a, it);
       if constexpr (kShared) {
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
           const int l = (2 * x.blk + i) * a.rows_l + pos;
           if (x.n() == 0) {
-            float z[32] = {};
-            for (int c = 0; c < DP / 32; ++c) put(x, l, c, z);
+            float z[16] = {};
+            for (int c = 0; c < DP / 16; ++c) put(out_row(x, l), c, z);
             put_lse(x, l, 0.0f, 0.0f);
             continue;
           }
@@ -664,28 +699,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float sum = sum_l[i * kRows + row];
           const float f = sum == 0.0f ? 0.0f : __frcp_rn(sum);
           put_lse(x, l, sum_m[i * kRows + row], sum);
+          const int64_t off = out_row(x, l);
+          __syncwarp();   // together again for the TMEM loads
 #pragma unroll 1
-          for (int c = 0; c < DP / 32; ++c) {
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(o_col(i) + quad + c * 32, r);
+          for (int c = 0; c < DP / 16; ++c) {
+            uint32_t r[16];
+            tmem_ld_32x32b_x16(o_col(i) + quad + c * 16, r);
             tmem_ld_wait();
-            if (c == DP / 32 - 1) {
+            if (c == DP / 16 - 1) {
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(o_free(i));
             }
-            float v[32];
+            float v[16];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = f == 0.0f ? 0.0f : __uint_as_float(r[e]) * f;
-            put(x, l, c, v);
+            for (int e = 0; e < 16; ++e) v[e] = f == 0.0f ? 0.0f : __uint_as_float(r[e]) * f;
+            put(off, c, v);
           }
         }
       } else {
         const int l = x.blk * a.rows_l + pos;
         const int n0 = slot_tiles(x.n(), 0), n1 = slot_tiles(x.n(), 1);
         if (n0 == 0) {
-          float z[32] = {};
-          for (int c = 0; c < DP / 32; ++c) put(x, l, c, z);
+          float z[16] = {};
+          for (int c = 0; c < DP / 16; ++c) put(out_row(x, l), c, z);
           put_lse(x, l, 0.0f, 0.0f);
           continue;
         }
@@ -704,16 +741,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float l0 = sum_l[row], l1 = n1 > 0 ? sum_l[kRows + row] : 0.0f;
         const float sum = a0 * l0 + a1 * l1;
         put_lse(x, l, top, sum);
+        const int64_t off = out_row(x, l);
+        __syncwarp();   // together again for the TMEM loads
         const float f = sum == 0.0f ? 0.0f : __frcp_rn(sum);
         a0 *= f;
         a1 *= f;
 #pragma unroll 1
-        for (int c = 0; c < DP / 32; ++c) {
-          uint32_t r0[32], r1[32];
-          tmem_ld_32x32b_x32(o_col(0) + quad + c * 32, r0);
-          if (n1 > 0) tmem_ld_32x32b_x32(o_col(1) + quad + c * 32, r1);
+        for (int c = 0; c < DP / 16; ++c) {
+          uint32_t r0[16], r1[16];
+          tmem_ld_32x32b_x16(o_col(0) + quad + c * 16, r0);
+          if (n1 > 0) tmem_ld_32x32b_x16(o_col(1) + quad + c * 16, r1);
           tmem_ld_wait();
-          if (c == DP / 32 - 1) {
+          if (c == DP / 16 - 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -721,13 +760,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (n1 > 0) mbar_arrive(o_free(1));
             }
           }
-          float v[32];
+          float v[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
+          for (int e = 0; e < 16; ++e) {
             v[e] = f == 0.0f ? 0.0f : __uint_as_float(r0[e]) * a0;
             if (n1 > 0 && f != 0.0f) v[e] = fmaf(__uint_as_float(r1[e]), a1, v[e]);
           }
-          put(x, l, c, v);
+          put(off, c, v);
         }
       }
     }
@@ -754,7 +793,8 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttnArgs a, i
   const int64_t rows = (int64_t)a.B * a.Hkv * a.Lq * a.G;   // (b, hk, l, g)
   const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (r >= rows) return;
-  const float inv_s = a.s_out ? __frcp_rn(__ldg(a.s_out)) : 1.0f;
+  float inv_s = 1.0f;
+  if (a.s_out) inv_s = __frcp_rn(load_scale(a.s_out));
   float top = -INFINITY;
   for (int s = 0; s < a.splits; ++s) top = fmaxf(top, a.part_lse[s * rows + r]);
   if (top == -INFINITY) top = 0.0f;
@@ -830,9 +870,9 @@ Plan make_plan(const AttnProblem& p, int sms) {
   return x;
 }
 
-template <int DP, bool kF16, bool kMask, bool kShared>
+template <int DP, bool kF16, bool kLens, bool kMask, bool kShared>
 cudaError_t launch_kernel(const AttnMaps& maps, const AttnArgs& a, int grid, cudaStream_t st) {
-  auto* k = cross_attention_kernel<DP, kF16, kMask, kShared>;
+  auto* k = cross_attention_kernel<DP, kF16, kLens, kMask, kShared>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<DP>::kAlloc);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -856,11 +896,19 @@ cudaError_t launch_kernel(const AttnMaps& maps, const AttnArgs& a, int grid, cud
   return cudaGetLastError();
 }
 
+template <int DP, bool kF16, bool kLens, bool kMask>
+cudaError_t launch_rows(const AttnMaps& maps, const AttnArgs& a, bool shared, int grid, cudaStream_t st) {
+  return shared ? launch_kernel<DP, kF16, kLens, kMask, true>(maps, a, grid, st)
+                : launch_kernel<DP, kF16, kLens, kMask, false>(maps, a, grid, st);
+}
+
 template <int DP, bool kF16>
-cudaError_t launch_type(const AttnMaps& maps, const AttnArgs& a, bool mask, bool shared, int grid, cudaStream_t st) {
-  if (mask)
-    return shared ? launch_kernel<DP, kF16, true, true>(maps, a, grid, st) : launch_kernel<DP, kF16, true, false>(maps, a, grid, st);
-  return shared ? launch_kernel<DP, kF16, false, true>(maps, a, grid, st) : launch_kernel<DP, kF16, false, false>(maps, a, grid, st);
+cudaError_t launch_type(const AttnMaps& maps, const AttnArgs& a, bool shared, int grid, cudaStream_t st) {
+  if (a.kv_mask)
+    return a.kv_len ? launch_rows<DP, kF16, true, true>(maps, a, shared, grid, st)
+                    : launch_rows<DP, kF16, false, true>(maps, a, shared, grid, st);
+  return a.kv_len ? launch_rows<DP, kF16, true, false>(maps, a, shared, grid, st)
+                  : launch_rows<DP, kF16, false, false>(maps, a, shared, grid, st);
 }
 
 }  // namespace
@@ -924,10 +972,9 @@ cudaError_t launch_cross_attention(const AttnProblem& p, int sms, cudaStream_t s
     *tmap_err = 1;
     return cudaSuccess;
   }
-  const bool mask = p.kv_len || p.kv_mask;
   const int grid = (int)(x.items < sms ? x.items : sms);
-  if (x.DP == 64) return p.f16 ? launch_type<64, true>(maps, a, mask, x.shared, grid, st) : launch_type<64, false>(maps, a, mask, x.shared, grid, st);
-  return p.f16 ? launch_type<128, true>(maps, a, mask, x.shared, grid, st) : launch_type<128, false>(maps, a, mask, x.shared, grid, st);
+  if (x.DP == 64) return p.f16 ? launch_type<64, true>(maps, a, x.shared, grid, st) : launch_type<64, false>(maps, a, x.shared, grid, st);
+  return p.f16 ? launch_type<128, true>(maps, a, x.shared, grid, st) : launch_type<128, false>(maps, a, x.shared, grid, st);
 }
 
 cudaError_t attention_read_error(cudaStream_t st, uint32_t* err) {
