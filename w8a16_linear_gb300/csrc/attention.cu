@@ -143,6 +143,12 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[32]) {
                : "memory");
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // mbar_wait_warp with every lane asking first: no broadcast on the way of a
 // phase that is complete or about to be.
 __device__ __forceinline__ bool mbar_wait_lanes(uint32_t bar, uint32_t parity, volatile int* abort) {
@@ -153,6 +159,17 @@ __device__ __forceinline__ bool mbar_wait_lanes(uint32_t bar, uint32_t parity, v
   if (!done) done = mbar_wait_warp(bar, parity, abort, kWaitLimitNs);
   __syncwarp();   // the TMEM instructions that follow want the warp together
   return done;
+}
+
+// The roles' registers a thread: softmax warps hold a row of 128 scores.  The
+// block starts with 128 x 512; 176 x 256 + 80 x 256 is the same sum.
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -317,6 +334,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     return true;
   };
 
+  if (warp >= 12) {
+  regs_down<80>();
   if (warp == 13) {
     // ---------------------------------------------------------------- loads
     if (lane == 0) {
@@ -373,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the time.  A slot's MMAs run in the order of their issue: the scores
     // of tile j + 1 may be written over P of tile j, and when they are complete
     // so is the product of tile j.
-    if (lane == 0) {
+    if (elect_one()) {
       const int i = warp == 12 ? 0 : 1;
       uint32_t base = 0;                         // entries of the ring before this item
       uint32_t qcount = 0, pcount = 0, icount = 0;
@@ -398,6 +417,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool first = j == (kShared ? 0 : i), last = j + (kShared ? 1 : 2) >= n;
           // where `walk` puts K and V of tile j
           const uint32_t ek = kShared ? 2 * j : j < 2 ? j : 2 * j - 1, ev = kShared ? 2 * j + 1 : j == n - 1 ? 2 * n - 1 : 2 * j + 2;
+          // The slots take turns: a slot's scores are started when the other's
+          // are complete.  Left alone the two fall into step, and the tensor core
+          // idles while both are in their softmax warps.
+          if (kShared && (i == 1 || pcount > 0))
+            ok = ok && mbar_wait(s_full(1 - i), (pcount - (1 - i)) & 1, abort, kWaitLimitNs);
           int st = take(base + ek);
           if (!ok) break;
           const uint64_t qd = sw128_kmajor_desc(sbase + C::kQ + (kShared ? i : 0) * C::kTile);
@@ -480,8 +504,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok && lane == 0) record_timeout(abort);
     }
+  }
   } else if (warp < 8) {
     // ---------------------------------------------------------------- softmax
+    regs_up<176>();
     const int i = warp >> 2;                     // slot
     const int row = (warp & 3) * 32 + lane;
     const uint32_t quad = (uint32_t)((warp & 3) * 32) << 16;
@@ -514,26 +540,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++scount;
         tc_fence_after();
-        // Two passes over the row's scores in TMEM, 32 columns at a time with the
-        // next 32 on their way: 128 registers a thread hold no whole row.
-        uint32_t r[2][32];
+        uint32_t r[4][32];
         float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         tmem_ld_32x32b_x32(s_col(i) + quad, r[0]);
+        tmem_ld_32x32b_x32(s_col(i) + quad + 32, r[1]);
+        tmem_ld_wait_for(r[0]);
+        tmem_ld_wait_for(r[1]);
+        tmem_ld_32x32b_x32(s_col(i) + quad + 64, r[2]);
+        tmem_ld_32x32b_x32(s_col(i) + quad + 96, r[3]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          tmem_ld_wait_for(r[c & 1]);
-          tmem_ld_32x32b_x32(s_col(i) + quad + (c + 1) % 4 * 32, r[(c + 1) & 1]);
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float v0 = __uint_as_float(r[c & 1][e]), v1 = __uint_as_float(r[c & 1][e + 1]);
-            if (masked) {
-              if (!((word[e & 3] >> (8 * c + (e >> 2))) & 1)) v0 = -INFINITY;
-              if (!((word[(e + 1) & 3] >> (8 * c + (e >> 2))) & 1)) v1 = -INFINITY;
-            }
-            tops[(e >> 1) & 3] = fmaxf(fmaxf(tops[(e >> 1) & 3], v0), v1);
+          if (c == 2) {
+            tmem_ld_wait_for(r[2]);
+            tmem_ld_wait_for(r[3]);
           }
+          if (masked) {   // a key that does not count has the weight exp2(-inf) = 0
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((word[e & 3] >> (8 * c + (e >> 2))) & 1)) r[c][e] = 0xFF800000u;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            tops[(e >> 1) & 3] = fmaxf(fmaxf(tops[(e >> 1) & 3], __uint_as_float(r[c][e])), __uint_as_float(r[c][e + 1]));
         }
-        tmem_ld_wait_for(r[0]);   // columns 0 - 31 again
         const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * a.scale_log2;
         // Scores of slot i are complete, so its product with the previous tile
         // is too (issued before them): O_i may be rescaled here.
@@ -560,21 +589,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t p[16];
-          if (c > 0) tmem_ld_wait_for(r[c & 1]);
-          if (c < 3) tmem_ld_32x32b_x32(s_col(i) + quad + (c + 1) * 32, r[(c + 1) & 1]);
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            const F2 t = fma2(F2{__uint_as_float(r[c & 1][e]), __uint_as_float(r[c & 1][e + 1])}, scale, minus_m);
-            F2 w = F2{ex2(t.x), ex2(t.y)};
-            if (masked) {
-              if (!((word[e & 3] >> (8 * c + (e >> 2))) & 1)) w.x = 0.0f;
-              if (!((word[(e + 1) & 3] >> (8 * c + (e >> 2))) & 1)) w.y = 0.0f;
-            }
+            const F2 t = fma2(F2{__uint_as_float(r[c][e]), __uint_as_float(r[c][e + 1])}, scale, minus_m);
+            const F2 w = F2{ex2(t.x), ex2(t.y)};
             sums[(e >> 1) & 1] = add2(sums[(e >> 1) & 1], w);
             p[e >> 1] = cvt16x2(kF16, w.x, w.y);
           }
-          // P takes the first half of S_i's columns: chunk c's 16 lie at or below
-          // the first column of the scores that are still to be read
+          // P takes the first half of S_i's columns, all of which are in registers
           tmem_st_32x32b_x16(s_col(i) + quad + c * 16, p);
           if (c & 1) {   // 64 keys of P: the product with V may start on them
             tmem_st_wait();
@@ -599,8 +621,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(l_full(i));
     }
     if (!ok && lane == 0) record_timeout(abort);
-  } else if (warp < 12) {
+  } else {
     // ---------------------------------------------------------------- epilogue
+    regs_down<80>();
     const int row = (warp & 3) * 32 + lane;
     const uint32_t quad = (uint32_t)((warp & 3) * 32) << 16;
     const int pos = row / a.G, g = row - pos * a.G;
