@@ -7,6 +7,7 @@ library is missing the calls raise instead of falling back to anything else.
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -96,9 +97,9 @@ SIGNATURES = {
     "fp8_linear_w8a8_pertoken": (ctypes.c_int, [_c_void_p, _i64, _i64, _c_void_p, _i32, ctypes.POINTER(_c_void_p),
                                                 ctypes.POINTER(_i64), ctypes.POINTER(_c_void_p),
                                                 ctypes.POINTER(_c_void_p), _c_void_p]),
-    "cross_attention": (ctypes.c_int, [ctypes.POINTER(AttentionDesc), _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+    "cross_attention": (ctypes.c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                        _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p]),
-    "cross_attention_workspace": (ctypes.c_int, [ctypes.POINTER(AttentionDesc), ctypes.POINTER(_i64)]),
+    "cross_attention_workspace": (ctypes.c_int, [_c_void_p, ctypes.POINTER(_i64)]),
     "step_policy_dispatch": (ctypes.c_int, [_c_void_p, _i32, _i32, ctypes.POINTER(_i32)]),
     "w8_check_group_scales": (ctypes.c_int, [ctypes.POINTER(_c_void_p), _i32]),
     "w8_step_policy_parse": (ctypes.c_int, [ctypes.c_char_p, ctypes.POINTER(StepPolicy),
@@ -568,11 +569,41 @@ def swiglu_2in_ex_16(gate, up, limit=None, alpha=1.0, beta=0.0, out=None, stream
     return out
 
 
-def _vector(t, n, name):
+# The calls below are made once a token and layer: their checks are a few
+# plain conditions each, and only a failed one goes on to say what is wrong.
+
+_DTYPE16 = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+_CODES = tuple(t for t in (torch.uint8, getattr(torch, "float8_e4m3fn", None)) if t is not None)
+
+
+def _raw_stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _refuse(t, name, dtypes, shape=None, numel=None):
+    """Raises what is wrong with ``t`` (wanted: a dense CUDA tensor of one of
+    ``dtypes`` and of this shape or number of values)."""
     _dense(t, name)
-    if t.dtype != torch.float32 or t.numel() != n:
-        raise W8Error(5, f"{name}: expected {n} float32 values on the device")
-    return t
+    if t.dtype not in dtypes:
+        raise W8Error(5, f"{name}: expected {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    want = tuple(shape) if shape is not None else numel
+    raise W8Error(2 if shape is not None else 5, f"{name}: shape {tuple(t.shape)}, expected {want}")
+
+
+def _like(t, name, dtypes, shape):
+    """data_ptr of ``t``, a dense CUDA tensor of one of ``dtypes`` and of ``shape``."""
+    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        _refuse(t, name, dtypes, shape=shape)
+    return t.data_ptr()
+
+
+def _floats(t, name, n):
+    """data_ptr of ``t``, n dense float32 values on the device."""
+    if t.dtype is not torch.float32 or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
+        _refuse(t, name, (torch.float32,), numel=n)
+    return t.data_ptr()
 
 
 def add_rms_norm_quant(x, residual, weight, eps=1e-6, s_in=None, out=None, s_tok=None, res_out=None, h_out=None,
@@ -583,39 +614,38 @@ def add_rms_norm_quant(x, residual, weight, eps=1e-6, s_in=None, out=None, s_tok
     tokens' scales (None with ``s_in``) and the sum in 16 bits (None without a
     residual).  ``res_out`` may be ``residual`` itself; ``h_out`` receives the
     norm in 16 bits when given."""
-    x, dt = _as_16(x, "x")
-    K = x.shape[-1]
+    dtype, shape = x.dtype, x.shape
+    dt = _DTYPE16.get(dtype)
+    if dt is None or not x.is_contiguous() or not x.is_cuda or not shape:
+        _as_16(x, "x")
+        raise W8Error(2, "x: expected at least one dimension")
+    same = (dtype,)
+    K = shape[-1]
     M = x.numel() // K if K else 0
-
-    def like_x(t, name):
-        t, d = _as_16(t, name)
-        if d != dt or t.shape != x.shape:
-            raise W8Error(5, f"{name}: expected {x.dtype} of shape {tuple(x.shape)}")
-        return t
-
-    weight, dw = _as_16(weight, "weight")
-    if dw != dt or weight.numel() != K:
-        raise W8Error(5, f"weight: expected {K} values of {x.dtype}")
+    p_w = _like(weight, "weight", same, (K,))
+    p_r = p_ro = p_in = p_tok = p_h = None
     if residual is not None:
-        like_x(residual, "residual")
-        res_out = torch.empty_like(x) if res_out is None else like_x(res_out, "res_out")
+        p_r = _like(residual, "residual", same, shape)
+        if res_out is None:
+            res_out = torch.empty_like(x)
+        p_ro = _like(res_out, "res_out", same, shape)
     elif res_out is not None:
         raise W8Error(1, "res_out without a residual")
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
-    q = _as_u8(out, "out")
-    if q.shape != x.shape:
-        raise W8Error(2, f"out: shape {tuple(q.shape)} differs from x {tuple(x.shape)}")
+        out = torch.empty(shape, dtype=torch.uint8, device=x.device)
+    p_q = _like(out, "out", _CODES, shape)
     if s_in is not None:
         if s_tok is not None:
             raise W8Error(11, "s_in and s_tok: one of them")
-        _scalar(s_in, "s_in")
+        p_in = _floats(s_in, "s_in", 1)
     else:
-        s_tok = torch.empty((M,), dtype=torch.float32, device=x.device) if s_tok is None else _vector(s_tok, M, "s_tok")
+        if s_tok is None:
+            s_tok = torch.empty((M,), dtype=torch.float32, device=x.device)
+        p_tok = _floats(s_tok, "s_tok", M)
     if h_out is not None:
-        like_x(h_out, "h_out")
-    _check(lib().add_rms_norm_quant(_ptr(x), _ptr(residual), dt, M, K, _ptr(weight), float(eps), _ptr(s_in),
-                                    _ptr(s_tok), _ptr(q), _ptr(h_out), _ptr(res_out), _stream(stream)))
+        p_h = _like(h_out, "h_out", same, shape)
+    _check(lib().add_rms_norm_quant(x.data_ptr(), p_r, dt, M, K, p_w, eps, p_in, p_tok, p_q, p_h, p_ro,
+                                    _raw_stream(stream)))
     return out, s_tok, res_out
 
 
@@ -623,28 +653,24 @@ def fp8_linear_w8a8_pertoken_group(qx, s_tok, weights, channel_scales, outs=None
     """G W8A8 projections of an activation whose tokens have scales of their own
     (``s_tok``, one float32 a token), on weights with one scale for each output
     channel."""
-    q = _as_u8(qx, "qx")
-    K = q.shape[-1]
-    M = q.numel() // K if K else 0
+    lead = qx.shape[:-1]
+    if qx.dtype not in _CODES or not qx.is_contiguous() or not qx.is_cuda or not qx.shape:
+        _as_u8(qx, "qx")
+        raise W8Error(2, "qx: expected at least one dimension")
+    K = qx.shape[-1]
+    M = qx.numel() // K if K else 0
     G = len(weights)
-    ws_q = [_as_u8(w, f"w[{i}]") for i, w in enumerate(weights)]
-    for i, w in enumerate(ws_q):
-        if w.dim() != 2 or w.shape[1] != K:
-            raise W8Error(2, f"w[{i}]: expected [N, {K}], got {tuple(w.shape)}")
-    if len(channel_scales) != G:
-        raise W8Error(2, f"{G} weights, {len(channel_scales)} sets of channel scales")
+    if len(channel_scales) != G or (outs is not None and len(outs) != G):
+        raise W8Error(2, f"{G} weights: as many sets of channel scales and outputs are wanted")
+    ns = [w.shape[0] for w in weights]
+    p_w = [_like(w, "w", _CODES, (n, K)) for w, n in zip(weights, ns)]
+    p_s = [_floats(c, "s_ch", n) for c, n in zip(channel_scales, ns)]
     if outs is None:
-        outs = [torch.empty(*qx.shape[:-1], w.shape[0], dtype=torch.bfloat16, device=qx.device) for w in ws_q]
-    for i, (o, w) in enumerate(zip(outs, ws_q)):
-        if _as_bf16(o, f"y[{i}]").numel() != M * w.shape[0]:
-            raise W8Error(2, f"y[{i}]: expected {M} x {w.shape[0]} values")
-    arr_w = (ctypes.c_void_p * G)(*[w.data_ptr() for w in ws_q])
-    arr_n = (ctypes.c_int64 * G)(*[w.shape[0] for w in ws_q])
-    arr_s = (ctypes.c_void_p * G)(*[_vector(s, w.shape[0], f"s_ch[{i}]").data_ptr()
-                                    for i, (s, w) in enumerate(zip(channel_scales, ws_q))])
-    arr_y = (ctypes.c_void_p * G)(*[o.data_ptr() for o in outs])
-    _check(lib().fp8_linear_w8a8_pertoken(_ptr(q), M, K, _ptr(_vector(s_tok, M, "s_tok")), G, arr_w, arr_n, arr_s,
-                                          arr_y, _stream(stream)))
+        outs = [torch.empty((*lead, n), dtype=torch.bfloat16, device=qx.device) for n in ns]
+    p_y = [_like(y, "y", (torch.bfloat16,), (*lead, n)) for y, n in zip(outs, ns)]
+    ptrs = ctypes.c_void_p * G
+    _check(lib().fp8_linear_w8a8_pertoken(qx.data_ptr(), M, K, _floats(s_tok, "s_tok", M), G, ptrs(*p_w),
+                                          (ctypes.c_int64 * G)(*ns), ptrs(*p_s), ptrs(*p_y), _raw_stream(stream)))
     return outs
 
 
@@ -654,31 +680,39 @@ def fp8_linear_w8a8_pertoken(qx, s_tok, w, s_ch, out=None, stream=None):
                                           stream=stream)[0]
 
 
-def _heads(t, name, dtype, device):
+# w8_attention_desc as bytes (the fields of AttentionDesc, in their order)
+_attention_desc = struct.Struct("=19qif").pack
+
+
+def _refuse_heads(t, name, dtypes, device):
     if t.dim() != 4:
         raise W8Error(2, f"{name}: expected [samples, positions, heads, D], got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise W8Error(5, f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != device or not t.is_cuda:
+    if t.dtype not in dtypes:
+        raise W8Error(5, f"{name}: expected {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if not t.is_cuda or t.device != device:
         raise W8Error(1, f"{name}: must be a CUDA tensor on q's device")
-    if t.shape[3] > 1 and t.stride(3) != 1:
-        raise W8Error(4, f"{name}: the head's dimensions must be contiguous")
-    return t
+    raise W8Error(4, f"{name}: the head's dimensions must be contiguous")
 
 
-def _attention_desc(q, k, v, out, kv_mask, scale):
-    B, Lq, Hq, D = q.shape
-    return AttentionDesc(B, Lq, k.shape[1], Hq, k.shape[2], D, q.stride()[:3], k.stride()[:3], v.stride()[:3],
-                         out.stride()[:3], kv_mask.stride(0) if kv_mask is not None else 0,
-                         DTYPE_F16 if q.dtype == torch.float16 else DTYPE_BF16,
-                         D ** -0.5 if scale is None else float(scale))
+def _heads(t, name, dtypes, device):
+    """(sample, position, head) strides of ``t``, [B, L, H, D] with dense D."""
+    if t.dim() != 4 or t.dtype not in dtypes or not t.is_cuda or t.device != device:
+        _refuse_heads(t, name, dtypes, device)
+    sb, sl, sh, sd = t.stride()
+    if sd != 1 and t.shape[3] > 1:
+        _refuse_heads(t, name, dtypes, device)
+    return sb, sl, sh
 
 
 def cross_attention_workspace(q, k, v):
     """float32 scratch for cross_attention(q, k, v, ..., ws=...) of these shapes
     (caller-side allocation; empty when none is needed)."""
     n = ctypes.c_int64(0)
-    _check(lib().cross_attention_workspace(ctypes.byref(_attention_desc(q, k, v, q, None, None)), ctypes.byref(n)))
+    B, Lq, H, D = q.shape
+    st = [_heads(t, name, tuple(_DTYPE16), q.device) for t, name in ((q, "q"), (k, "k"), (v, "v"))]
+    desc = _attention_desc(B, Lq, k.shape[1], H, k.shape[2], D, *st[0], *st[1], *st[2], *st[0], 0, _DTYPE16[q.dtype],
+                           D ** -0.5)
+    _check(lib().cross_attention_workspace(desc, ctypes.byref(n)))
     return torch.empty((n.value,), dtype=torch.float32, device=q.device)
 
 
@@ -689,19 +723,24 @@ def cross_attention(q, k, v, kv_len=None, kv_mask=None, scale=None, s_out=None, 
     ``kv_mask`` (bool or uint8 [B, Lk], true where a key counts) limit the keys;
     a row without keys is 0.  ``scale`` defaults to D ** -0.5.  Returns [B, Lq, Hq, D]
     in q's dtype, or with ``s_out`` E4M3 codes."""
-    if q.dtype not in (torch.bfloat16, torch.float16):
+    dt, device = _DTYPE16.get(q.dtype), q.device
+    if dt is None:
         raise W8Error(5, f"q: expected bfloat16 or float16, got {q.dtype}")
-    _heads(q, "q", q.dtype, q.device)
-    _heads(k, "k", q.dtype, q.device)
-    _heads(v, "v", q.dtype, q.device)
-    B, Lq, Hq, D = q.shape
-    Lk = k.shape[1]
+    same = (q.dtype,)
+    sq = _heads(q, "q", same, device)
+    sk = _heads(k, "k", same, device)
+    sv = _heads(v, "v", same, device)
+    shape = q.shape
+    B, Lq, H, D = shape
+    Lk, Hk = k.shape[1], k.shape[2]
     if k.shape != v.shape or k.shape[0] != B or k.shape[3] != D:
         raise W8Error(2, f"q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)} do not fit together")
+    p_len = p_mask = p_s = p_ws = None
+    mask_stride = n_ws = 0
     if kv_len is not None:
-        _dense(kv_len, "kv_len")
-        if kv_len.dtype != torch.int32 or kv_len.numel() != B:
-            raise W8Error(5, f"kv_len: expected {B} int32 values")
+        if kv_len.dtype is not torch.int32 or kv_len.numel() != B or not kv_len.is_contiguous() or not kv_len.is_cuda:
+            _refuse(kv_len, "kv_len", (torch.int32,), numel=B)
+        p_len = kv_len.data_ptr()
     if kv_mask is not None:
         if kv_mask.dtype not in (torch.bool, torch.uint8) or kv_mask.shape != (B, Lk):
             raise W8Error(5, f"kv_mask: expected bool or uint8 [{B}, {Lk}]")
@@ -709,28 +748,30 @@ def cross_attention(q, k, v, kv_len=None, kv_mask=None, scale=None, s_out=None, 
             raise W8Error(1, "kv_mask: must be a CUDA tensor")
         if Lk > 1 and kv_mask.stride(1) != 1:
             raise W8Error(4, "kv_mask: a sample's keys must be contiguous")
+        mask_stride = kv_mask.stride(0)
+        p_mask = kv_mask.data_ptr()
+    kinds = same
+    if s_out is not None:
+        kinds = _CODES
+        p_s = _floats(s_out, "s_out", 1)
     if out is None:
-        out = torch.empty((B, Lq, Hq, D), dtype=q.dtype if s_out is None else torch.uint8, device=q.device)
-    if out.shape != q.shape:
+        out = torch.empty(shape, dtype=kinds[0], device=device)
+    elif out.shape != shape:
         raise W8Error(2, f"out: shape {tuple(out.shape)} differs from q {tuple(q.shape)}")
-    if s_out is None:
-        _heads(out, "out", q.dtype, q.device)
-    else:
-        _scalar(s_out, "s_out")
-        if out.dtype not in (torch.uint8, getattr(torch, "float8_e4m3fn", None)):
-            raise W8Error(5, f"out: expected E4M3 codes (uint8 or float8_e4m3fn), got {out.dtype}")
-        _heads(out, "out", out.dtype, q.device)
-    desc = _attention_desc(q, k, v, out, kv_mask, scale)
+    so = _heads(out, "out", kinds, device)
+    desc = _attention_desc(B, Lq, Lk, H, Hk, D, *sq, *sk, *sv, *so, mask_stride, dt,
+                           D ** -0.5 if scale is None else scale)
+    L = lib()
     if ws is None:
         n = ctypes.c_int64(0)
-        _check(lib().cross_attention_workspace(ctypes.byref(desc), ctypes.byref(n)))
+        _check(L.cross_attention_workspace(desc, ctypes.byref(n)))
         if n.value:
-            ws = torch.empty((n.value,), dtype=torch.float32, device=q.device)
-    elif _dense(ws, "ws").dtype != torch.float32:
-        raise W8Error(5, f"ws: expected float32, got {ws.dtype}")
-    _check(lib().cross_attention(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(kv_len), _ptr(kv_mask),
-                                 _ptr(s_out), _ptr(out), _ptr(ws), ws.numel() if ws is not None else 0,
-                                 _stream(stream)))
+            ws = torch.empty((n.value,), dtype=torch.float32, device=device)
+    if ws is not None:
+        n_ws = ws.numel()
+        p_ws = _floats(ws, "ws", n_ws)
+    _check(L.cross_attention(desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), p_len, p_mask, p_s, out.data_ptr(), p_ws,
+                             n_ws, _raw_stream(stream)))
     return out
 
 

@@ -35,6 +35,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 
@@ -121,16 +122,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-
 // Waits for this thread's TMEM loads; naming the registers keeps their uses
 // behind the wait while other loads are still under way.
 __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[32]) {
@@ -141,12 +132,6 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[32]) {
                  "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
                :
                : "memory");
-}
-
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
-  return p != 0;
 }
 
 // mbar_wait_warp with every lane asking first: no broadcast on the way of a
@@ -206,11 +191,6 @@ struct Item {
 __device__ __forceinline__ int load_len(const int32_t* p) {
   int v;
   asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
-__device__ __forceinline__ float load_scale(const float* p) {
-  float v;
-  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
   return v;
 }
 __device__ __forceinline__ bool load_mask(const uint8_t* p) {
@@ -628,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t quad = (uint32_t)((warp & 3) * 32) << 16;
     const int pos = row / a.G, g = row - pos * a.G;
     float inv_s = 1.0f;
-    if (a.s_out) inv_s = __frcp_rn(load_scale(a.s_out));
+    if (a.s_out) inv_s = __frcp_rn(ld_f32(a.s_out));
     uint32_t icount[2] = {0, 0};
     bool ok = true;
 
@@ -817,7 +797,7 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttnArgs a, i
   const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (r >= rows) return;
   float inv_s = 1.0f;
-  if (a.s_out) inv_s = __frcp_rn(load_scale(a.s_out));
+  if (a.s_out) inv_s = __frcp_rn(ld_f32(a.s_out));
   float top = -INFINITY;
   for (int s = 0; s < a.splits; ++s) top = fmaxf(top, a.part_lse[s * rows + r]);
   if (top == -INFINITY) top = 0.0f;
@@ -896,8 +876,16 @@ Plan make_plan(const AttnProblem& p, int sms) {
 template <int DP, bool kF16, bool kLens, bool kMask, bool kShared>
 cudaError_t launch_kernel(const AttnMaps& maps, const AttnArgs& a, int grid, cudaStream_t st) {
   auto* k = cross_attention_kernel<DP, kF16, kLens, kMask, kShared>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<DP>::kAlloc);
+  static std::atomic<uint64_t> allowed{0};   // devices on which the kernel may use its shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(allowed.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<DP>::kAlloc);
+    if (e != cudaSuccess) return e;
+    allowed.fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);

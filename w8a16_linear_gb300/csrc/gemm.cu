@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(Layout<MODE, CG>::kThreads, 1)
       tc_fence_after();
       const int row0 = m0 + (int)rank * BM + wq * 32;
       const int ng = args.N[g];
-      if constexpr (C::kTok) alpha = __ldg(args.s_in + min(row0 + lane, args.M - 1));
+      if constexpr (C::kTok) alpha = ld_f32(args.s_in + min(row0 + lane, args.M - 1));
       const uint32_t tbase = tmem_base + ((uint32_t)(wq * 32) << 16) + (uint32_t)(acc * kAccCols);
       if constexpr (!kGlu) {
         const int chunks = width / 64;
@@ -929,6 +929,200 @@ __global__ void __launch_bounds__(a16t::kThreads, 1)
   }
 }
 
+// ------------------------------------------------------------------ few tokens
+//
+// W8A8T for few tokens, where the time is that of reading the weights (one
+// token: N K bytes, 2 N K operations).  gemm_kernel's tiles of 256 columns
+// would leave most SMs idle, so the product is computed transposed and cut
+// along K as well: a tile is 128 weight rows (the MMA's M) by up to 128
+// tokens (its N, padded to 16), and a cluster of `split` CTAs shares its K
+// range.  Each CTA streams its part of the weights through a TMA ring (6 to 8
+// stages of 128 bytes of K, up to 144 KB in flight) and leaves its partial
+// sums, binary32, in its shared memory; after a cluster barrier the CTAs add
+// them through distributed shared memory, each a share of the outputs, always in
+// the order of the ranks: no workspace, no atomics, the same bits each time.
+namespace few {
+constexpr int BW = 128;                        // weight rows per tile
+constexpr int kWBytes = BW * 128;
+constexpr int kThreads = 192;                  // producer, MMA, four epilogue warps
+constexpr int kMaxStages = 8;
+constexpr int kNumBars = 2 * kMaxStages + 2;   // full, empty, accumulator, drain
+constexpr int kTail = kNumBars * 8 + 8 + 1024; // barriers, TMEM slot, abort flag, alignment
+constexpr int kMaxSmem = 6 * (kWBytes + 128 * 128) + kTail;
+static_assert(kMaxSmem <= 232448, "shared memory budget");
+
+struct Args {
+  int G, M, NT;            // tokens per tile: NT (a multiple of 16, at most 128)
+  int N[kMaxGroup], tiles_n[kMaxGroup];
+  int tiles_t;             // token tiles
+  int split, atoms;        // CTAs per cluster; 128-byte pieces of K
+  int stages;
+  const float* s_tok;
+  const float* s_ch[kMaxGroup];
+  uint16_t* y[kMaxGroup];
+};
+}  // namespace few
+
+__global__ void __launch_bounds__(few::kThreads) gemm_few_kernel(const __grid_constant__ Maps maps,
+                                                                 const __grid_constant__ few::Args a) {
+  using namespace few;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const int S = a.stages;
+  const int stage_bytes = kWBytes + a.NT * 128;
+  const uint32_t bar0 = sbase + (uint32_t)(S * stage_bytes);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
+  const uint32_t acc_bar = bar0 + 8u * (2 * kMaxStages), drain_bar = acc_bar + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S * stage_bytes + kNumBars * 8);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = a.split > 1 ? (int)cluster_ctarank() : 0;
+  uint32_t cols = 32;
+  while ((int)cols < a.NT) cols *= 2;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    mbar_init(acc_bar, 1);
+    mbar_init(drain_bar, 1);
+    *abort = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&maps.a);
+    for (int g = 0; g < a.G; ++g) prefetch_tensormap(map_b(maps, g));
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+
+  // tile -> projection, first weight row, first token; this CTA's share of K
+  int tile = (int)blockIdx.x / a.split, g = 0;
+  const int t0 = tile % a.tiles_t * a.NT;
+  tile /= a.tiles_t;
+  while (g < a.G - 1 && tile >= a.tiles_n[g]) tile -= a.tiles_n[g++];
+  const int n0 = tile * BW;
+  const int k0 = a.atoms * rank / a.split, k1 = a.atoms * (rank + 1) / a.split;
+
+  if (warp == 0) {
+    if (elect_one()) {
+      int s = 0;
+      uint32_t ph = 0, issued = 0;
+      for (int k = k0; k < k1; ++k) {
+        if (!mbar_wait(empty_bar(s), ph ^ 1, abort, kWaitLimitNs)) {
+          record_timeout(abort);
+          break;
+        }
+        ++issued;
+        mbar_arrive_expect_tx(full_bar(s), (uint32_t)stage_bytes);
+        const uint32_t dst = sbase + (uint32_t)(s * stage_bytes);
+        tma_load_2d(dst, map_b(maps, g), full_bar(s), 128 * k, n0);
+        tma_load_2d(dst + kWBytes, &maps.a, full_bar(s), 128 * k, t0);
+        if (++s == S) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+      // Every stage's most recent copies must have landed before exit.
+      volatile int never = 0;
+      for (int j = 0; j < S && (uint32_t)j < issued; ++j) {
+        const uint32_t l = issued - 1 - j;
+        if (!mbar_wait(full_bar((int)(l % S)), (l / S) & 1, &never, kWaitLimitNs)) atomicOr(&g_gemm_err, kErrTimeout);
+      }
+    }
+  } else if (warp == 1) {
+    if (elect_one()) {
+      const uint32_t idesc = make_idesc(0, 0, BW, (uint32_t)a.NT);
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int k = k0; k < k1; ++k) {
+        if (!(ok = mbar_wait(full_bar(s), ph, abort, kWaitLimitNs))) {
+          record_timeout(abort);
+          break;
+        }
+        tc_fence_after();
+        const uint64_t wd = sw128_kmajor_desc(sbase + (uint32_t)(s * stage_bytes));
+        const uint64_t xd = sw128_kmajor_desc(sbase + (uint32_t)(s * stage_bytes + kWBytes));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)   // 32 bytes of K each
+          mma_f8f6f4(tmem, wd + 2 * j, xd + 2 * j, idesc, (k - k0) | j);
+        mma_commit(empty_bar(s));
+        if (++s == S) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+      if (ok) mma_commit(acc_bar);
+      mma_commit(drain_bar);
+      volatile int never = 0;
+      if (!mbar_wait(drain_bar, 0, &never, kWaitLimitNs)) atomicOr(&g_gemm_err, kErrTimeout);
+    }
+  } else {
+    // Partial sums to shared memory, [token][weight row], over the ring: its
+    // last copies have been read when the accumulator is complete.
+    const int q = warp & 3;
+    float* red = reinterpret_cast<float*>(smem);
+    if (mbar_wait_warp(acc_bar, 0, abort, kWaitLimitNs)) {
+      tc_fence_after();
+      for (int c = 0; c < a.NT; c += 16) {
+        uint32_t r[16];
+        tmem_ld_32x32b_x16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c, r);
+        tmem_ld_wait();
+        if (k0 == k1) {   // no part of K: nothing was accumulated
+#pragma unroll
+          for (int j = 0; j < 16; ++j) r[j] = 0;
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) red[(c + j) * BW + q * 32 + lane] = __uint_as_float(r[j]);
+      }
+    } else if (lane == 0) {
+      record_timeout(abort);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, cols);
+  }
+  if (a.split > 1) cluster_sync();
+  // Eight weight rows of one token at a time, shared out over the cluster.
+  const int tokens = min(a.NT, a.M - t0);
+  const int ng = a.N[g];
+  for (int u = rank * kThreads + (int)threadIdx.x; u < tokens * (BW / 8); u += a.split * kThreads) {
+    const int t = u / (BW / 8), f = u % (BW / 8) * 8;
+    if (n0 + f >= ng) continue;
+    const uint32_t at = sbase + (uint32_t)((t * BW + f) * 4);
+    float v[8] = {};
+    for (int s = 0; s < a.split; ++s) {
+      const uint32_t peer = a.split > 1 ? mapa_shared(at, (uint32_t)s) : at;
+      const float4 lo = ld_cluster_f4(peer), hi = ld_cluster_f4(peer + 16);
+      v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w;
+      v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
+    }
+    const float st = ld_f32(a.s_tok + t0 + t);
+    const float* ch = g == 0 ? a.s_ch[0] : g == 1 ? a.s_ch[1] : a.s_ch[2];
+    uint16_t* y = g == 0 ? a.y[0] : g == 1 ? a.y[1] : a.y[2];
+    const float4 c0 = __ldg(reinterpret_cast<const float4*>(ch + n0 + f));
+    const float4 c1 = __ldg(reinterpret_cast<const float4*>(ch + n0 + f + 4));
+    auto val = [&](float x, float c) { return __fmul_rn(__fmul_rn(x, st), c); };
+    *reinterpret_cast<uint4*>(y + (int64_t)(t0 + t) * ng + n0 + f) =
+        make_uint4(cvt_bf16x2(val(v[0], c0.x), val(v[1], c0.y)), cvt_bf16x2(val(v[2], c0.z), val(v[3], c0.w)),
+                   cvt_bf16x2(val(v[4], c1.x), val(v[5], c1.y)), cvt_bf16x2(val(v[6], c1.z), val(v[7], c1.w)));
+  }
+  if (a.split > 1) cluster_sync();   // no CTA leaves while another reads its sums
+}
+
 // ------------------------------------------------------------------ host side
 
 // m-blocks per rasterisation group: as many as keep the group's activation
@@ -987,8 +1181,9 @@ bool encode_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint6
   return r == CUDA_SUCCESS;
 }
 
-cudaError_t launch_cluster(void (*kern)(Maps, Args), int grid, int threads, int smem, int cg,
-                           cudaStream_t st, const Maps& maps, const Args& args) {
+template <typename A>
+cudaError_t launch_cluster(void (*kern)(Maps, A), int grid, int threads, int smem, int cg,
+                           cudaStream_t st, const Maps& maps, const A& args) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -1153,7 +1348,53 @@ cudaError_t launch_gemm_w8a8(const GemmProblem& p, int sms, cudaStream_t st, int
                      : launch<Mode::W8A8, 1>(p, sms, st, tmap_err);
 }
 
+cudaError_t launch_few(const GemmProblem& p, int sms, cudaStream_t st, int* tmap_err) {
+  using namespace few;
+  *tmap_err = 0;
+  Maps maps;
+  few::Args a;
+  std::memset(&maps, 0, sizeof(maps));
+  std::memset(&a, 0, sizeof(a));
+  a.G = p.G;
+  a.M = (int)p.M;
+  a.NT = p.M >= 128 ? 128 : ((int)p.M + 15) / 16 * 16;
+  a.tiles_t = (a.M + a.NT - 1) / a.NT;
+  a.atoms = (int)((p.K + 127) / 128);
+  a.s_tok = p.s_in;
+  bool ok = encode_2d(&maps.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.x, p.K, p.M, p.K, 128, a.NT, CU_TENSOR_MAP_SWIZZLE_128B);
+  int tiles = 0;
+  for (int g = 0; g < p.G; ++g) {
+    a.N[g] = (int)p.N[g];
+    a.tiles_n[g] = (a.N[g] + BW - 1) / BW;
+    tiles += a.tiles_n[g] * a.tiles_t;
+    a.s_ch[g] = p.s_w[g];
+    a.y[g] = static_cast<uint16_t*>(p.y[g]);
+    ok = ok && encode_2d(&maps.b[g], CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w[g], p.K, p.N[g], p.K, 128, BW,
+                         CU_TENSOR_MAP_SWIZZLE_128B);
+  }
+  if (!ok) {
+    *tmap_err = 1;
+    return cudaSuccess;
+  }
+  // as many CTAs a tile as fill the GPU once, each with two pieces of K at least
+  a.split = 1;
+  while (a.split < 8 && tiles * a.split * 2 <= sms && a.atoms >= a.split * 4) a.split *= 2;
+  const int stage = kWBytes + a.NT * 128;
+  a.stages = (kMaxSmem - kTail) / stage;
+  if (a.stages > kMaxStages) a.stages = kMaxStages;
+  // the partial sums go over the ring
+  return launch_cluster(gemm_few_kernel, tiles * a.split, kThreads, a.stages * stage + kTail, a.split, st, maps, a);
+}
+
+// Few tokens: tiles of gemm_kernel that would fill less than half of the GPU.
+bool use_few(const GemmProblem& p, int sms) {
+  int64_t tiles = 0;
+  for (int g = 0; g < p.G; ++g) tiles += (p.M + 2 * BM - 1) / (2 * BM) * ((p.N[g] + 255) / 256);
+  return p.M <= BM || 4 * tiles <= sms;
+}
+
 cudaError_t launch_gemm_w8a8_token(const GemmProblem& p, int sms, cudaStream_t st, int* tmap_err) {
+  if (use_few(p, sms)) return launch_few(p, sms, st, tmap_err);
   return use_pair(p) ? launch<Mode::W8A8T, 2>(p, sms, st, tmap_err)
                      : launch<Mode::W8A8T, 1>(p, sms, st, tmap_err);
 }
