@@ -67,8 +67,7 @@ struct Cfg {
   static constexpr int kStages = DP == 128 ? 4 : 6;
   static constexpr int kQ = 0;
   static constexpr int kRing = kQ + 2 * kTile;
-  static constexpr int kOut = kRing + kStages * kTile;   // 32 rows of 128 bytes for each epilogue warp
-  static constexpr int kSum = kOut + 4 * 32 * 128;       // l[2][128], m[2][128]
+  static constexpr int kSum = kRing + kStages * kTile;   // l[2][128], m[2][128]
   static constexpr int kBar = kSum + 4 * kRows * 4;
   // full[S], empty[S], clean[S], q_full[2], q_empty[2], s_full[2], p_full[2],
   // o_full[2], l_full[2], o_free[2], p_half[2], drain[2]
@@ -96,6 +95,7 @@ struct AttnArgs {
   const float* s_out;         // not null: E4M3 output
   void* out;
   int64_t o_b, o_l, o_h;      // element strides of the output
+  int wide;                   // output rows are 32-byte aligned and whole multiples of 32 bytes
   float* part;                // splits > 1: normalised partial outputs, then their log2 sums
   float* part_lse;
 };
@@ -147,7 +147,7 @@ __device__ __forceinline__ bool mbar_wait_lanes(uint32_t bar, uint32_t parity, v
 }
 
 // The roles' registers a thread: softmax warps hold a row of 128 scores.  The
-// block starts with 128 x 512; 176 x 256 + 80 x 256 is the same sum.
+// block starts with 128 x 512; 176 x 256 + 88 x 128 + 72 x 128 is the same sum.
 template <int N>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp >= 12) {
-  regs_down<80>();
+  regs_down<72>();
   if (warp == 13) {
     // ---------------------------------------------------------------- loads
     if (lane == 0) {
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) record_timeout(abort);
   } else {
     // ---------------------------------------------------------------- epilogue
-    regs_down<80>();
+    regs_down<88>();
     const int row = (warp & 3) * 32 + lane;
     const uint32_t quad = (uint32_t)((warp & 3) * 32) << 16;
     const int pos = row / a.G, g = row - pos * a.G;
@@ -612,67 +612,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t icount[2] = {0, 0};
     bool ok = true;
 
-    // A warp's 32 rows leave through 4 KB of shared memory, 128 bytes of each at
-    // a time (32 columns of binary32 partials, 64 of 16 bits, 128 codes), so
-    // that whole sectors of a row are written together: 16-byte stores from the
-    // rows' own threads took 1.2 times as long over a short key side.
-    uint8_t* stage = smem + C::kOut + (warp & 3) * 32 * 128;
     const int kind = a.splits > 1 ? 2 : a.s_out ? 0 : 1;             // log2 of a value's bytes
-    auto out_row = [&](const Item& x, int l) -> int64_t {            // element offset, or -1
-      if (pos >= a.rows_l || l >= a.Lq) return -1;
+    // Where row (position l, this thread's head) starts, or null.
+    auto out_row = [&](const Item& x, int l) -> uint8_t* {
+      if (pos >= a.rows_l || l >= a.Lq) return nullptr;
       if (kind == 2)
-        return ((((int64_t)x.split * a.B + x.b) * a.Hkv + x.hk) * ((int64_t)a.Lq * a.G) + (int64_t)l * a.G + g) * DP;
-      return x.b * a.o_b + l * a.o_l + (int64_t)(x.hk * a.G + g) * a.o_h;
+        return reinterpret_cast<uint8_t*>(
+            a.part + ((((int64_t)x.split * a.B + x.b) * a.Hkv + x.hk) * ((int64_t)a.Lq * a.G) + (int64_t)l * a.G + g) * DP);
+      return static_cast<uint8_t*>(a.out) + ((x.b * a.o_b + l * a.o_l + (int64_t)(x.hk * a.G + g) * a.o_h) << kind);
     };
-    uint8_t* const out_base = static_cast<uint8_t*>(kind == 2 ? static_cast<void*>(a.part) : a.out);
-    // 16 columns (chunk c) of this thread's row; the store of the span follows
-    // when its 128 bytes (or the row) are complete.
-    auto put = [&](int64_t off, int c, const float (&v)[16]) {
-      const int span = 128 >> kind;                                  // columns of 128 bytes
-      const int u0 = (16 * c % span << kind) >> 4;                   // first 16-byte unit of the chunk
-      uint8_t* mine = stage + lane * 128;
-      auto unit = [&](int u, uint4 w) { *reinterpret_cast<uint4*>(mine + ((u ^ (lane & 7)) << 4)) = w; };
+    // 32 columns (chunk c) of this thread's row, straight from its registers:
+    // whole 32-byte sectors where the rows allow it.  The accumulator is free for the next
+    // item as soon as it is in registers, which is what a short key side waits
+    // for: through shared memory, with a warp's lanes on one row, the epilogue
+    // took 4 times as long.
+    auto put = [&](uint8_t* row_at, int c, const float (&v)[32]) {
+      if (!row_at) return;
+      if (kind == 2) {
+        float4* dst = reinterpret_cast<float4*>(row_at) + 8 * c;     // partial rows are DP wide
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        return;
+      }
+      if (32 * c >= a.D) return;
       if (kind == 0) {
         uint32_t w[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = cvt_e4m3x2(v[2 * k] * inv_s, v[2 * k + 1] * inv_s);
-        unit(u0, make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16)));
-      } else if (kind == 1) {
-        uint32_t w[8];
+        for (int k = 0; k < 8; ++k)
+          w[k] = cvt_e4m3x2(v[4 * k] * inv_s, v[4 * k + 1] * inv_s) | (cvt_e4m3x2(v[4 * k + 2] * inv_s, v[4 * k + 3] * inv_s) << 16);
+        if (a.wide) {
+          st_global_32(row_at + 32 * c, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+        } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = cvt16x2(kF16, v[2 * k], v[2 * k + 1]);
-        unit(u0, make_uint4(w[0], w[1], w[2], w[3]));
-        unit(u0 + 1, make_uint4(w[4], w[5], w[6], w[7]));
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          unit(u0 + k, make_uint4(__float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]), __float_as_uint(v[4 * k + 2]),
-                                  __float_as_uint(v[4 * k + 3])));
-      }
-      const int end = 16 * (c + 1);
-      if (end % span != 0 && end != DP) return;
-      __syncwarp();
-      const int d0 = (end - 1) / span * span;
-      const int width = kind == 2 ? DP : a.D;                        // partial rows are DP wide
-      if (kind == 0) {                                               // a row of codes is 8-byte aligned
-#pragma unroll 4
-        for (int k = 0; k < 16; ++k) {
-          const int row = 2 * k + (lane >> 4), u = lane & 15;
-          const int64_t o = __shfl_sync(0xFFFFFFFFu, off, row);
-          const uint2 w = *reinterpret_cast<const uint2*>(stage + row * 128 + ((u >> 1 ^ (row & 7)) << 4) + 8 * (u & 1));
-          if (o >= 0 && d0 + 8 * u < width) *reinterpret_cast<uint2*>(out_base + o + d0 + 8 * u) = w;
+          for (int k = 0; k < 4; ++k)
+            if (32 * c + 8 * k < a.D) *reinterpret_cast<uint2*>(row_at + 32 * c + 8 * k) = make_uint2(w[2 * k], w[2 * k + 1]);
         }
       } else {
-#pragma unroll 4
-        for (int k = 0; k < 8; ++k) {
-          const int row = 4 * k + (lane >> 3), u = lane & 7;
-          const int64_t o = __shfl_sync(0xFFFFFFFFu, off, row);
-          const uint4 w = *reinterpret_cast<const uint4*>(stage + row * 128 + ((u ^ (row & 7)) << 4));
-          if (o >= 0 && d0 + (16 >> kind) * u < width)
-            *reinterpret_cast<uint4*>(out_base + ((o + d0) << kind) + 16 * u) = w;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) w[k] = cvt16x2(kF16, v[16 * h + 2 * k], v[16 * h + 2 * k + 1]);
+          uint8_t* dst = row_at + 64 * c + 32 * h;
+          if (a.wide) {
+            if (32 * c + 16 * h < a.D) st_global_32(dst, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              if (32 * c + 16 * h + 8 * k < a.D)
+                *reinterpret_cast<uint4*>(dst + 16 * k) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+          }
         }
       }
-      __syncwarp();
     };
     auto put_lse = [&](const Item& x, int l, float m, float sum) {
       if (a.splits == 1 || pos >= a.rows_l || l >= a.Lq) return;
@@ -686,9 +677,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
           const int l = (2 * x.blk + i) * a.rows_l + pos;
+          uint8_t* row_at = out_row(x, l);
           if (x.n() == 0) {
-            float z[16] = {};
-            for (int c = 0; c < DP / 16; ++c) put(out_row(x, l), c, z);
+            const float z[32] = {};
+            for (int c = 0; c < DP / 32; ++c) put(row_at, c, z);
             put_lse(x, l, 0.0f, 0.0f);
             continue;
           }
@@ -702,30 +694,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float sum = sum_l[i * kRows + row];
           const float f = sum == 0.0f ? 0.0f : __frcp_rn(sum);
           put_lse(x, l, sum_m[i * kRows + row], sum);
-          const int64_t off = out_row(x, l);
           __syncwarp();   // together again for the TMEM loads
 #pragma unroll 1
-          for (int c = 0; c < DP / 16; ++c) {
-            uint32_t r[16];
-            tmem_ld_32x32b_x16(o_col(i) + quad + c * 16, r);
+          for (int c = 0; c < DP / 32; ++c) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(o_col(i) + quad + c * 32, r);
             tmem_ld_wait();
-            if (c == DP / 16 - 1) {
+            if (c == DP / 32 - 1) {
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(o_free(i));
             }
-            float v[16];
+            float v[32];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = f == 0.0f ? 0.0f : __uint_as_float(r[e]) * f;
-            put(off, c, v);
+            for (int e = 0; e < 32; ++e) v[e] = f == 0.0f ? 0.0f : __uint_as_float(r[e]) * f;
+            put(row_at, c, v);
+            __syncwarp();
           }
         }
       } else {
         const int l = x.blk * a.rows_l + pos;
+        uint8_t* row_at = out_row(x, l);
         const int n0 = slot_tiles(x.n(), 0), n1 = slot_tiles(x.n(), 1);
         if (n0 == 0) {
-          float z[16] = {};
-          for (int c = 0; c < DP / 16; ++c) put(out_row(x, l), c, z);
+          const float z[32] = {};
+          for (int c = 0; c < DP / 32; ++c) put(row_at, c, z);
           put_lse(x, l, 0.0f, 0.0f);
           continue;
         }
@@ -744,18 +737,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float l0 = sum_l[row], l1 = n1 > 0 ? sum_l[kRows + row] : 0.0f;
         const float sum = a0 * l0 + a1 * l1;
         put_lse(x, l, top, sum);
-        const int64_t off = out_row(x, l);
-        __syncwarp();   // together again for the TMEM loads
         const float f = sum == 0.0f ? 0.0f : __frcp_rn(sum);
         a0 *= f;
         a1 *= f;
+        __syncwarp();   // together again for the TMEM loads
 #pragma unroll 1
-        for (int c = 0; c < DP / 16; ++c) {
-          uint32_t r0[16], r1[16];
-          tmem_ld_32x32b_x16(o_col(0) + quad + c * 16, r0);
-          if (n1 > 0) tmem_ld_32x32b_x16(o_col(1) + quad + c * 16, r1);
-          tmem_ld_wait();
-          if (c == DP / 16 - 1) {
+        for (int c = 0; c < DP / 32; ++c) {
+          float v[32];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r0[16], r1[16];
+            tmem_ld_32x32b_x16(o_col(0) + quad + c * 32 + h * 16, r0);
+            if (n1 > 0) tmem_ld_32x32b_x16(o_col(1) + quad + c * 32 + h * 16, r1);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float y = f == 0.0f ? 0.0f : __uint_as_float(r0[e]) * a0;
+              if (n1 > 0 && f != 0.0f) y = fmaf(__uint_as_float(r1[e]), a1, y);
+              v[16 * h + e] = y;
+            }
+          }
+          if (c == DP / 32 - 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -763,13 +765,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (n1 > 0) mbar_arrive(o_free(1));
             }
           }
-          float v[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            v[e] = f == 0.0f ? 0.0f : __uint_as_float(r0[e]) * a0;
-            if (n1 > 0 && f != 0.0f) v[e] = fmaf(__uint_as_float(r1[e]), a1, v[e]);
-          }
-          put(off, c, v);
+          put(row_at, c, v);
+          __syncwarp();
         }
       }
     }
@@ -956,6 +953,12 @@ cudaError_t launch_cross_attention(const AttnProblem& p, int sms, cudaStream_t s
   a.o_b = p.os[0];
   a.o_l = p.os[1];
   a.o_h = p.os[2];
+  {
+    const int64_t bytes = p.s_out ? 1 : 2;
+    auto odd = [&](int64_t stride, int n) { return n > 1 && stride * bytes % 32 != 0; };
+    a.wide = reinterpret_cast<uintptr_t>(p.out) % 32 == 0 && p.D * bytes % 32 == 0 && !odd(a.o_b, p.B) &&
+             !odd(a.o_l, p.Lq) && !odd(a.o_h, p.Hq);
+  }
   a.part = p.ws;
   a.part_lse = p.ws + (int64_t)x.splits * p.B * p.Hq * p.Lq * x.DP;   // not used with one split
   a.q_bytes = (uint32_t)(x.G * x.rows_l * 128);

@@ -109,6 +109,14 @@ __device__ __forceinline__ float ld_f32(const float* p) {
   return v;
 }
 
+// One whole 32-byte sector from one thread (32-byte aligned).
+__device__ __forceinline__ void st_global_32(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e,
+                                             uint32_t f, uint32_t g, uint32_t h) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d),
+               "r"(e), "r"(f), "r"(g), "r"(h)
+               : "memory");
+}
+
 // One thread of a converged warp (the same one for the compiler to see: a loop
 // under this condition runs in one thread, and its operands stay uniform).
 __device__ __forceinline__ bool elect_one() {
