@@ -64,7 +64,7 @@ template <int DP>
 struct Cfg {
   static constexpr int kAtoms = DP / 64;
   static constexpr int kTile = kAtoms * kAtom;           // bytes of 128 rows of Q, K or V
-  static constexpr int kStages = DP == 128 ? 4 : 6;
+  static constexpr int kStages = DP == 128 ? 4 : 6;      // even: see the cleaning warp
   static constexpr int kQ = 0;
   static constexpr int kRing = kQ + 2 * kTile;
   static constexpr int kSum = kRing + kStages * kTile;   // l[2][128], m[2][128]
@@ -86,6 +86,7 @@ struct AttnArgs {
   int blocks;                 // query blocks per (sample, key head)
   int splits;                 // parts of the key axis
   int items;
+  uint64_t by_blocks, by_splits, by_hkv;   // 2^64 / d rounded up, 0 for d = 1
   int q_bmul, k_bmul, v_bmul; // 0 where the samples share one array
   uint32_t q_bytes;           // bytes of one Q atom's box
   float scale_log2;
@@ -199,20 +200,40 @@ __device__ __forceinline__ bool load_mask(const uint8_t* p) {
   return v != 0;
 }
 
+// n / d for n < 2^32, with by = 2^64 / d rounded up.
+__device__ __forceinline__ int quotient(int n, uint64_t by) {
+  return by ? (int)__umul64hi((uint64_t)(uint32_t)n, by) : n;
+}
+
+// The number of keys of item `it`'s sample, asked for an item ahead: its
+// latency (some 700 cycles) would stand between two items in every role.
 template <bool kLens>
-__device__ __forceinline__ Item decode(const AttnArgs& a, int it) {
+__device__ __forceinline__ int len_of(const AttnArgs& a, int it) {
+  if constexpr (kLens) {
+    if (it < a.items) return load_len(a.kv_len + quotient(quotient(quotient(it, a.by_blocks), a.by_splits), a.by_hkv));
+  }
+  return 0;
+}
+
+template <bool kLens>
+__device__ __forceinline__ Item decode(const AttnArgs& a, int it, int len) {
   Item x;
-  x.blk = it % a.blocks;
-  it /= a.blocks;
-  x.split = it % a.splits;
-  it /= a.splits;
-  x.hk = it % a.Hkv;
-  x.b = it / a.Hkv;
-  x.len = a.Lk;
-  if constexpr (kLens) x.len = min(max(load_len(a.kv_len + x.b), 0), a.Lk);
+  int q = quotient(it, a.by_blocks);
+  x.blk = it - q * a.blocks;
+  it = q;
+  q = quotient(it, a.by_splits);
+  x.split = it - q * a.splits;
+  it = q;
+  x.b = quotient(it, a.by_hkv);
+  x.hk = it - x.b * a.Hkv;
+  x.len = kLens ? min(max(len, 0), a.Lk) : a.Lk;
   const int tiles = (x.len + kKeys - 1) / kKeys;
-  x.t0 = (int)((int64_t)tiles * x.split / a.splits);
-  x.t1 = (int)((int64_t)tiles * (x.split + 1) / a.splits);
+  x.t0 = 0;
+  x.t1 = tiles;
+  if (a.splits > 1) {
+    x.t0 = quotient(tiles * x.split, a.by_splits);
+    x.t1 = quotient(tiles * (x.split + 1), a.by_splits);
+  }
   return x;
 }
 
@@ -331,8 +352,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_5d(sbase + C::kQ + i * C::kTile + at * kAtom, &maps.q, q_full(i), 64 * at, 0, l0, x.hk, x.b * a.q_bmul);
         return true;
       };
+      int len = len_of<kLens>(a, blockIdx.x);
       for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
-        const Item x = decode<kLens>(a, it);
+        const Item x = decode<kLens>(a, it, len);
+        len = len_of<kLens>(a, it + gridDim.x);
         if (x.n() == 0) continue;
         bool first = true;
         ok = load_q(x, 0);
@@ -377,17 +400,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t base = 0;                         // entries of the ring before this item
       uint32_t qcount = 0, pcount = 0, icount = 0;
       bool ok = true;
-      // Waits for entry e of the ring; returns its stage.  With limits the
-      // cleaning warp passes every stage first, K's too: a stage can then not
-      // be refilled before that warp has seen it.
-      auto take = [&](uint32_t e) {
+      // Waits for entry e of the ring; returns its stage.  With limits V goes by
+      // way of the cleaning warp.  So does K in the separate form, where a stage
+      // holds K and V in no fixed order: that warp then sees every filling of
+      // a stage before it can be replaced.  In the shared form V has the odd
+      // stages (S is even) and the cleaning warp waits for those alone.
+      auto take = [&](uint32_t e, bool is_v) {
         const int st = (int)(e % S);
-        ok = ok && mbar_wait(kClean ? clean_bar(st) : full_bar(st), (e / S) & 1, abort, kWaitLimitNs);
+        ok = ok && mbar_wait(kClean && (is_v || !kShared) ? clean_bar(st) : full_bar(st), (e / S) & 1, abort, kWaitLimitNs);
         tc_fence_after();
         return st;
       };
+      int len = len_of<kLens>(a, blockIdx.x);
       for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
-        const int n = decode<kLens>(a, it).n();
+        const int n = decode<kLens>(a, it, len).n();
+        len = len_of<kLens>(a, it + gridDim.x);
         if (n == 0) continue;
         if (slot_tiles(n, i) > 0) {
           ok = mbar_wait(q_full(kShared ? i : 0), qcount & 1, abort, kWaitLimitNs);
@@ -402,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // idles while both are in their softmax warps.
           if (kShared && (i == 1 || pcount > 0))
             ok = ok && mbar_wait(s_full(1 - i), (pcount - (1 - i)) & 1, abort, kWaitLimitNs);
-          int st = take(base + ek);
+          int st = take(base + ek, false);
           if (!ok) break;
           const uint64_t qd = sw128_kmajor_desc(sbase + C::kQ + (kShared ? i : 0) * C::kTile);
           const uint64_t kd = sw128_kmajor_desc(sbase + C::kRing + st * C::kTile);
@@ -415,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit(empty_bar(st));
           if (last) mma_commit(q_empty(kShared ? i : 0));
 
-          st = take(base + ev);
+          st = take(base + ev, true);
           if (first) ok = ok && mbar_wait(o_free(i), (icount++ & 1) ^ 1, abort, kWaitLimitNs);   // the epilogue has read O_i
           const uint64_t vd = sw128_mnmajor_desc(sbase + C::kRing + st * C::kTile);
 #pragma unroll
@@ -450,10 +477,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       int st = 0;
       uint32_t ph = 0;
       bool ok = true;
+      int len = len_of<kLens>(a, blockIdx.x);
       for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
-        const Item x = decode<kLens>(a, it);
+        const Item x = decode<kLens>(a, it, len);
+        len = len_of<kLens>(a, it + gridDim.x);
         ok = walk(x, [&](bool is_v, int tile) {
-          if (!mbar_wait_warp(full_bar(st), ph, abort, kWaitLimitNs)) return false;
+          const bool pass = kShared && !is_v;
+          if (!pass && !mbar_wait_warp(full_bar(st), ph, abort, kWaitLimitNs)) return false;
           if (is_v) {
             uint8_t* v = smem + C::kRing + st * C::kTile;
             bool wrote = false;
@@ -474,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (wrote) fence_proxy_async_smem();
             __syncwarp();
           }
-          if (lane == 0) mbar_arrive(clean_bar(st));
+          if (!pass && lane == 0) mbar_arrive(clean_bar(st));
           if (++st == S) {
             st = 0;
             ph ^= 1;
@@ -493,8 +523,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t quad = (uint32_t)((warp & 3) * 32) << 16;
     uint32_t scount = 0, icount = 0;
     bool ok = true;
+    int len = len_of<kLens>(a, blockIdx.x);
     for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
-      const Item x = decode<kLens>(a, it);
+      const Item x = decode<kLens>(a, it, len);
+      len = len_of<kLens>(a, it + gridDim.x);
       const int n = slot_tiles(x.n(), i);
       if (n == 0) continue;
       float m = -INFINITY, l = 0.0f;             // m in powers of two: scaled scores
@@ -621,49 +653,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             a.part + ((((int64_t)x.split * a.B + x.b) * a.Hkv + x.hk) * ((int64_t)a.Lq * a.G) + (int64_t)l * a.G + g) * DP);
       return static_cast<uint8_t*>(a.out) + ((x.b * a.o_b + l * a.o_l + (int64_t)(x.hk * a.G + g) * a.o_h) << kind);
     };
-    // 32 columns (chunk c) of this thread's row, straight from its registers:
-    // whole 32-byte sectors where the rows allow it.  The accumulator is free for the next
-    // item as soon as it is in registers, which is what a short key side waits
-    // for: through shared memory, with a warp's lanes on one row, the epilogue
-    // took 4 times as long.
-    auto put = [&](uint8_t* row_at, int c, const float (&v)[32]) {
-      if (!row_at) return;
-      if (kind == 2) {
-        float4* dst = reinterpret_cast<float4*>(row_at) + 8 * c;     // partial rows are DP wide
+    // Packs 32 scaled columns: 8 words of codes or 16 of 16-bit values.
+    auto pack = [&](const uint32_t (&r)[32], float f, uint32_t* w) {
+      const F2 ff = splat(kind == 0 ? f * inv_s : f);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-        return;
+      for (int k = 0; k < 16; ++k) {
+        const F2 v = mul2(F2{__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])}, ff);
+        if (kind == 0) {
+          const uint32_t c = cvt_e4m3x2(v.x, v.y);
+          w[k >> 1] = k & 1 ? w[k >> 1] | (c << 16) : c;
+        } else {
+          w[k] = cvt16x2(kF16, v.x, v.y);
+        }
       }
-      if (32 * c >= a.D) return;
-      if (kind == 0) {
-        uint32_t w[8];
+    };
+    // A thread's packed row (or 32 columns of it): whole 32-byte sectors where
+    // the rows allow it.
+    auto put_words = [&](uint8_t* at, int words, int bytes, const uint32_t* w) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          w[k] = cvt_e4m3x2(v[4 * k] * inv_s, v[4 * k + 1] * inv_s) | (cvt_e4m3x2(v[4 * k + 2] * inv_s, v[4 * k + 3] * inv_s) << 16);
+      for (int k = 0; k < words; k += 8) {
         if (a.wide) {
-          st_global_32(row_at + 32 * c, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+          if (4 * k < bytes) st_global_32(at + 4 * k, w[k], w[k + 1], w[k + 2], w[k + 3], w[k + 4], w[k + 5], w[k + 6], w[k + 7]);
         } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (32 * c + 8 * k < a.D) *reinterpret_cast<uint2*>(row_at + 32 * c + 8 * k) = make_uint2(w[2 * k], w[2 * k + 1]);
-        }
-      } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) w[k] = cvt16x2(kF16, v[16 * h + 2 * k], v[16 * h + 2 * k + 1]);
-          uint8_t* dst = row_at + 64 * c + 32 * h;
-          if (a.wide) {
-            if (32 * c + 16 * h < a.D) st_global_32(dst, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              if (32 * c + 16 * h + 8 * k < a.D)
-                *reinterpret_cast<uint4*>(dst + 16 * k) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-          }
+          for (int h = 0; h < 8; h += 2)   // rows of codes are 8-byte aligned
+            if (4 * (k + h) < bytes) *reinterpret_cast<uint2*>(at + 4 * (k + h)) = make_uint2(w[k + h], w[k + h + 1]);
         }
       }
+    };
+    auto put_zeros = [&](uint8_t* row_at) {
+      if (!row_at) return;
+      const int bytes = kind == 2 ? DP * 4 : a.D << kind;
+      for (int k = 0; k < bytes; k += 8) *reinterpret_cast<uint2*>(row_at + k) = make_uint2(0, 0);
     };
     auto put_lse = [&](const Item& x, int l, float m, float sum) {
       if (a.splits == 1 || pos >= a.rows_l || l >= a.Lq) return;
@@ -671,16 +692,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       a.part_lse[at] = sum == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) + log2f(sum);
     };
 
+    int len = len_of<kLens>(a, blockIdx.x);
     for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
-      const Item x = decode<kLens>(a, it);
+      const Item x = decode<kLens>(a, it, len);
+      len = len_of<kLens>(a, it + gridDim.x);
       if constexpr (kShared) {
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
           const int l = (2 * x.blk + i) * a.rows_l + pos;
           uint8_t* row_at = out_row(x, l);
           if (x.n() == 0) {
-            const float z[32] = {};
-            for (int c = 0; c < DP / 32; ++c) put(row_at, c, z);
+            put_zeros(row_at);
             put_lse(x, l, 0.0f, 0.0f);
             continue;
           }
@@ -695,30 +717,60 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float f = sum == 0.0f ? 0.0f : __frcp_rn(sum);
           put_lse(x, l, sum_m[i * kRows + row], sum);
           __syncwarp();   // together again for the TMEM loads
-#pragma unroll 1
-          for (int c = 0; c < DP / 32; ++c) {
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(o_col(i) + quad + c * 32, r);
-            tmem_ld_wait();
-            if (c == DP / 32 - 1) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(o_free(i));
-            }
-            float v[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = f == 0.0f ? 0.0f : __uint_as_float(r[e]) * f;
-            put(row_at, c, v);
+          // The accumulator goes to registers, packed, before anything is
+          // stored: the next item's first product waits for it.
+          auto free_o = [&] {
+            tc_fence_before();
             __syncwarp();
+            if (lane == 0) mbar_arrive(o_free(i));
+          };
+          if (kind == 2) {
+#pragma unroll 1
+            for (int c = 0; c < DP / 32; ++c) {
+              uint32_t r[32];
+              tmem_ld_32x32b_x32(o_col(i) + quad + c * 32, r);
+              tmem_ld_wait_for(r);
+              if (c == DP / 32 - 1) free_o();
+              if (row_at) {
+                float4* dst = reinterpret_cast<float4*>(row_at) + 8 * c;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  dst[k] = make_float4(__uint_as_float(r[4 * k]) * f, __uint_as_float(r[4 * k + 1]) * f,
+                                       __uint_as_float(r[4 * k + 2]) * f, __uint_as_float(r[4 * k + 3]) * f);
+              }
+              __syncwarp();
+            }
+          } else if (kind == 0) {
+            uint32_t w[DP / 4];
+#pragma unroll
+            for (int c = 0; c < DP / 32; ++c) {
+              uint32_t r[32];
+              tmem_ld_32x32b_x32(o_col(i) + quad + c * 32, r);
+              tmem_ld_wait_for(r);
+              if (c == DP / 32 - 1) free_o();
+              pack(r, f, w + 8 * c);
+            }
+            if (row_at) put_words(row_at, DP / 4, a.D, w);
+          } else {
+            uint32_t w[DP / 2];
+#pragma unroll
+            for (int c = 0; c < DP / 32; ++c) {
+              uint32_t r[32];
+              tmem_ld_32x32b_x32(o_col(i) + quad + c * 32, r);
+              tmem_ld_wait_for(r);
+              if (c == DP / 32 - 1) free_o();
+              pack(r, f, w + 16 * c);
+            }
+            if (row_at) put_words(row_at, DP / 2, 2 * a.D, w);
           }
+          __syncwarp();
         }
       } else {
         const int l = x.blk * a.rows_l + pos;
         uint8_t* row_at = out_row(x, l);
         const int n0 = slot_tiles(x.n(), 0), n1 = slot_tiles(x.n(), 1);
         if (n0 == 0) {
-          const float z[32] = {};
-          for (int c = 0; c < DP / 32; ++c) put(row_at, c, z);
+          put_zeros(row_at);
           put_lse(x, l, 0.0f, 0.0f);
           continue;
         }
@@ -743,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();   // together again for the TMEM loads
 #pragma unroll 1
         for (int c = 0; c < DP / 32; ++c) {
-          float v[32];
+          uint32_t r[32];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t r0[16], r1[16];
@@ -752,9 +804,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              float y = f == 0.0f ? 0.0f : __uint_as_float(r0[e]) * a0;
-              if (n1 > 0 && f != 0.0f) y = fmaf(__uint_as_float(r1[e]), a1, y);
-              v[16 * h + e] = y;
+              float y = __uint_as_float(r0[e]) * a0;
+              if (n1 > 0) y = fmaf(__uint_as_float(r1[e]), a1, y);
+              r[16 * h + e] = __float_as_uint(y);
             }
           }
           if (c == DP / 32 - 1) {
@@ -765,7 +817,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (n1 > 0) mbar_arrive(o_free(1));
             }
           }
-          put(row_at, c, v);
+          if (row_at && kind == 2) {
+            uint4* dst = reinterpret_cast<uint4*>(row_at) + 8 * c;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) dst[k] = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+          } else if (row_at && kind == 0) {
+            uint32_t w[8];
+            pack(r, 1.0f, w);
+            put_words(row_at + 32 * c, 8, a.D - 32 * c, w);
+          } else if (row_at) {
+            uint32_t w[16];
+            pack(r, 1.0f, w);
+            put_words(row_at + 64 * c, 16, 2 * a.D - 64 * c, w);
+          }
           __syncwarp();
         }
       }
@@ -944,6 +1008,10 @@ cudaError_t launch_cross_attention(const AttnProblem& p, int sms, cudaStream_t s
   a.blocks = x.blocks;
   a.splits = x.splits;
   a.items = (int)x.items;
+  auto by = [](int d) { return d == 1 ? 0ull : ~0ull / (uint64_t)d + 1; };
+  a.by_blocks = by(x.blocks);
+  a.by_splits = by(x.splits);
+  a.by_hkv = by(p.Hkv);
   a.scale_log2 = p.scale * 1.4426950408889634f;
   a.kv_len = p.kv_len;
   a.kv_mask = p.kv_mask;
