@@ -458,7 +458,8 @@ w8_status fp8_linear_w8a8_pertoken(const uint8_t* qx, int64_t M, int64_t K, cons
  * stride of q, k or v may be 0 where all samples share one array. */
 typedef struct {
   int64_t B, Lq, Lk;     /* samples, queries, keys; any may be 0 */
-  int64_t Hq, Hkv, D;    /* heads; Hq a multiple of Hkv, at most 128 times it; 8 <= D <= 128, D % 8 == 0 */
+  int64_t Hq, Hkv, D;    /* heads; Hq a multiple of Hkv, at most 128 times it; 8 <= D <= 128, D % 8 == 0;
+                          * B * Hq * Lq at most 2^30 */
   int64_t q_stride[3], k_stride[3], v_stride[3], o_stride[3];
   int64_t mask_stride;   /* bytes between the samples of kv_mask (0: one for all) */
   int32_t dtype;         /* of q, k, v: W8_DTYPE_BF16 or W8_DTYPE_F16 */

@@ -686,9 +686,9 @@ static w8_status check_attention(const char* fn, const w8_attention_desc* d, w8:
   if (d->Hq < 1 || d->Hkv < 1 || d->Hq % d->Hkv || d->Hq / d->Hkv > 128)
     return fail(W8_ERR_SHAPE, "%s: Hq=%lld Hkv=%lld (need Hq a multiple of Hkv, at most 128 times it)", fn,
                 (long long)d->Hq, (long long)d->Hkv);
-  // work items and joined rows are counted in 32 bits
+  // work items are counted in 32 bits
   const double rows = (double)d->B * (double)d->Hq * (double)d->Lq;
-  if (rows > (double)(1ll << 32)) return fail(W8_ERR_SHAPE, "%s: B * Hq * Lq = %.0f is above 2^32", fn, rows);
+  if (rows > (double)(1ll << 30)) return fail(W8_ERR_SHAPE, "%s: B * Hq * Lq = %.0f is above 2^30", fn, rows);
   if (!std::isfinite(d->scale) || !(d->scale > 0.0f)) return fail(W8_ERR_PARAM, "%s: scale=%g", fn, (double)d->scale);
   const int64_t* strides[4] = {d->q_stride, d->k_stride, d->v_stride, d->o_stride};
   for (int t = 0; t < 4; ++t) {

@@ -22,8 +22,9 @@
 //   O_i += P_i V_j      P_i from TMEM, V_j from shared memory (MN-major)
 // TMEM: S_0, S_1 (128 columns each), O_0, O_1.  With at most 128 rows
 // the two slots take the even and the odd key tiles of the same rows, and the
-// epilogue joins them; few items are further split along the keys into partial
-// results that a second kernel joins.
+// epilogue joins them.  Where whole items would leave CTAs without work or with
+// uneven work, items are cut along the keys into partial results that a second
+// kernel joins.
 //
 // Roles: warps 0-3 and 4-7 softmax of slot 0 / 1 (a thread per row, so row
 // maxima and sums need no shuffles), 8-11 epilogue, 12 and 15 MMA issue of slot 0 / 1,
@@ -60,6 +61,10 @@ constexpr int kAtom = 128 * 128;                  // 128 rows of one 128-byte sw
 // (m is whatever the sums used), and most tiles touch O_i not at all.
 constexpr float kLazyMax = 8.0f;
 
+// Samples with lengths of their own whose items may be cut (their tile counts
+// are kept in shared memory).
+constexpr int kMaxCutSamples = 128;
+
 template <int DP>
 struct Cfg {
   static constexpr int kAtoms = DP / 64;
@@ -68,7 +73,8 @@ struct Cfg {
   static constexpr int kQ = 0;
   static constexpr int kRing = kQ + 2 * kTile;
   static constexpr int kSum = kRing + kStages * kTile;   // l[2][128], m[2][128]
-  static constexpr int kBar = kSum + 4 * kRows * 4;
+  static constexpr int kTab = kSum + 4 * kRows * 4;      // first tile and tiles per item of each sample
+  static constexpr int kBar = kTab + (2 * kMaxCutSamples + 2) * 4;
   // full[S], empty[S], clean[S], q_full[2], q_empty[2], s_full[2], p_full[2],
   // o_full[2], l_full[2], o_free[2], p_half[2], drain[2]
   static constexpr int kNumBars = 3 * kStages + 18;
@@ -84,9 +90,10 @@ struct AttnArgs {
   int B, Lq, Lk, Hkv, G, D;
   int rows_l;                 // query positions per slot: 128 / G
   int blocks;                 // query blocks per (sample, key head)
-  int splits;                 // parts of the key axis
   int items;
-  uint64_t by_blocks, by_splits, by_hkv;   // 2^64 / d rounded up, 0 for d = 1
+  uint64_t by_blocks, by_hkv; // 2^64 / d rounded up, 0 for d = 1
+  int cut;                    // CTAs share out tiles, not items
+  int groups;                 // entries of the tile table: samples with lengths of their own, else 1
   int q_bmul, k_bmul, v_bmul; // 0 where the samples share one array
   uint32_t q_bytes;           // bytes of one Q atom's box
   float scale_log2;
@@ -97,8 +104,9 @@ struct AttnArgs {
   void* out;
   int64_t o_b, o_l, o_h;      // element strides of the output
   int wide;                   // output rows are 32-byte aligned and whole multiples of 32 bytes
-  float* part;                // splits > 1: normalised partial outputs, then their log2 sums
-  float* part_lse;
+  float* part;                // cut: two partial results of each CTA, normalised
+  float* part_lse;            // and the log2 of their sums
+  uint32_t* tab;              // and the tile table, for the joining kernel
 };
 
 struct AttnMaps {
@@ -177,12 +185,13 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
   return d;
 }
 
-// One work item: a block of query rows of one (sample, key head), and the key
-// tiles [t0, t1) of one split.
+// One unit of work: a block of query rows of one (sample, key head), and its
+// key tiles [t0, t1).
 struct Item {
-  int b, hk, blk, split;
+  int b, hk, blk;
   int len;        // keys that may count
   int t0, t1;
+  int part;       // the partial result it writes, or -1: its output rows
   __device__ __forceinline__ int n() const { return t1 - t0; }
 };
 
@@ -200,42 +209,75 @@ __device__ __forceinline__ bool load_mask(const uint8_t* p) {
   return v != 0;
 }
 
-// n / d for n < 2^32, with by = 2^64 / d rounded up.
+// n / d for n < 2^32 (d from the host), with by = 2^64 / d rounded up.
 __device__ __forceinline__ int quotient(int n, uint64_t by) {
   return by ? (int)__umul64hi((uint64_t)(uint32_t)n, by) : n;
 }
 
-// The number of keys of item `it`'s sample, asked for an item ahead: its
-// latency (some 700 cycles) would stand between two items in every role.
+// A CTA's units, in the order in which each of its roles goes through them.
+//
+// Whole items: CTA c takes items c, c + CTAs, ...  Cut items: all key tiles of
+// all items stand in one row, of which CTA c takes its even share, so that no
+// CTA waits for another one's longer or additional item: it begins and
+// ends inside an item, as a rule, and writes partial results for those two.
 template <bool kLens>
-__device__ __forceinline__ int len_of(const AttnArgs& a, int it) {
-  if constexpr (kLens) {
-    if (it < a.items) return load_len(a.kv_len + quotient(quotient(quotient(it, a.by_blocks), a.by_splits), a.by_hkv));
-  }
-  return 0;
-}
+struct Units {
+  const AttnArgs& a;
+  const uint32_t* tab;   // cut: first tile of each table entry (groups + 1), then its items' tiles
+  uint32_t cur;          // the next item, or cut: the next tile
+  int entry = 0;         // cut: its table entry
+  int raw = 0;           // whole items with lengths: the next item's
 
-template <bool kLens>
-__device__ __forceinline__ Item decode(const AttnArgs& a, int it, int len) {
-  Item x;
-  int q = quotient(it, a.by_blocks);
-  x.blk = it - q * a.blocks;
-  it = q;
-  q = quotient(it, a.by_splits);
-  x.split = it - q * a.splits;
-  it = q;
-  x.b = quotient(it, a.by_hkv);
-  x.hk = it - x.b * a.Hkv;
-  x.len = kLens ? min(max(len, 0), a.Lk) : a.Lk;
-  const int tiles = (x.len + kKeys - 1) / kKeys;
-  x.t0 = 0;
-  x.t1 = tiles;
-  if (a.splits > 1) {
-    x.t0 = quotient(tiles * x.split, a.by_splits);
-    x.t1 = quotient(tiles * (x.split + 1), a.by_splits);
+  __device__ __forceinline__ Units(const AttnArgs& args, const uint32_t* table) : a(args), tab(table) {
+    cur = a.cut ? begin(blockIdx.x) : blockIdx.x;
+    if (!a.cut) ask();
   }
-  return x;
-}
+  __device__ __forceinline__ uint32_t begin(uint32_t cta) const {
+    return (uint32_t)((uint64_t)tab[a.groups] * cta / gridDim.x);
+  }
+  // The number of keys of the next item's sample, asked for an item ahead: its
+  // latency (some 700 cycles) would stand between two items in every role.
+  __device__ __forceinline__ void ask() {
+    if constexpr (kLens) {
+      if (cur < (uint32_t)a.items) raw = load_len(a.kv_len + quotient(quotient((int)cur, a.by_blocks), a.by_hkv));
+    }
+  }
+  __device__ __forceinline__ void place(Item& x, int item) const {
+    const int q = quotient(item, a.by_blocks);
+    x.blk = item - q * a.blocks;
+    x.b = quotient(q, a.by_hkv);
+    x.hk = q - x.b * a.Hkv;
+  }
+  __device__ __forceinline__ bool next(Item& x) {
+    x.part = -1;
+    if (!a.cut) {
+      if (cur >= (uint32_t)a.items) return false;
+      place(x, (int)cur);
+      x.len = kLens ? min(max(raw, 0), a.Lk) : a.Lk;
+      x.t0 = 0;
+      x.t1 = (x.len + kKeys - 1) / kKeys;
+      cur += gridDim.x;
+      ask();
+      return true;
+    }
+    const uint32_t end = begin(blockIdx.x + 1);
+    if (cur >= end) return false;
+    while (cur >= tab[entry + 1]) ++entry;
+    const uint32_t tiles = tab[a.groups + 1 + entry];
+    const uint32_t at = cur - tab[entry], item = at / tiles;
+    place(x, (int)item);
+    x.len = a.Lk;
+    if (kLens) {   // a table entry is a sample, and its items are counted from 0
+      x.b = entry;
+      x.len = min(max(load_len(a.kv_len + entry), 0), a.Lk);
+    }
+    x.t0 = (int)(at - item * tiles);
+    x.t1 = (int)min(tiles, (uint32_t)x.t0 + (end - cur));
+    if (x.n() < (int)tiles) x.part = 2 * blockIdx.x + (cur == begin(blockIdx.x) ? 0 : 1);
+    cur += (uint32_t)x.n();
+    return true;
+  }
+};
 
 __device__ __forceinline__ void record_timeout(volatile int* abort) {
   *abort = 1;
@@ -313,24 +355,58 @@ __global__ void __launch_bounds__(kThreads, 1)
   const auto s_col = [&](int i) { return tmem + (uint32_t)(i * kKeys); };
   const auto o_col = [&](int i) { return tmem + 256u + (uint32_t)(i * DP); };
   griddep_wait();   // from here on what earlier kernels wrote may be read
+  uint32_t* tab = reinterpret_cast<uint32_t*>(smem + C::kTab);
+  if (a.cut) {
+    // Tiles of each sample's items, and where they begin in the row of all tiles.
+    const int per = a.Hkv * a.blocks;
+    if constexpr (kLens) {
+      for (int b = threadIdx.x; b < a.groups; b += kThreads)
+        tab[a.groups + 1 + b] = (uint32_t)(min(max(load_len(a.kv_len + b), 0), a.Lk) + kKeys - 1) / kKeys;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        uint32_t sum = 0;
+        for (int b = 0; b < a.groups; ++b) {
+          tab[b] = sum;
+          sum += tab[a.groups + 1 + b] * (uint32_t)per;
+        }
+        tab[a.groups] = sum;
+      }
+    } else if (threadIdx.x == 0) {
+      tab[2] = (uint32_t)(a.Lk + kKeys - 1) / kKeys;
+      tab[0] = 0;
+      tab[1] = tab[2] * (uint32_t)a.items;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0)
+      for (int k = threadIdx.x; k < 2 * a.groups + 1; k += kThreads) a.tab[k] = tab[k];
+  }
 
   // Tiles that slot i works on in an item of n tiles.
   const auto slot_tiles = [](int n, int i) { return kShared ? n : (n + 1 - i) / 2; };
 
-  // The order in which K and V tiles pass through the ring, which the loader,
-  // the cleaner and the MMA issue all follow:
+  // The stages are one ring in the shared form, which both slots go through
+  // tile by tile (K and V in turn), and a ring for each slot in the separate form.  A
+  // waiter then sees every filling of its stages: waiting by parity for a
+  // filling whose predecessor, another slot's, is still to come would not wait.
+  constexpr int R = kShared ? S : S / 2;                              // stages of a ring
+  const auto stage_of = [](int i, uint32_t e) { return (kShared ? 0 : i * R) + (int)(e % R); };
+  const auto phase_of = [](uint32_t e) { return (e / R) & 1; };
+
+  // The order in which K and V tiles are loaded and cleared:
   //   shared:   K0 V0 K1 V1 ...
-  //   separate: K(0) K(1) | V(0) K(2) V(1) K(3) | ...   (tiles of the item)
-  const auto walk = [&](const Item& x, auto&& f) {
+  //   separate: K0 K1 V0 V1 K2 K3 V2 V3 ...   (slots 0 and 1 in turn)
+  const auto walk = [&](const Item& x, auto&& f) {   // f(V?, ring, tile)
     const int n = x.n();
     if constexpr (kShared) {
       for (int j = 0; j < n; ++j)
-        if (!f(false, x.t0 + j) || !f(true, x.t0 + j)) return false;
+        if (!f(false, 0, x.t0 + j) || !f(true, 0, x.t0 + j)) return false;
     } else {
-      for (int j = 0; j < 2 && j < n; ++j)
-        if (!f(false, x.t0 + j)) return false;
-      for (int j = 0; j < n; ++j)
-        if (!f(true, x.t0 + j) || (j + 2 < n && !f(false, x.t0 + j + 2))) return false;
+      for (int j = 0; j < n; j += 2) {
+        const bool two = j + 1 < n;
+        if (!f(false, 0, x.t0 + j) || (two && !f(false, 1, x.t0 + j + 1)) || !f(true, 0, x.t0 + j) ||
+            (two && !f(true, 1, x.t0 + j + 1)))
+          return false;
+      }
     }
     return true;
   };
@@ -340,8 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 13) {
     // ---------------------------------------------------------------- loads
     if (lane == 0) {
-      int st = 0;
-      uint32_t ph = 0, issued = 0, qcount[2] = {0, 0};
+      uint32_t filled[2] = {0, 0}, qcount[2] = {0, 0};
       bool ok = true;
       auto load_q = [&](const Item& x, int i) {
         if (!mbar_wait(q_empty(i), (qcount[i] & 1) ^ 1, abort, kWaitLimitNs)) return false;
@@ -352,24 +427,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_5d(sbase + C::kQ + i * C::kTile + at * kAtom, &maps.q, q_full(i), 64 * at, 0, l0, x.hk, x.b * a.q_bmul);
         return true;
       };
-      int len = len_of<kLens>(a, blockIdx.x);
-      for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
-        const Item x = decode<kLens>(a, it, len);
-        len = len_of<kLens>(a, it + gridDim.x);
+      Units<kLens> units(a, tab);
+      Item x;
+      while (ok && units.next(x)) {
         if (x.n() == 0) continue;
         bool first = true;
         ok = load_q(x, 0);
-        ok = ok && walk(x, [&](bool is_v, int tile) {
-          if (!mbar_wait(empty_bar(st), ph ^ 1, abort, kWaitLimitNs)) return false;
+        ok = ok && walk(x, [&](bool is_v, int ring, int tile) {
+          const uint32_t e = ring ? filled[1]++ : filled[0]++;
+          const int st = stage_of(ring, e);
+          if (!mbar_wait(empty_bar(st), phase_of(e) ^ 1, abort, kWaitLimitNs)) {
+            --filled[ring];
+            return false;
+          }
           mbar_arrive_expect_tx(full_bar(st), C::kTile);
           for (int at = 0; at < C::kAtoms; ++at)
             tma_load_4d(sbase + C::kRing + st * C::kTile + at * kAtom, is_v ? &maps.v : &maps.k, full_bar(st), 64 * at,
                         x.hk, tile * kKeys, x.b * (is_v ? a.v_bmul : a.k_bmul));
-          ++issued;
-          if (++st == S) {
-            st = 0;
-            ph ^= 1;
-          }
           if (kShared && first) {
             first = false;
             return load_q(x, 1);
@@ -380,10 +454,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) record_timeout(abort);
       // Every copy must have landed before the block ends.
       volatile int never = 0;
-      for (int j = 0; j < S && (uint32_t)j < issued; ++j) {
-        const uint32_t l = issued - 1 - j;
-        if (!mbar_wait(full_bar((int)(l % S)), (l / S) & 1, &never, kWaitLimitNs)) atomicOr(&g_attn_err, kErrTimeout);
-      }
+      for (int i = 0; i < (kShared ? 1 : 2); ++i)
+        for (uint32_t j = 1; j <= R && j <= filled[i]; ++j) {
+          const uint32_t e = filled[i] - j;
+          if (!mbar_wait(full_bar(stage_of(i, e)), phase_of(e), &never, kWaitLimitNs)) atomicOr(&g_attn_err, kErrTimeout);
+        }
       for (int i = 0; i < 2; ++i)
         if (qcount[i] > 0 && !mbar_wait(q_full(i), (qcount[i] - 1) & 1, &never, kWaitLimitNs))
           atomicOr(&g_attn_err, kErrTimeout);
@@ -397,39 +472,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     // so is the product of tile j.
     if (elect_one()) {
       const int i = warp == 12 ? 0 : 1;
-      uint32_t base = 0;                         // entries of the ring before this item
+      uint32_t entry = 0;                        // of this slot's ring
       uint32_t qcount = 0, pcount = 0, icount = 0;
       bool ok = true;
-      // Waits for entry e of the ring; returns its stage.  With limits V goes by
+      // Waits for the ring's next entry; returns its stage.  With limits V goes by
       // way of the cleaning warp.  So does K in the separate form, where a stage
       // holds K and V in no fixed order: that warp then sees every filling of
       // a stage before it can be replaced.  In the shared form V has the odd
       // stages (S is even) and the cleaning warp waits for those alone.
-      auto take = [&](uint32_t e, bool is_v) {
-        const int st = (int)(e % S);
-        ok = ok && mbar_wait(kClean && (is_v || !kShared) ? clean_bar(st) : full_bar(st), (e / S) & 1, abort, kWaitLimitNs);
+      auto take = [&](bool is_v) {
+        const uint32_t e = entry++;
+        const int st = stage_of(i, e);
+        ok = ok && mbar_wait(kClean && (is_v || !kShared) ? clean_bar(st) : full_bar(st), phase_of(e), abort, kWaitLimitNs);
         tc_fence_after();
         return st;
       };
-      int len = len_of<kLens>(a, blockIdx.x);
-      for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
-        const int n = decode<kLens>(a, it, len).n();
-        len = len_of<kLens>(a, it + gridDim.x);
+      Units<kLens> units(a, tab);
+      Item x;
+      while (ok && units.next(x)) {
+        const int n = x.n();
         if (n == 0) continue;
-        if (slot_tiles(n, i) > 0) {
-          ok = mbar_wait(q_full(kShared ? i : 0), qcount & 1, abort, kWaitLimitNs);
-          tc_fence_after();
-        }
+        // also by a slot without a tile: its word on Q below belongs to this Q
+        ok = mbar_wait(q_full(kShared ? i : 0), qcount & 1, abort, kWaitLimitNs);
+        if (!ok) break;
+        tc_fence_after();
         for (int j = kShared ? 0 : i; ok && j < n; j += kShared ? 1 : 2) {
           const bool first = j == (kShared ? 0 : i), last = j + (kShared ? 1 : 2) >= n;
-          // where `walk` puts K and V of tile j
-          const uint32_t ek = kShared ? 2 * j : j < 2 ? j : 2 * j - 1, ev = kShared ? 2 * j + 1 : j == n - 1 ? 2 * n - 1 : 2 * j + 2;
           // The slots take turns: a slot's scores are started when the other's
           // are complete.  Left alone the two fall into step, and the tensor core
           // idles while both are in their softmax warps.
           if (kShared && (i == 1 || pcount > 0))
             ok = ok && mbar_wait(s_full(1 - i), (pcount - (1 - i)) & 1, abort, kWaitLimitNs);
-          int st = take(base + ek, false);
+          int st = take(false);
           if (!ok) break;
           const uint64_t qd = sw128_kmajor_desc(sbase + C::kQ + (kShared ? i : 0) * C::kTile);
           const uint64_t kd = sw128_kmajor_desc(sbase + C::kRing + st * C::kTile);
@@ -442,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit(empty_bar(st));
           if (last) mma_commit(q_empty(kShared ? i : 0));
 
-          st = take(base + ev, true);
+          st = take(true);
           if (first) ok = ok && mbar_wait(o_free(i), (icount++ & 1) ^ 1, abort, kWaitLimitNs);   // the epilogue has read O_i
           const uint64_t vd = sw128_mnmajor_desc(sbase + C::kRing + st * C::kTile);
 #pragma unroll
@@ -459,8 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit(empty_bar(st));
           if (last) mma_commit(o_full(i));
         }
-        if (!kShared && i == 1 && n == 1) mma_commit(q_empty(0));   // no tile of this item: its word on Q all the same
-        base += 2 * (uint32_t)n;
+        if (!kShared && i == 1 && n == 1) mma_commit(q_empty(0));   // no tile of its own
         ++qcount;
       }
       if (!ok) record_timeout(abort);
@@ -474,16 +547,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Keys that do not count have P = 0, but their V may be anything, NaN and
     // infinities included: those rows are cleared before the product.
     if constexpr (kClean) {
-      int st = 0;
-      uint32_t ph = 0;
+      uint32_t seen[2] = {0, 0};
       bool ok = true;
-      int len = len_of<kLens>(a, blockIdx.x);
-      for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
-        const Item x = decode<kLens>(a, it, len);
-        len = len_of<kLens>(a, it + gridDim.x);
-        ok = walk(x, [&](bool is_v, int tile) {
+      Units<kLens> units(a, tab);
+      Item x;
+      while (ok && units.next(x)) {
+        ok = walk(x, [&](bool is_v, int ring, int tile) {
+          const uint32_t e = ring ? seen[1]++ : seen[0]++;
+          const int st = stage_of(ring, e);
           const bool pass = kShared && !is_v;
-          if (!pass && !mbar_wait_warp(full_bar(st), ph, abort, kWaitLimitNs)) return false;
+          if (!pass && !mbar_wait_warp(full_bar(st), phase_of(e), abort, kWaitLimitNs)) return false;
           if (is_v) {
             uint8_t* v = smem + C::kRing + st * C::kTile;
             bool wrote = false;
@@ -505,10 +578,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
           if (!pass && lane == 0) mbar_arrive(clean_bar(st));
-          if (++st == S) {
-            st = 0;
-            ph ^= 1;
-          }
           return true;
         });
       }
@@ -523,10 +592,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t quad = (uint32_t)((warp & 3) * 32) << 16;
     uint32_t scount = 0, icount = 0;
     bool ok = true;
-    int len = len_of<kLens>(a, blockIdx.x);
-    for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
-      const Item x = decode<kLens>(a, it, len);
-      len = len_of<kLens>(a, it + gridDim.x);
+    Units<kLens> units(a, tab);
+    Item x;
+    while (ok && units.next(x)) {
       const int n = slot_tiles(x.n(), i);
       if (n == 0) continue;
       float m = -INFINITY, l = 0.0f;             // m in powers of two: scaled scores
@@ -644,13 +712,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t icount[2] = {0, 0};
     bool ok = true;
 
-    const int kind = a.splits > 1 ? 2 : a.s_out ? 0 : 1;             // log2 of a value's bytes
-    // Where row (position l, this thread's head) starts, or null.
-    auto out_row = [&](const Item& x, int l) -> uint8_t* {
+    const int out_kind = a.s_out ? 0 : 1;      // log2 of a value's bytes
+    int kind = out_kind;                       // 2 in a unit that writes a partial result
+    constexpr int kUnitRows = kShared ? 2 * kRows : kRows;
+    // Where this thread's row (position l, row r of the unit) starts, or null.
+    auto out_row = [&](const Item& x, int l, int r) -> uint8_t* {
       if (pos >= a.rows_l || l >= a.Lq) return nullptr;
-      if (kind == 2)
-        return reinterpret_cast<uint8_t*>(
-            a.part + ((((int64_t)x.split * a.B + x.b) * a.Hkv + x.hk) * ((int64_t)a.Lq * a.G) + (int64_t)l * a.G + g) * DP);
+      if (kind == 2) return reinterpret_cast<uint8_t*>(a.part + ((int64_t)x.part * kUnitRows + r) * DP);
       return static_cast<uint8_t*>(a.out) + ((x.b * a.o_b + l * a.o_l + (int64_t)(x.hk * a.G + g) * a.o_h) << kind);
     };
     // Packs 32 scaled columns: 8 words of codes or 16 of 16-bit values.
@@ -683,27 +751,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto put_zeros = [&](uint8_t* row_at) {
       if (!row_at) return;
-      const int bytes = kind == 2 ? DP * 4 : a.D << kind;
+      const int bytes = a.D << kind;
       for (int k = 0; k < bytes; k += 8) *reinterpret_cast<uint2*>(row_at + k) = make_uint2(0, 0);
     };
-    auto put_lse = [&](const Item& x, int l, float m, float sum) {
-      if (a.splits == 1 || pos >= a.rows_l || l >= a.Lq) return;
-      const int64_t at = (((int64_t)x.split * a.B + x.b) * a.Hkv + x.hk) * ((int64_t)a.Lq * a.G) + (int64_t)l * a.G + g;
-      a.part_lse[at] = sum == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) + log2f(sum);
+    auto put_lse = [&](const Item& x, int r, float m, float sum) {
+      if (kind == 2) a.part_lse[(int64_t)x.part * kUnitRows + r] = sum == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) + log2f(sum);
     };
 
-    int len = len_of<kLens>(a, blockIdx.x);
-    for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
-      const Item x = decode<kLens>(a, it, len);
-      len = len_of<kLens>(a, it + gridDim.x);
+    if (kLens && a.cut) {   // samples without keys have no tiles: their rows are zeros
+      for (int b = 0; b < a.groups; ++b) {
+        if (tab[a.groups + 1 + b] != 0) continue;
+        Item x;
+        for (int it = blockIdx.x; it < a.Hkv * a.blocks; it += gridDim.x) {
+          x.blk = it % a.blocks;
+          x.hk = it / a.blocks;
+          x.b = b;
+          for (int i = 0; i < (kShared ? 2 : 1); ++i) put_zeros(out_row(x, (kShared ? 2 * x.blk + i : x.blk) * a.rows_l + pos, 0));
+        }
+      }
+    }
+    Units<kLens> units(a, tab);
+    Item x;
+    while (ok && units.next(x)) {
+      kind = x.part < 0 ? out_kind : 2;
       if constexpr (kShared) {
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
           const int l = (2 * x.blk + i) * a.rows_l + pos;
-          uint8_t* row_at = out_row(x, l);
+          uint8_t* row_at = out_row(x, l, i * kRows + row);
           if (x.n() == 0) {
             put_zeros(row_at);
-            put_lse(x, l, 0.0f, 0.0f);
             continue;
           }
           if (!mbar_wait_warp(l_full(i), icount[i] & 1, abort, kWaitLimitNs) ||
@@ -715,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const float sum = sum_l[i * kRows + row];
           const float f = sum == 0.0f ? 0.0f : __frcp_rn(sum);
-          put_lse(x, l, sum_m[i * kRows + row], sum);
+          put_lse(x, i * kRows + row, sum_m[i * kRows + row], sum);
           __syncwarp();   // together again for the TMEM loads
           // The accumulator goes to registers, packed, before anything is
           // stored: the next item's first product waits for it.
@@ -767,11 +844,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         const int l = x.blk * a.rows_l + pos;
-        uint8_t* row_at = out_row(x, l);
+        uint8_t* row_at = out_row(x, l, row);
         const int n0 = slot_tiles(x.n(), 0), n1 = slot_tiles(x.n(), 1);
         if (n0 == 0) {
           put_zeros(row_at);
-          put_lse(x, l, 0.0f, 0.0f);
           continue;
         }
         for (int i = 0; i < (n1 > 0 ? 2 : 1) && ok; ++i) {
@@ -788,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float a0 = m0 == -INFINITY ? 0.0f : ex2(m0 - top), a1 = m1 == -INFINITY ? 0.0f : ex2(m1 - top);
         const float l0 = sum_l[row], l1 = n1 > 0 ? sum_l[kRows + row] : 0.0f;
         const float sum = a0 * l0 + a1 * l1;
-        put_lse(x, l, top, sum);
+        put_lse(x, row, top, sum);
         const float f = sum == 0.0f ? 0.0f : __frcp_rn(sum);
         a0 *= f;
         a1 *= f;
@@ -845,32 +921,55 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// ------------------------------------------------------------------ joining the splits
+// ------------------------------------------------------------------ joining cut items
 //
-// o = sum_s 2^(lse_s - max) o_s / sum_s 2^(lse_s - max), a warp per output row;
-// a split without keys has lse = -inf.  Its bytes are splits x 4 D a row, which
-// the kernel before has just left in L2.
+// o = sum_s 2^(lse_s - max) o_s / sum_s 2^(lse_s - max) over the parts of an
+// item that CTAs shared; a part without counting keys has lse = -inf.  Blocks go
+// by the places where the row of all tiles was cut: the first cut inside an item
+// stands for it.  A warp per output row; the parts have just been left in L2.
 template <bool kF16>
-__global__ void __launch_bounds__(128) attention_join_kernel(const AttnArgs a, int DP) {
+__global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs a, int DP, int ctas, int unit_rows) {
   griddep_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t rows = (int64_t)a.B * a.Hkv * a.Lq * a.G;   // (b, hk, l, g)
-  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (r >= rows) return;
+  const int blocks_of = unit_rows / 8;
+  const int c = 1 + (int)blockIdx.x / blocks_of;
+  const int r = (int)blockIdx.x % blocks_of * 8 + (threadIdx.x >> 5);   // row of the unit
+  const uint64_t total = a.tab[a.groups];
+  auto start = [&](int k) { return (uint32_t)(total * k / ctas); };
+  const uint32_t p = start(c);
+  if (p >= total) return;
+  int entry = 0;   // the table entry that holds tile p
+  for (int k = lane + 1; k <= a.groups; k += 32) entry += a.tab[k] <= p;
+  for (int o = 16; o >= 1; o /= 2) entry += __shfl_xor_sync(0xFFFFFFFFu, entry, o);
+  const uint32_t tiles = a.tab[a.groups + 1 + entry], base = a.tab[entry];
+  const uint32_t item = (p - base) / tiles, s0 = base + item * tiles, s1 = s0 + tiles;
+  if (p == s0 || start(c - 1) > s0) return;   // not inside an item, or not its first cut
+  const int q = quotient((int)item, a.by_blocks);
+  const int blk = (int)item - q * a.blocks;
+  int b = quotient(q, a.by_hkv);
+  const int hk = q - b * a.Hkv;
+  if (a.groups > 1) b = entry;
+  const int row = r % kRows, pos = row / a.G, g = row - pos * a.G;
+  const int l = (unit_rows > kRows ? 2 * blk + r / kRows : blk) * a.rows_l + pos;
+  if (pos >= a.rows_l || l >= a.Lq) return;
   float inv_s = 1.0f;
   if (a.s_out) inv_s = __frcp_rn(ld_f32(a.s_out));
+  // parts: the CTA that begins in the item or before it, and those after it
+  auto part = [&](int k) { return (int64_t)(2 * k + (start(k) < s0 ? 1 : 0)) * unit_rows + r; };
   float top = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) top = fmaxf(top, a.part_lse[s * rows + r]);
+  for (int k = c - 1; k < ctas && start(k) < s1; ++k)
+    if (start(k) < start(k + 1)) top = fmaxf(top, a.part_lse[part(k)]);
   if (top == -INFINITY) top = 0.0f;
   float sum = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   const bool on = 4 * lane < a.D;
-  for (int s = 0; s < a.splits; ++s) {
-    const float w = exp2f(a.part_lse[s * rows + r] - top);
+  for (int k = c - 1; k < ctas && start(k) < s1; ++k) {
+    if (start(k) == start(k + 1)) continue;
+    const float w = exp2f(a.part_lse[part(k)] - top);
     if (w == 0.0f) continue;
     sum += w;
     if (on) {
-      const float4 v = *reinterpret_cast<const float4*>(a.part + (s * rows + r) * DP + 4 * lane);
+      const float4 v = *reinterpret_cast<const float4*>(a.part + part(k) * DP + 4 * lane);
       acc.x = fmaf(w, v.x, acc.x);
       acc.y = fmaf(w, v.y, acc.y);
       acc.z = fmaf(w, v.z, acc.z);
@@ -879,12 +978,7 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttnArgs a, i
   }
   if (!on) return;
   const float f = sum == 0.0f ? 0.0f : __frcp_rn(sum);
-  const int g = (int)(r % a.G);
-  int64_t q = r / a.G;
-  const int64_t l = q % a.Lq;
-  q /= a.Lq;
-  const int hk = (int)(q % a.Hkv);
-  const int64_t off = (q / a.Hkv) * a.o_b + l * a.o_l + (int64_t)(hk * a.G + g) * a.o_h + 4 * lane;
+  const int64_t off = b * a.o_b + l * a.o_l + (int64_t)(hk * a.G + g) * a.o_h + 4 * lane;
   acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
   if (a.s_out)
     *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.out) + off) =
@@ -911,11 +1005,18 @@ bool encode(CUtensorMap* map, bool f16, const void* base, int rank, const cuuint
 }
 
 struct Plan {
-  bool shared;      // 256 rows a work item, else 128 rows over even and odd tiles
-  int DP, G, rows_l, blocks, splits;
+  bool shared;      // 256 rows a unit, else 128 rows over even and odd tiles
+  bool cut;
+  int DP, G, rows_l, blocks, ctas, groups;
   int64_t items;
+  int unit_rows() const { return shared ? 2 * kRows : kRows; }
+  int64_t part_rows() const { return cut ? 2ll * ctas * unit_rows() : 0; }
 };
 
+// Whole items or cut ones: by an estimate of either's time, in units of a tile's
+// time (measured: about 1.75 us with 256 rows a unit; with 128 rows and two
+// tiles at once 0.7 us a tile).  Cutting costs the writing and joining of
+// the partial results, some 8 us.
 Plan make_plan(const AttnProblem& p, int sms) {
   Plan x;
   x.DP = p.D <= 64 ? 64 : 128;
@@ -924,13 +1025,20 @@ Plan make_plan(const AttnProblem& p, int sms) {
   const int slots = (p.Lq + x.rows_l - 1) / x.rows_l;
   x.shared = slots > 1;
   x.blocks = x.shared ? (slots + 1) / 2 : 1;
-  const int64_t base = (int64_t)p.B * p.Hkv * x.blocks;
-  const int tiles = (p.Lk + kKeys - 1) / kKeys;
-  const int per = x.shared ? 2 : 4;    // fewest tiles of a split that are worth its partials
-  int64_t s = base >= sms ? 1 : sms / base;
-  if (s > tiles / per) s = tiles / per;
-  x.splits = s < 1 ? 1 : (int)s;
-  x.items = base * x.splits;
+  x.items = (int64_t)p.B * p.Hkv * x.blocks;
+  const int64_t tiles = (p.Lk + kKeys - 1) / kKeys, total = x.items * tiles;
+  x.groups = p.kv_len ? p.B : 1;
+  const int64_t share = (total + sms - 1) / sms, least = 4;   // tiles a CTA
+  const int64_t per = share > least ? share : least;
+  const int64_t rounds = (x.items + sms - 1) / sms;
+  double whole = (double)(rounds * tiles), cut = (double)per + (x.shared ? 5.0 : 11.0);
+  // Lengths of their own make whole items uneven, the more so the fewer a CTA has.
+  if (p.kv_len && p.B > 1) {
+    whole *= rounds < 8 ? 1.0 : 0.8;
+    cut = (double)per * 0.8 + (x.shared ? 5.0 : 11.0);
+  }
+  x.cut = cut < whole && total < (1ll << 31) && x.groups <= kMaxCutSamples;
+  x.ctas = (int)(x.cut ? (total + per - 1) / per : x.items < sms ? x.items : sms);
   return x;
 }
 
@@ -958,12 +1066,12 @@ cudaError_t launch_kernel(const AttnMaps& maps, const AttnArgs& a, int grid, cud
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, k, maps, a)) != cudaSuccess) return e;
-  if (a.splits > 1) {
-    const int64_t rows = (int64_t)a.B * a.Hkv * a.Lq * a.G;
-    cfg.gridDim = dim3((unsigned)((rows + 3) / 4), 1, 1);
-    cfg.blockDim = dim3(128, 1, 1);
+  if (a.cut && grid > 1) {
+    const int unit_rows = kShared ? 2 * kRows : kRows;
+    cfg.gridDim = dim3((unsigned)((grid - 1) * (unit_rows / 8)), 1, 1);
+    cfg.blockDim = dim3(256, 1, 1);
     cfg.dynamicSmemBytes = 0;
-    if ((e = cudaLaunchKernelEx(&cfg, attention_join_kernel<kF16>, a, DP)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, attention_join_kernel<kF16>, a, DP, grid, unit_rows)) != cudaSuccess) return e;
   }
   return cudaGetLastError();
 }
@@ -987,8 +1095,7 @@ cudaError_t launch_type(const AttnMaps& maps, const AttnArgs& a, bool shared, in
 
 int64_t cross_attention_ws_floats(const AttnProblem& p, int sms) {
   const Plan x = make_plan(p, sms);
-  if (x.splits == 1) return 0;
-  return (int64_t)x.splits * p.B * p.Hq * p.Lq * (x.DP + 1);
+  return x.cut ? x.part_rows() * (x.DP + 1) + 2 * x.groups + 1 : 0;
 }
 
 cudaError_t launch_cross_attention(const AttnProblem& p, int sms, cudaStream_t st, int* tmap_err) {
@@ -1006,11 +1113,11 @@ cudaError_t launch_cross_attention(const AttnProblem& p, int sms, cudaStream_t s
   a.D = p.D;
   a.rows_l = x.rows_l;
   a.blocks = x.blocks;
-  a.splits = x.splits;
+  a.cut = x.cut;
+  a.groups = x.groups;
   a.items = (int)x.items;
   auto by = [](int d) { return d == 1 ? 0ull : ~0ull / (uint64_t)d + 1; };
   a.by_blocks = by(x.blocks);
-  a.by_splits = by(x.splits);
   a.by_hkv = by(p.Hkv);
   a.scale_log2 = p.scale * 1.4426950408889634f;
   a.kv_len = p.kv_len;
@@ -1027,8 +1134,11 @@ cudaError_t launch_cross_attention(const AttnProblem& p, int sms, cudaStream_t s
     a.wide = reinterpret_cast<uintptr_t>(p.out) % 32 == 0 && p.D * bytes % 32 == 0 && !odd(a.o_b, p.B) &&
              !odd(a.o_l, p.Lq) && !odd(a.o_h, p.Hq);
   }
-  a.part = p.ws;
-  a.part_lse = p.ws + (int64_t)x.splits * p.B * p.Hq * p.Lq * x.DP;   // not used with one split
+  if (x.cut) {
+    a.part = p.ws;
+    a.part_lse = a.part + x.part_rows() * x.DP;
+    a.tab = reinterpret_cast<uint32_t*>(a.part_lse + x.part_rows());
+  }
   a.q_bytes = (uint32_t)(x.G * x.rows_l * 128);
   const cuuint64_t D = p.D, B = p.B;
   a.q_bmul = p.qs[0] != 0;
@@ -1054,7 +1164,7 @@ cudaError_t launch_cross_attention(const AttnProblem& p, int sms, cudaStream_t s
     *tmap_err = 1;
     return cudaSuccess;
   }
-  const int grid = (int)(x.items < sms ? x.items : sms);
+  const int grid = x.ctas;
   if (x.DP == 64) return p.f16 ? launch_type<64, true>(maps, a, x.shared, grid, st) : launch_type<64, false>(maps, a, x.shared, grid, st);
   return p.f16 ? launch_type<128, true>(maps, a, x.shared, grid, st) : launch_type<128, false>(maps, a, x.shared, grid, st);
 }
