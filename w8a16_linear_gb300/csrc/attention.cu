@@ -72,7 +72,8 @@ struct Cfg {
   static constexpr int kStages = DP == 128 ? 4 : 6;      // even: see the cleaning warp
   static constexpr int kQ = 0;
   static constexpr int kRing = kQ + 2 * kTile;
-  static constexpr int kSum = kRing + kStages * kTile;   // l[2][128], m[2][128]
+  static constexpr int kOut = kRing + kStages * kTile;   // 32 rows of 128 bytes for each epilogue warp
+  static constexpr int kSum = kOut + 4 * 32 * 128;       // l[2][128], m[2][128]
   static constexpr int kTab = kSum + 4 * kRows * 4;      // first tile and tiles per item of each sample
   static constexpr int kBar = kTab + (2 * kMaxCutSamples + 2) * 4;
   // full[S], empty[S], clean[S], q_full[2], q_empty[2], s_full[2], p_full[2],
@@ -104,13 +105,14 @@ struct AttnArgs {
   void* out;
   int64_t o_b, o_l, o_h;      // element strides of the output
   int wide;                   // output rows are 32-byte aligned and whole multiples of 32 bytes
+  int tma_out;                // a warp's 32 rows are whole positions, which one bulk copy can write
   float* part;                // cut: two partial results of each CTA, normalised
   float* part_lse;            // and the log2 of their sums
   uint32_t* tab;              // and the tile table, for the joining kernel
 };
 
 struct AttnMaps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, o;
 };
 
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
@@ -119,6 +121,14 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
       "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_store_5d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2, int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5, %6}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(src), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
       : "memory");
 }
 
@@ -203,10 +213,10 @@ __device__ __forceinline__ int load_len(const int32_t* p) {
   asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
-__device__ __forceinline__ bool load_mask(const uint8_t* p) {
+__device__ __forceinline__ uint32_t load_mask(const uint8_t* p) {
   uint32_t v;
   asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v != 0;
+  return v;
 }
 
 // n / d for n < 2^32 (d from the host), with by = 2^64 / d rounded up.
@@ -556,25 +566,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t e = ring ? seen[1]++ : seen[0]++;
           const int st = stage_of(ring, e);
           const bool pass = kShared && !is_v;
-          if (!pass && !mbar_wait_warp(full_bar(st), phase_of(e), abort, kWaitLimitNs)) return false;
+          // Bit lane of word e: row 32 e + lane of the tile is to be cleared
+          // (beyond the array the copy has written zeros).  The mask does not
+          // wait for the copy.
+          uint32_t word[4] = {0, 0, 0, 0};
           if (is_v) {
-            uint8_t* v = smem + C::kRing + st * C::kTile;
-            bool wrote = false;
-            for (int r = lane; r < kKeys; r += 32) {
-              const int j = tile * kKeys + r;
-              // beyond the array the copy has written zeros
-              if (j >= a.Lk) continue;
-              bool on = j < x.len;
-              if constexpr (kMask)
-                if (on) on = load_mask(a.kv_mask + x.b * a.mask_stride + j);
-              if (on) continue;
-              wrote = true;
-              for (int at = 0; at < C::kAtoms; ++at)
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                  *reinterpret_cast<uint4*>(v + at * kAtom + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+            for (int e = 0; e < 4; ++e) {
+              const int j = tile * kKeys + 32 * e + lane;
+              bool off = j < a.Lk && j >= x.len;
+              if constexpr (kMask)
+                if (j < x.len) off = load_mask(a.kv_mask + x.b * a.mask_stride + j) == 0;
+              word[e] = __ballot_sync(0xFFFFFFFFu, off);
             }
-            if (wrote) fence_proxy_async_smem();
+          }
+          if (!pass && !mbar_wait_warp(full_bar(st), phase_of(e), abort, kWaitLimitNs)) return false;
+          if (word[0] | word[1] | word[2] | word[3]) {
+            // eight lanes to a row's 128 bytes, four rows at a time
+            uint8_t* v = smem + C::kRing + st * C::kTile + (lane & 7) * 16;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll 1
+              for (int k = 0; k < 32; k += 4) {
+                if (!(word[e] >> k & 15)) continue;
+                const int r = k + (lane >> 3);
+                if (word[e] >> r & 1)
+#pragma unroll
+                  for (int at = 0; at < C::kAtoms; ++at)
+                    *reinterpret_cast<uint4*>(v + at * kAtom + (32 * e + r) * 128) = make_uint4(0, 0, 0, 0);
+              }
+            fence_proxy_async_smem();
             __syncwarp();
           }
           if (!pass && lane == 0) mbar_arrive(clean_bar(st));
@@ -598,20 +619,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = slot_tiles(x.n(), i);
       if (n == 0) continue;
       float m = -INFINITY, l = 0.0f;             // m in powers of two: scaled scores
+      const auto first_key = [&](int j) { return (x.t0 + (kShared ? j : 2 * j + i)) * kKeys; };
+      // The mask of the lane's four keys, asked for a tile ahead.
+      uint32_t ahead[4];
+      const auto ask = [&](int key0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = key0 + 4 * lane + e;
+          ahead[e] = 0;
+          if (key < x.len) ahead[e] = load_mask(a.kv_mask + x.b * a.mask_stride + key);
+        }
+      };
+      if constexpr (kMask) ask(first_key(0));
       for (int j = 0; j < n; ++j) {
-        const int key0 = (x.t0 + (kShared ? j : 2 * j + i)) * kKeys;
+        const int key0 = first_key(j);
         // Bit lane of word e: key 4 lane + e of the tile counts.
-        const bool masked = kMask || key0 + kKeys > x.len;
+        // The masking and the rescaling below are kept out of the line of the
+        // loop, which is long enough to weigh on the instruction cache.
+        const bool masked = kMask || __builtin_expect(key0 + kKeys > x.len, 0);
         uint32_t word[4];
         if (masked) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int key = key0 + 4 * lane + e;
-            bool on = key < x.len;
-            if constexpr (kMask)
-              if (on) on = load_mask(a.kv_mask + x.b * a.mask_stride + key);
+            const bool on = kMask ? ahead[e] != 0 : key0 + 4 * lane + e < x.len;
             word[e] = __ballot_sync(0xFFFFFFFFu, on);
           }
+          if constexpr (kMask)
+            if (j + 1 < n) ask(first_key(j + 1));
           __syncwarp();   // lanes past the last key took another path
         }
         if (!mbar_wait_lanes(s_full(i), scount & 1, abort)) {
@@ -628,16 +662,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait_for(r[1]);
         tmem_ld_32x32b_x32(s_col(i) + quad + 64, r[2]);
         tmem_ld_32x32b_x32(s_col(i) + quad + 96, r[3]);
+        if (masked) {   // a key that does not count has the weight exp2(-inf) = 0
+          tmem_ld_wait_for(r[2]);
+          tmem_ld_wait_for(r[3]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((word[e & 3] >> (8 * c + (e >> 2))) & 1)) r[c][e] = 0xFF800000u;
+        }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           if (c == 2) {
             tmem_ld_wait_for(r[2]);
             tmem_ld_wait_for(r[3]);
-          }
-          if (masked) {   // a key that does not count has the weight exp2(-inf) = 0
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!((word[e & 3] >> (8 * c + (e >> 2))) & 1)) r[c][e] = 0xFF800000u;
           }
 #pragma unroll
           for (int e = 0; e < 32; e += 2)
@@ -647,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Scores of slot i are complete, so its product with the previous tile
         // is too (issued before them): O_i may be rescaled here.
         const bool grow = top > m + kLazyMax || (m == -INFINITY && top > m);
-        if (__any_sync(0xFFFFFFFFu, grow)) {
+        if (__builtin_expect(__any_sync(0xFFFFFFFFu, grow), 0)) {
           const float m_new = fmaxf(m, top);
           if (j > 0) {
             const float f = m_new == -INFINITY ? 1.0f : ex2(m - m_new);
@@ -706,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_down<88>();
     const int row = (warp & 3) * 32 + lane;
     const uint32_t quad = (uint32_t)((warp & 3) * 32) << 16;
-    const int pos = row / a.G, g = row - pos * a.G;
+    const int pos = row / a.G, g = row - pos * a.G, warp_l = 32 / a.G;
     float inv_s = 1.0f;
     if (a.s_out) inv_s = __frcp_rn(ld_f32(a.s_out));
     uint32_t icount[2] = {0, 0};
@@ -749,6 +787,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     };
+    // A warp's packed rows by way of its 4 KB of shared memory and a bulk copy
+    // for each 128 bytes of a row (64 for codes of small heads).  Stores from the
+    // rows' own threads, a sector each, kept the load/store path busy for some
+    // 4000 cycles a slot, and the other roles' barriers and the next slot's rows behind them.
+    auto put_bulk = [&](const Item& x, int l_warp, const uint32_t* w) {
+      constexpr int kHalves = DP / 64;                               // 16-bit rows: 64 columns at a time
+      uint8_t* stage = smem + C::kOut + (warp & 3) * 32 * 128;
+      const uint32_t stage_at = sbase + C::kOut + (uint32_t)((warp & 3) * 32 * 128);
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        if (kind == 0 && h > 0) break;
+        if (lane == 0) tma_store_wait_read<0>();                     // the copy before has read the stage
+        __syncwarp();
+        if (kind == 0 && DP == 64) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(stage + lane * 64 + ((k ^ (lane >> 1 & 3)) << 4)) =
+                make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int at = (kind == 0 ? 0 : 32 * h) + 4 * k;
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) = make_uint4(w[at], w[at + 1], w[at + 2], w[at + 3]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && l_warp < a.Lq) {
+          tma_store_5d(&maps.o, stage_at, kind == 0 ? 0 : 64 * h, 0, l_warp, x.hk, x.b);
+          tma_store_commit();
+        }
+      }
+    };
     auto put_zeros = [&](uint8_t* row_at) {
       if (!row_at) return;
       const int bytes = a.D << kind;
@@ -779,6 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i) {
           const int l = (2 * x.blk + i) * a.rows_l + pos;
           uint8_t* row_at = out_row(x, l, i * kRows + row);
+          const int l_warp = l - pos + (warp & 3) * warp_l;   // position of the warp's first row
           if (x.n() == 0) {
             put_zeros(row_at);
             continue;
@@ -827,7 +899,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (c == DP / 32 - 1) free_o();
               pack(r, f, w + 8 * c);
             }
-            if (row_at) put_words(row_at, DP / 4, a.D, w);
+            if (a.tma_out) put_bulk(x, l_warp, w);
+            else if (row_at) put_words(row_at, DP / 4, a.D, w);
           } else {
             uint32_t w[DP / 2];
 #pragma unroll
@@ -838,7 +911,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (c == DP / 32 - 1) free_o();
               pack(r, f, w + 16 * c);
             }
-            if (row_at) put_words(row_at, DP / 2, 2 * a.D, w);
+            if (a.tma_out) put_bulk(x, l_warp, w);
+            else if (row_at) put_words(row_at, DP / 2, 2 * a.D, w);
           }
           __syncwarp();
         }
@@ -910,6 +984,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    if (lane == 0) tma_store_wait_all();
     if (!ok && lane == 0) record_timeout(abort);
   }
 
@@ -992,15 +1067,15 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs a, i
 
 // A dimension of one entry, or one that the samples share, gets the stride
 // of the dimension before it: its own is never used, and may be anything.
-bool encode(CUtensorMap* map, bool f16, const void* base, int rank, const cuuint64_t* dims, const int64_t* strides,
-            const cuuint32_t* box) {
+bool encode(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank, const cuuint64_t* dims,
+            const int64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   EncodeTiledFn fn = get_encode_tiled();
   if (!fn) return false;
+  const cuuint64_t bytes = type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 1 : 2;
   cuuint64_t st[4];
-  for (int i = 0; i + 1 < rank; ++i) st[i] = dims[i + 1] > 1 ? (cuuint64_t)strides[i] * 2 : i ? st[i - 1] : dims[0] * 2;
+  for (int i = 0; i + 1 < rank; ++i) st[i] = dims[i + 1] > 1 ? (cuuint64_t)strides[i] * bytes : i ? st[i - 1] : dims[0] * bytes;
   const cuuint32_t es[5] = {1, 1, 1, 1, 1};
-  return fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
-            const_cast<void*>(base), dims, st, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return fn(map, type, (cuuint32_t)rank, const_cast<void*>(base), dims, st, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1144,13 +1219,14 @@ cudaError_t launch_cross_attention(const AttnProblem& p, int sms, cudaStream_t s
   a.q_bmul = p.qs[0] != 0;
   a.k_bmul = p.ks[0] != 0;
   a.v_bmul = p.vs[0] != 0;
+  const CUtensorMapDataType type16 = p.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   bool ok = true;
   {
     // (dimension, head of the group, position, key head, sample)
     const cuuint64_t dims[5] = {D, (cuuint64_t)x.G, (cuuint64_t)p.Lq, (cuuint64_t)p.Hkv, a.q_bmul ? B : 1};
     const int64_t s[4] = {p.qs[2], p.qs[1], p.qs[2] * x.G, p.qs[0]};
     const cuuint32_t box[5] = {64, (cuuint32_t)x.G, (cuuint32_t)x.rows_l, 1, 1};
-    ok = ok && encode(&maps.q, p.f16, p.q, 5, dims, s, box);
+    ok = ok && encode(&maps.q, type16, p.q, 5, dims, s, box);
   }
   for (int kv = 0; kv < 2; ++kv) {
     const int64_t* t = kv ? p.vs : p.ks;
@@ -1158,7 +1234,19 @@ cudaError_t launch_cross_attention(const AttnProblem& p, int sms, cudaStream_t s
     const cuuint64_t dims[4] = {D, (cuuint64_t)p.Hkv, (cuuint64_t)(p.Lk ? p.Lk : 1), (kv ? a.v_bmul : a.k_bmul) ? B : 1};
     const int64_t s[3] = {t[2], t[1], t[0]};
     const cuuint32_t box[4] = {64, 1, (cuuint32_t)kKeys, 1};
-    ok = ok && encode(kv ? &maps.v : &maps.k, p.f16, !p.Lk ? p.q : kv ? p.v : p.k, 4, dims, s, box);
+    ok = ok && encode(kv ? &maps.v : &maps.k, type16, !p.Lk ? p.q : kv ? p.v : p.k, 4, dims, s, box);
+  }
+  {
+    const int64_t bytes = p.s_out ? 1 : 2;
+    auto odd = [&](int64_t stride, int n) { return n > 1 && stride * bytes % 16 != 0; };
+    a.tma_out = x.shared && 32 % x.G == 0 && p.D * bytes % 16 == 0 && !odd(a.o_b, p.B) && !odd(a.o_l, p.Lq) && !odd(a.o_h, p.Hq);
+    if (a.tma_out) {
+      const cuuint64_t dims[5] = {D, (cuuint64_t)x.G, (cuuint64_t)p.Lq, (cuuint64_t)p.Hkv, B};
+      const int64_t s[4] = {p.os[2], p.os[1], p.os[2] * x.G, p.os[0]};
+      const cuuint32_t box[5] = {p.s_out ? (cuuint32_t)x.DP : 64, (cuuint32_t)x.G, (cuuint32_t)(32 / x.G), 1, 1};
+      ok = ok && encode(&maps.o, p.s_out ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : type16, p.out, 5, dims, s, box,
+                        p.s_out && x.DP == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+    }
   }
   if (!ok) {
     *tmap_err = 1;
