@@ -1,6 +1,7 @@
 """One transformer block's linear sites on one denoising step, in the
 precision the step policy picks: the call sequence of the step-scheduled
-stack, over the C ABI.
+stack, over the C ABI; and the site where a block attends to an encoder's
+states (CrossSite, at the end).
 
 This module only orders calls, owns the buffers they write and the streams
 they overlap on; every value is computed by the library's kernels.
@@ -22,6 +23,10 @@ seven weights are dequantized on a side stream in the order the GEMMs need
 them (weights do not depend on activations), and each site runs the bf16
 GEMM on its dequantized weight as soon as that is ready; gate/up run with
 the bf16 SwiGLU fused into their epilogue.
+
+Cross attention takes keys and values from another tensor, so they share no
+quantization with the queries (TensorRT-LLM PR #17476, section What changed);
+CrossSite makes them once and keeps them.
 """
 
 from dataclasses import dataclass
@@ -131,3 +136,60 @@ class BlockStep:
         main.wait_event(self.dq_ev[3])
         W.bf16_linear_group(self.h16, [self.wd_down], outs=[self.y_down])
         return 11 if fused else 12
+
+
+@dataclass
+class CrossWeights:
+    """A cross-attention site's norms (bfloat16 ``[H]`` / ``[E]``), E4M3 weights
+    ``[N, K]`` with one float32 scale for each output channel, and the
+    out-projection's weight with its own scale and static input scale."""
+    norm: torch.Tensor                                # of the block's tokens
+    enc_norm: torch.Tensor                            # of the encoder's states
+    q: Tuple[torch.Tensor, torch.Tensor]              # [heads * D, H], [heads * D]
+    k: Tuple[torch.Tensor, torch.Tensor]              # [kv_heads * D, E], [kv_heads * D]
+    v: Tuple[torch.Tensor, torch.Tensor]
+    out: Tuple[torch.Tensor, torch.Tensor]            # [H, heads * D], one scale
+    s_attn: torch.Tensor                              # input scale of the out-projection
+
+
+class CrossSite:
+    """The site where a block's tokens attend to an encoder's states: the
+    residual's addition and norm to E4M3 with a scale for each token, the query
+    projection on those codes, softmax attention over the encoder's keys and
+    values, written as E4M3 codes, and the out-projection on them.
+
+    ``encode`` makes the keys and values, once for all denoising steps (or all
+    tokens of an answer); ``run`` is one pass over ``M = batch * tokens`` rows.
+    Buffers are the site's own, so that a pass can be captured in a CUDA graph."""
+
+    def __init__(self, batch, tokens, hidden, heads, kv_heads, head_dim, device):
+        self.B, self.L, self.H = batch, tokens, hidden
+        self.heads, self.kv_heads, self.D = heads, kv_heads, head_dim
+        M, N = batch * tokens, heads * head_dim
+        bf = dict(dtype=torch.bfloat16, device=device)
+        u8 = dict(dtype=torch.uint8, device=device)
+        self.codes = torch.empty((M, hidden), **u8)
+        self.s_tok = torch.empty((M,), dtype=torch.float32, device=device)
+        self.res = torch.empty((M, hidden), **bf)
+        self.q = torch.empty((M, N), **bf)
+        self.attn = torch.empty((batch, tokens, heads, head_dim), **u8)
+        self.y = torch.empty((M, hidden), **bf)
+        self.k = self.v = self.ws = None
+
+    def encode(self, W, w, states):
+        """Keys and values of ``states`` [batch, positions, E] (bfloat16)."""
+        B, T, E = states.shape
+        codes, s_tok, _ = W.add_rms_norm_quant(states.reshape(B * T, E), None, w.enc_norm)
+        kv = W.fp8_linear_w8a8_pertoken_group(codes, s_tok, [w.k[0], w.v[0]], [w.k[1], w.v[1]])
+        self.k, self.v = (t.view(B, T, self.kv_heads, self.D) for t in kv)
+        self.ws = W.cross_attention_workspace(self.q.view(B, self.L, self.heads, self.D), self.k, self.v)
+
+    def run(self, W, w, x, residual, kv_len=None, kv_mask=None):
+        """One pass on the current stream: returns the out-projection's output
+        (``y``) and the sum of ``x`` and ``residual`` (``res``), [M, hidden]."""
+        W.add_rms_norm_quant(x, residual, w.norm, out=self.codes, s_tok=self.s_tok, res_out=self.res)
+        W.fp8_linear_w8a8_pertoken(self.codes, self.s_tok, w.q[0], w.q[1], out=self.q)
+        q = self.q.view(self.B, self.L, self.heads, self.D)
+        W.cross_attention(q, self.k, self.v, kv_len=kv_len, kv_mask=kv_mask, s_out=w.s_attn, out=self.attn, ws=self.ws)
+        W.fp8_linear_w8a8(self.attn.view(self.B * self.L, -1), w.out[0], w.s_attn, w.out[1], out=self.y)
+        return self.y, self.res
