@@ -212,6 +212,35 @@ def test_equal_calls_give_equal_bits_on_any_stream(W):
         assert torch.equal(want.view(torch.int16), got.view(torch.int16))
 
 
+@pytest.mark.parametrize("D,dtype", [(128, "bf16"), (64, "f16")])
+def test_long_keys_of_few_queries_back_to_back(W, D, dtype):
+    """Key sides that come from memory tile by tile, cut over all CTAs, in calls
+    that follow one another without a pause: the same bits each time."""
+    q, k, v = make(6, 1, 9001, 12, 4, D, dtype, seed=13)
+    outs = [W.cross_attention(q, k, v) for _ in range(12)]
+    torch.cuda.synchronize()
+    W.poll_device_error()
+    for o in outs[1:]:
+        assert torch.equal(o.view(torch.int16), outs[0].view(torch.int16))
+    check(outs[0], *exact(q, k, v))
+
+
+@pytest.mark.parametrize("Lq,H,Hk", [(1, 8, 2), (700, 4, 4)])
+def test_lengths_of_many_samples(W, Lq, H, Hk):
+    """Lengths from none to all of the keys, one tile and part of one, in turn:
+    units of one and two tiles next to long ones in the same CTA; and more
+    samples than the tile table has room for."""
+    for B in (9, 70):
+        if B == 70 and Lq > 1:
+            continue
+        q, k, v = make(B, Lq, 1500, H, Hk, 64, seed=B)
+        lens = torch.tensor([[0, 1500, 128, 129, 1, 640, 0, 257, 1499][b % 9] for b in range(B)], dtype=torch.int32,
+                            device="cuda")
+        o = W.cross_attention(q, k, v, kv_len=lens)
+        W.poll_device_error()
+        check(o, *exact(q, k, v, keep_of(B, 1500, lens)))
+
+
 def test_a_workspace_too_small_is_refused(W):
     q, k, v = make(1, 1, 6000, 8, 2, 128)
     ws = W.cross_attention_workspace(q, k, v)
