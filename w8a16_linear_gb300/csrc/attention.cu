@@ -224,6 +224,12 @@ __device__ __forceinline__ int quotient(int n, uint64_t by) {
   return by ? (int)__umul64hi((uint64_t)(uint32_t)n, by) : n;
 }
 
+// Where CTA k of `ctas` begins in a row of `total` tiles: total k / ctas, in 32 bits.
+__device__ __forceinline__ uint32_t share_begin(uint32_t total, uint32_t k, uint32_t ctas) {
+  const uint32_t q = total / ctas;
+  return k * q + k * (total - q * ctas) / ctas;
+}
+
 // A CTA's units, in the order in which each of its roles goes through them.
 //
 // Whole items: CTA c takes items c, c + CTAs, ...  Cut items: all key tiles of
@@ -243,7 +249,7 @@ struct Units {
     if (!a.cut) ask();
   }
   __device__ __forceinline__ uint32_t begin(uint32_t cta) const {
-    return (uint32_t)((uint64_t)tab[a.groups] * cta / gridDim.x);
+    return share_begin(tab[a.groups], cta, gridDim.x);
   }
   // The number of keys of the next item's sample, asked for an item ahead: its
   // latency (some 700 cycles) would stand between two items in every role.
@@ -753,10 +759,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int out_kind = a.s_out ? 0 : 1;      // log2 of a value's bytes
     int kind = out_kind;                       // 2 in a unit that writes a partial result
     constexpr int kUnitRows = kShared ? 2 * kRows : kRows;
-    // Where this thread's row (position l, row r of the unit) starts, or null.
-    auto out_row = [&](const Item& x, int l, int r) -> uint8_t* {
+    // 32 columns (chunk c) of a partial result.  Four columns of a warp's 32 rows
+    // stand together, so that a store is 512 bytes in one piece: row by row they
+    // were 4096 sectors a slot, and 16 us.
+    auto put_part = [&](const Item& x, int row_group, int c, const uint32_t (&r)[32], float f) {
+      float4* dst = reinterpret_cast<float4*>(a.part) + (((int64_t)x.part * (kUnitRows / 32) + row_group) * (DP / 4) + 8 * c) * 32 + lane;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        dst[k * 32] = make_float4(__uint_as_float(r[4 * k]) * f, __uint_as_float(r[4 * k + 1]) * f,
+                                  __uint_as_float(r[4 * k + 2]) * f, __uint_as_float(r[4 * k + 3]) * f);
+    };
+    // Where this thread's row (position l) starts, or null.
+    auto out_row = [&](const Item& x, int l) -> uint8_t* {
       if (pos >= a.rows_l || l >= a.Lq) return nullptr;
-      if (kind == 2) return reinterpret_cast<uint8_t*>(a.part + ((int64_t)x.part * kUnitRows + r) * DP);
       return static_cast<uint8_t*>(a.out) + ((x.b * a.o_b + l * a.o_l + (int64_t)(x.hk * a.G + g) * a.o_h) << kind);
     };
     // Packs 32 scaled columns: 8 words of codes or 16 of 16-bit values.
@@ -837,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           x.blk = it % a.blocks;
           x.hk = it / a.blocks;
           x.b = b;
-          for (int i = 0; i < (kShared ? 2 : 1); ++i) put_zeros(out_row(x, (kShared ? 2 * x.blk + i : x.blk) * a.rows_l + pos, 0));
+          for (int i = 0; i < (kShared ? 2 : 1); ++i) put_zeros(out_row(x, (kShared ? 2 * x.blk + i : x.blk) * a.rows_l + pos));
         }
       }
     }
@@ -849,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
           const int l = (2 * x.blk + i) * a.rows_l + pos;
-          uint8_t* row_at = out_row(x, l, i * kRows + row);
+          uint8_t* row_at = out_row(x, l);
           const int l_warp = l - pos + (warp & 3) * warp_l;   // position of the warp's first row
           if (x.n() == 0) {
             put_zeros(row_at);
@@ -880,13 +895,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_ld_32x32b_x32(o_col(i) + quad + c * 32, r);
               tmem_ld_wait_for(r);
               if (c == DP / 32 - 1) free_o();
-              if (row_at) {
-                float4* dst = reinterpret_cast<float4*>(row_at) + 8 * c;
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  dst[k] = make_float4(__uint_as_float(r[4 * k]) * f, __uint_as_float(r[4 * k + 1]) * f,
-                                       __uint_as_float(r[4 * k + 2]) * f, __uint_as_float(r[4 * k + 3]) * f);
-              }
+              put_part(x, 4 * i + (warp & 3), c, r, f);
               __syncwarp();
             }
           } else if (kind == 0) {
@@ -918,7 +927,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         const int l = x.blk * a.rows_l + pos;
-        uint8_t* row_at = out_row(x, l, row);
+        uint8_t* row_at = out_row(x, l);
+        const bool any = __any_sync(0xFFFFFFFFu, row_at != nullptr);
         const int n0 = slot_tiles(x.n(), 0), n1 = slot_tiles(x.n(), 1);
         if (n0 == 0) {
           put_zeros(row_at);
@@ -967,10 +977,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (n1 > 0) mbar_arrive(o_free(1));
             }
           }
-          if (row_at && kind == 2) {
-            uint4* dst = reinterpret_cast<uint4*>(row_at) + 8 * c;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) dst[k] = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+          if (kind == 2) {
+            if (any) put_part(x, warp & 3, c, r, 1.0f);
           } else if (row_at && kind == 0) {
             uint32_t w[8];
             pack(r, 1.0f, w);
@@ -1001,16 +1009,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 // o = sum_s 2^(lse_s - max) o_s / sum_s 2^(lse_s - max) over the parts of an
 // item that CTAs shared; a part without counting keys has lse = -inf.  Blocks go
 // by the places where the row of all tiles was cut: the first cut inside an item
-// stands for it.  A warp per output row; the parts have just been left in L2.
-template <bool kF16>
-__global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs a, int DP, int ctas, int unit_rows) {
+// stands for it.  A warp takes 16 columns of 32 rows, a lane a row, in the
+// order in which the parts were written (and have been left in L2).
+template <int DP, bool kF16>
+__global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs a, int ctas, int unit_rows) {
   griddep_wait();
   const int lane = threadIdx.x & 31;
-  const int blocks_of = unit_rows / 8;
-  const int c = 1 + (int)blockIdx.x / blocks_of;
-  const int r = (int)blockIdx.x % blocks_of * 8 + (threadIdx.x >> 5);   // row of the unit
-  const uint64_t total = a.tab[a.groups];
-  auto start = [&](int k) { return (uint32_t)(total * k / ctas); };
+  constexpr int kChunks = DP / 16;
+  const int groups = unit_rows / 32;
+  const int w = (int)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int c = 1 + w / (groups * kChunks);
+  const int chunk = w % kChunks, group = w / kChunks % groups;
+  const uint32_t total = a.tab[a.groups];
+  auto start = [&](int k) { return share_begin(total, (uint32_t)k, (uint32_t)ctas); };
   const uint32_t p = start(c);
   if (p >= total) return;
   int entry = 0;   // the table entry that holds tile p
@@ -1024,43 +1035,52 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs a, i
   int b = quotient(q, a.by_hkv);
   const int hk = q - b * a.Hkv;
   if (a.groups > 1) b = entry;
+  const int r = 32 * group + lane;            // row of the unit
   const int row = r % kRows, pos = row / a.G, g = row - pos * a.G;
   const int l = (unit_rows > kRows ? 2 * blk + r / kRows : blk) * a.rows_l + pos;
-  if (pos >= a.rows_l || l >= a.Lq) return;
+  const bool on = pos < a.rows_l && l < a.Lq && 16 * chunk < a.D;
+  if (!__any_sync(0xFFFFFFFFu, on)) return;
   float inv_s = 1.0f;
   if (a.s_out) inv_s = __frcp_rn(ld_f32(a.s_out));
   // parts: the CTA that begins in the item or before it, and those after it
-  auto part = [&](int k) { return (int64_t)(2 * k + (start(k) < s0 ? 1 : 0)) * unit_rows + r; };
+  auto part = [&](int k) { return 2 * k + (start(k) < s0 ? 1 : 0); };
   float top = -INFINITY;
   for (int k = c - 1; k < ctas && start(k) < s1; ++k)
-    if (start(k) < start(k + 1)) top = fmaxf(top, a.part_lse[part(k)]);
+    if (start(k) < start(k + 1)) top = fmaxf(top, a.part_lse[(int64_t)part(k) * unit_rows + r]);
   if (top == -INFINITY) top = 0.0f;
-  float sum = 0.0f;
-  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  const bool on = 4 * lane < a.D;
+  float sum = 0.0f, acc[16] = {};
   for (int k = c - 1; k < ctas && start(k) < s1; ++k) {
     if (start(k) == start(k + 1)) continue;
-    const float w = exp2f(a.part_lse[part(k)] - top);
-    if (w == 0.0f) continue;
-    sum += w;
-    if (on) {
-      const float4 v = *reinterpret_cast<const float4*>(a.part + part(k) * DP + 4 * lane);
-      acc.x = fmaf(w, v.x, acc.x);
-      acc.y = fmaf(w, v.y, acc.y);
-      acc.z = fmaf(w, v.z, acc.z);
-      acc.w = fmaf(w, v.w, acc.w);
+    const float weight = exp2f(a.part_lse[(int64_t)part(k) * unit_rows + r] - top);
+    sum += weight;
+    const float4* src = reinterpret_cast<const float4*>(a.part) + (((int64_t)part(k) * groups + group) * (DP / 4) + 4 * chunk) * 32 + lane;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float4 v = src[e * 32];
+      acc[4 * e] = fmaf(weight, v.x, acc[4 * e]);
+      acc[4 * e + 1] = fmaf(weight, v.y, acc[4 * e + 1]);
+      acc[4 * e + 2] = fmaf(weight, v.z, acc[4 * e + 2]);
+      acc[4 * e + 3] = fmaf(weight, v.w, acc[4 * e + 3]);
     }
   }
   if (!on) return;
   const float f = sum == 0.0f ? 0.0f : __frcp_rn(sum);
-  const int64_t off = b * a.o_b + l * a.o_l + (int64_t)(hk * a.G + g) * a.o_h + 4 * lane;
-  acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-  if (a.s_out)
-    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.out) + off) =
-        cvt_e4m3x2(acc.x * inv_s, acc.y * inv_s) | (cvt_e4m3x2(acc.z * inv_s, acc.w * inv_s) << 16);
-  else
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + off) =
-        make_uint2(cvt16x2(kF16, acc.x, acc.y), cvt16x2(kF16, acc.z, acc.w));
+  const int64_t off = b * a.o_b + l * a.o_l + (int64_t)(hk * a.G + g) * a.o_h + 16 * chunk;
+#pragma unroll
+  for (int e = 0; e < 16; e += 8) {           // eight columns: 16 bytes, or 8 of codes
+    if (16 * chunk + e >= a.D) break;
+    if (a.s_out) {
+      uint32_t c8[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) c8[k] = cvt_e4m3x2(acc[e + 2 * k] * f * inv_s, acc[e + 2 * k + 1] * f * inv_s);
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + off + e) = make_uint2(c8[0] | (c8[1] << 16), c8[2] | (c8[3] << 16));
+    } else {
+      uint32_t v8[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v8[k] = cvt16x2(kF16, acc[e + 2 * k] * f, acc[e + 2 * k + 1] * f);
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + off + e) = make_uint4(v8[0], v8[1], v8[2], v8[3]);
+    }
+  }
 }
 
 // ------------------------------------------------------------------ host side
@@ -1143,10 +1163,10 @@ cudaError_t launch_kernel(const AttnMaps& maps, const AttnArgs& a, int grid, cud
   if ((e = cudaLaunchKernelEx(&cfg, k, maps, a)) != cudaSuccess) return e;
   if (a.cut && grid > 1) {
     const int unit_rows = kShared ? 2 * kRows : kRows;
-    cfg.gridDim = dim3((unsigned)((grid - 1) * (unit_rows / 8)), 1, 1);
+    cfg.gridDim = dim3((unsigned)((grid - 1) * (unit_rows / 32 * (DP / 16) / 8)), 1, 1);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.dynamicSmemBytes = 0;
-    if ((e = cudaLaunchKernelEx(&cfg, attention_join_kernel<kF16>, a, DP, grid, unit_rows)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, attention_join_kernel<DP, kF16>, a, grid, unit_rows)) != cudaSuccess) return e;
   }
   return cudaGetLastError();
 }
