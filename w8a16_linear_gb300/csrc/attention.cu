@@ -1042,21 +1042,29 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs a, i
   if (!__any_sync(0xFFFFFFFFu, on)) return;
   float inv_s = 1.0f;
   if (a.s_out) inv_s = __frcp_rn(ld_f32(a.s_out));
-  // parts: the CTA that begins in the item or before it, and those after it
-  auto part = [&](int k) { return 2 * k + (start(k) < s0 ? 1 : 0); };
+  // Parts: of CTA c - 1, which begins in the item (its first unit) or before it
+  // (its second), and of those that begin after it: k < ctas s1 / total.  A CTA
+  // without a share (fewer tiles than CTAs) has none.
+  const int k0 = c - 1, k1 = (int)min((uint64_t)ctas, ((uint64_t)s1 * ctas + total - 1) / total);
+  const int first = 2 * k0 + (start(k0) < s0 ? 1 : 0);
+  auto lse = [&](int k) {
+    return total >= (uint32_t)ctas || start(k) < start(k + 1) ? a.part_lse[(int64_t)(k == k0 ? first : 2 * k) * unit_rows + r] : -INFINITY;
+  };
   float top = -INFINITY;
-  for (int k = c - 1; k < ctas && start(k) < s1; ++k)
-    if (start(k) < start(k + 1)) top = fmaxf(top, a.part_lse[(int64_t)part(k) * unit_rows + r]);
+#pragma unroll 8
+  for (int k = k0; k < k1; ++k) top = fmaxf(top, lse(k));
   if (top == -INFINITY) top = 0.0f;
   float sum = 0.0f, acc[16] = {};
-  for (int k = c - 1; k < ctas && start(k) < s1; ++k) {
-    if (start(k) == start(k + 1)) continue;
-    const float weight = exp2f(a.part_lse[(int64_t)part(k) * unit_rows + r] - top);
+#pragma unroll 4
+  for (int k = k0; k < k1; ++k) {
+    const float weight = exp2f(lse(k) - top);
+    const float4* src = reinterpret_cast<const float4*>(a.part) +
+                        (((int64_t)(k == k0 ? first : 2 * k) * groups + group) * (DP / 4) + 4 * chunk) * 32 + lane;
     sum += weight;
-    const float4* src = reinterpret_cast<const float4*>(a.part) + (((int64_t)part(k) * groups + group) * (DP / 4) + 4 * chunk) * 32 + lane;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float4 v = src[e * 32];
+      float4 v = src[e * 32];
+      if (weight == 0.0f) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);   // a part that nobody wrote
       acc[4 * e] = fmaf(weight, v.x, acc[4 * e]);
       acc[4 * e + 1] = fmaf(weight, v.y, acc[4 * e + 1]);
       acc[4 * e + 2] = fmaf(weight, v.z, acc[4 * e + 2]);
@@ -1108,10 +1116,12 @@ struct Plan {
   int64_t part_rows() const { return cut ? 2ll * ctas * unit_rows() : 0; }
 };
 
-// Whole items or cut ones: by an estimate of either's time, in units of a tile's
-// time (measured: about 1.75 us with 256 rows a unit; with 128 rows and two
-// tiles at once 0.7 us a tile).  Cutting costs the writing and joining of
-// the partial results, some 8 us.
+// Whole items or cut ones: by an estimate of either's time, in tiles of one CTA.
+// Cutting costs the writing and joining of the partial results and a second
+// launch: with 256 rows a unit the time of about 10 tiles (2 x 2000 queries,
+// 2000 keys, 16 heads: 65 us whole in 32 tiles, 74 cut in 27), with 128 rows about 8,
+// and the tiles get slower as more CTAs load at once (one token, 8 key heads: 2048 keys
+// 19.9 whole, 14.5 cut, 1024 keys 12.8 and 13.1; 8 tokens: 2048 keys 21.6 and 23.8 us).
 Plan make_plan(const AttnProblem& p, int sms) {
   Plan x;
   x.DP = p.D <= 64 ? 64 : 128;
@@ -1123,15 +1133,17 @@ Plan make_plan(const AttnProblem& p, int sms) {
   x.items = (int64_t)p.B * p.Hkv * x.blocks;
   const int64_t tiles = (p.Lk + kKeys - 1) / kKeys, total = x.items * tiles;
   x.groups = p.kv_len ? p.B : 1;
-  const int64_t share = (total + sms - 1) / sms, least = 4;   // tiles a CTA
+  const int64_t share = (total + sms - 1) / sms, least = x.shared ? 8 : 4;   // tiles a CTA
   const int64_t per = share > least ? share : least;
   const int64_t rounds = (x.items + sms - 1) / sms;
-  double whole = (double)(rounds * tiles), cut = (double)per + (x.shared ? 5.0 : 11.0);
-  // Lengths of their own make whole items uneven, the more so the fewer a CTA has.
+  double whole = (double)(rounds * tiles), mine = (double)per;
+  // Lengths of their own (by half of the range on average) make whole items
+  // uneven, the more so the fewer a CTA has.
   if (p.kv_len && p.B > 1) {
     whole *= rounds < 8 ? 1.0 : 0.8;
-    cut = (double)per * 0.8 + (x.shared ? 5.0 : 11.0);
+    mine *= 0.8;
   }
+  const double cut = x.shared ? mine + 10.0 : 1.4 * mine + 8.0;
   x.cut = cut < whole && total < (1ll << 31) && x.groups <= kMaxCutSamples;
   x.ctas = (int)(x.cut ? (total + per - 1) / per : x.items < sms ? x.items : sms);
   return x;
