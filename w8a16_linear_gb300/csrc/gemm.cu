@@ -35,7 +35,7 @@
 //        The scales are constant over k, so they stay in the epilogue, where a
 //        thread holds one token's row of the tile: its token scale is one
 //        register, the channel scales of a 64-column chunk are broadcast
-//        loads that L1 serves.
+//        loads that L1 serves.  20670 x 4096 x 4096: 193 us = 3.6 PFLOP/s.
 //  W8A16 (kind::f16, gemm_a16t_kernel below): the same product with the
 //        dequantized weight formed in TMEM inside the GEMM, for calls that
 //        provide no workspace.
