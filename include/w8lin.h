@@ -457,7 +457,7 @@ w8_status fp8_linear_w8a8_pertoken(const uint8_t* qx, int64_t M, int64_t K, cons
  * is a positive multiple of 8 (dimensions of one entry aside); the sample's
  * stride of q, k or v may be 0 where all samples share one array. */
 typedef struct {
-  int64_t B, Lq, Lk;     /* samples, queries, keys; any may be 0 */
+  int64_t B, Lq, Lk;     /* samples, queries, keys; any may be 0; Lk at most 2^26 */
   int64_t Hq, Hkv, D;    /* heads; Hq a multiple of Hkv, at most 128 times it; 8 <= D <= 128, D % 8 == 0;
                           * B * Hq * Lq at most 2^30 */
   int64_t q_stride[3], k_stride[3], v_stride[3], o_stride[3];
@@ -480,8 +480,9 @@ typedef struct {
  *   kv_len   [B] int32, device (clamped to 0 .. Lk), or NULL
  *   kv_mask  [B, Lk] bytes, device, nonzero where a key counts, or NULL
  *   s_out    NULL: out is of dtype, round16(o).  Device float scalar: out is
- *            E4M3_satRNE( fl32(o * fl32(1/s_out)) ), the codes that an
- *            out-projection with that input scale reads
+ *            E4M3_satRNE(o / s_out), the codes that an out-projection with that
+ *            input scale reads; o / s_out is a binary32 product of the
+ *            accumulator with 1 / sum and 1 / s_out, not rounded to dtype first
  *   out      [B, Lq, Hq, D] by o_stride, device, written
  *   ws       ws_floats floats, device, of which cross_attention_workspace()
  *            says how many the call needs (none when it says 0: may be NULL);
@@ -496,7 +497,8 @@ w8_status cross_attention(const w8_attention_desc* desc, const void* q, const vo
                           int64_t ws_floats, void* stream);
 
 /* Floats of workspace that cross_attention needs for these sizes on the
- * current device (it splits few queries along the keys).  Errors as above. */
+ * current device, with lengths or without (long key sides are cut into parts
+ * whose results stand there until they are joined).  Errors as above. */
 w8_status cross_attention_workspace(const w8_attention_desc* desc, int64_t* floats);
 
 /*

@@ -241,6 +241,25 @@ def test_lengths_of_many_samples(W, Lq, H, Hk):
         check(o, *exact(q, k, v, keep_of(B, 1500, lens)))
 
 
+@pytest.mark.parametrize("B,Lq,Lk,H,Hk,D", [(8, 1, 9000, 8, 2, 128), (100, 1, 6000, 2, 1, 64), (40, 1, 1500, 4, 4, 128),
+                                            (2, 1, 2100, 64, 64, 64), (2, 2000, 2000, 12, 12, 64)])
+def test_nothing_is_written_behind_the_workspace(W, B, Lq, Lk, H, Hk, D):
+    """Exactly the workspace that was asked for, with and without lengths: what
+    lies behind it keeps its contents."""
+    q, k, v = make(B, Lq, Lk, H, Hk, D, seed=17)
+    lens = torch.tensor([(b * 977) % (Lk + 1) for b in range(B)], dtype=torch.int32, device="cuda")
+    n = W.cross_attention_workspace(q, k, v).numel()
+    for kv_len in (lens, None):
+        mem = torch.full((n + 4096,), 3.0, device="cuda")
+        o = W.cross_attention(q, k, v, kv_len=kv_len, ws=mem[:n])
+        W.poll_device_error()
+        torch.cuda.synchronize()
+        assert (mem[n:] == 3.0).all()
+        rows = slice(0, 8) if Lq > 100 else slice(None)
+        ref, err = exact(q[:, rows], k, v, None if kv_len is None else keep_of(B, Lk, kv_len))
+        check(o[:, rows], ref, err)
+
+
 def test_a_workspace_too_small_is_refused(W):
     q, k, v = make(1, 1, 6000, 8, 2, 128)
     ws = W.cross_attention_workspace(q, k, v)

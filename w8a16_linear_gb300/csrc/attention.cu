@@ -1132,7 +1132,7 @@ struct Plan {
 // 2000 keys, 16 heads: 65 us whole in 32 tiles, 74 cut in 27), with 128 rows about 8,
 // and the tiles get slower as more CTAs load at once (one token, 8 key heads: 2048 keys
 // 19.9 whole, 14.5 cut, 1024 keys 12.8 and 13.1; 8 tokens: 2048 keys 21.6 and 23.8 us).
-Plan make_plan(const AttnProblem& p, int sms) {
+Plan make_plan(const AttnProblem& p, bool lens, int sms) {
   Plan x;
   x.DP = p.D <= 64 ? 64 : 128;
   x.G = p.Hq / p.Hkv;
@@ -1142,14 +1142,14 @@ Plan make_plan(const AttnProblem& p, int sms) {
   x.blocks = x.shared ? (slots + 1) / 2 : 1;
   x.items = (int64_t)p.B * p.Hkv * x.blocks;
   const int64_t tiles = (p.Lk + kKeys - 1) / kKeys, total = x.items * tiles;
-  x.groups = p.kv_len ? p.B : 1;
+  x.groups = lens ? p.B : 1;
   const int64_t share = (total + sms - 1) / sms, least = x.shared ? 8 : 4;   // tiles a CTA
   const int64_t per = share > least ? share : least;
   const int64_t rounds = (x.items + sms - 1) / sms;
   double whole = (double)(rounds * tiles), mine = (double)per;
   // Lengths of their own (by half of the range on average) make whole items
   // uneven, the more so the fewer a CTA has.
-  if (p.kv_len && p.B > 1) {
+  if (lens && p.B > 1) {
     whole *= rounds < 8 ? 1.0 : 0.8;
     mine *= 0.8;
   }
@@ -1211,13 +1211,20 @@ cudaError_t launch_type(const AttnMaps& maps, const AttnArgs& a, bool shared, in
 }  // namespace
 
 int64_t cross_attention_ws_floats(const AttnProblem& p, int sms) {
-  const Plan x = make_plan(p, sms);
-  return x.cut ? x.part_rows() * (x.DP + 1) + 2 * x.groups + 1 : 0;
+  // With lengths and without them items are cut by different rules, and the tile
+  // table has other sizes: enough for both, since the lengths come with the call.
+  int64_t most = 0;
+  for (int lens = 0; lens < 2; ++lens) {
+    const Plan x = make_plan(p, lens != 0, sms);
+    const int64_t n = x.cut ? x.part_rows() * (x.DP + 1) + 2 * x.groups + 1 : 0;
+    most = n > most ? n : most;
+  }
+  return most;
 }
 
 cudaError_t launch_cross_attention(const AttnProblem& p, int sms, cudaStream_t st, int* tmap_err) {
   *tmap_err = 0;
-  const Plan x = make_plan(p, sms);
+  const Plan x = make_plan(p, p.kv_len != nullptr, sms);
   AttnMaps maps;
   AttnArgs a;
   std::memset(&maps, 0, sizeof(maps));

@@ -99,7 +99,7 @@ struct AttnProblem {             // validated by the caller
   void* out;
   float* ws;                     // cross_attention_ws_floats() floats
 };
-int64_t cross_attention_ws_floats(const AttnProblem& p, int sms);
+int64_t cross_attention_ws_floats(const AttnProblem& p, int sms);   // by sizes alone: with lengths or without
 cudaError_t launch_cross_attention(const AttnProblem& p, int sms, cudaStream_t st, int* tmap_err);
 // Reads and clears the attention kernels' device error word (synchronises `st`).
 cudaError_t attention_read_error(cudaStream_t st, uint32_t* err);
