@@ -73,7 +73,8 @@ def test_cross_attention(L):
     assert L.cross_attention(None, P, P, P, NUL, NUL, NUL, P, NUL, 0, None) == 1
     assert f(dtype=1) == 5
     for bad in (dict(B=-1), dict(Lq=-1), dict(Lk=-1), dict(D=4), dict(D=136), dict(D=68), dict(Hq=3), dict(Hkv=0),
-                dict(Hq=0), dict(Hq=258), dict(B=1 << 20, Lq=1 << 20)):
+                dict(Hq=0), dict(Hq=258), dict(B=1 << 20, Lq=1 << 20),
+                dict(Lk=(1 << 26) + 1)):
         assert f(**bad) == 2, bad
     for scale in (0.0, -1.0, float("nan"), float("inf")):
         assert f(scale=scale) == 11

@@ -686,6 +686,8 @@ static w8_status check_attention(const char* fn, const w8_attention_desc* d, w8:
   if (d->Hq < 1 || d->Hkv < 1 || d->Hq % d->Hkv || d->Hq / d->Hkv > 128)
     return fail(W8_ERR_SHAPE, "%s: Hq=%lld Hkv=%lld (need Hq a multiple of Hkv, at most 128 times it)", fn,
                 (long long)d->Hq, (long long)d->Hkv);
+  // an item's keys have to be gone through well within the kernel's wait limit
+  if (d->Lk > (1ll << 26)) return fail(W8_ERR_SHAPE, "%s: Lk=%lld is above 2^26", fn, (long long)d->Lk);
   // work items are counted in 32 bits
   const double rows = (double)d->B * (double)d->Hq * (double)d->Lq;
   if (rows > (double)(1ll << 30)) return fail(W8_ERR_SHAPE, "%s: B * Hq * Lq = %.0f is above 2^30", fn, rows);

