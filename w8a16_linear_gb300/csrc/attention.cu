@@ -83,7 +83,8 @@ struct Cfg {
   static constexpr int kQ = 0;
   static constexpr int kRing = kQ + 2 * kTile;
   static constexpr int kOut = kRing + kStages * kTile;   // 32 rows of 128 bytes for each epilogue warp
-  static constexpr int kSum = kOut + 4 * 32 * 128;       // l[2][128], m[2][128]
+  static constexpr int kBound = kOut + 4 * 32 * 128;     // 128 bounds of scores for each softmax warp
+  static constexpr int kSum = kBound + 8 * kKeys * 4;    // l[2][128], m[2][128]
   static constexpr int kTab = kSum + 4 * kRows * 4;      // first tile and tiles per item of each sample
   static constexpr int kBar = kTab + (2 * kMaxCutSamples + 2) * 4;
   // full[S], empty[S], clean[S], q_full[2], q_empty[2], s_full[2], p_full[2],
@@ -627,6 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int i = warp >> 2;                     // slot
     const int row = (warp & 3) * 32 + lane;
     const uint32_t quad = (uint32_t)((warp & 3) * 32) << 16;
+    float4* bounds = reinterpret_cast<float4*>(smem + C::kBound) + warp * (kKeys / 4);
     uint32_t scount = 0, icount = 0;
     bool ok = true;
     Units<kLens> units(a, tab);
@@ -649,17 +651,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (kMask) ask(first_key(0));
       for (int j = 0; j < n; ++j) {
         const int key0 = first_key(j);
-        // Bit lane of word e: key 4 lane + e of the tile counts.
+        // A key's bound is +inf if it counts and -inf if not: the minimum of score
+        // and bound is one instruction a score, where bits of a word take three
+        // (and NaN scores of keys that do not count are gone too; one of a key that
+        // counts becomes +inf, which makes its row NaN all the same).
         // The masking and the rescaling below are kept out of the line of the
         // loop, which is long enough to weigh on the instruction cache.
         const bool masked = kMask || __builtin_expect(key0 + kKeys > x.len, 0);
-        uint32_t word[4];
         if (masked) {
+          float bound[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const bool on = kMask ? ahead[e] != 0 : key0 + 4 * lane + e < x.len;
-            word[e] = __ballot_sync(0xFFFFFFFFu, on);
-          }
+          for (int e = 0; e < 4; ++e)
+            bound[e] = (kMask ? ahead[e] != 0 : key0 + 4 * lane + e < x.len) ? INFINITY : -INFINITY;
+          bounds[lane] = make_float4(bound[0], bound[1], bound[2], bound[3]);
           if constexpr (kMask)
             if (j + 1 < n) ask(first_key(j + 1));
           __syncwarp();   // lanes past the last key took another path
@@ -684,8 +688,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!((word[e & 3] >> (8 * c + (e >> 2))) & 1)) r[c][e] = 0xFF800000u;
+            for (int e = 0; e < 32; e += 4) {
+              const float4 b = bounds[8 * c + e / 4];
+              r[c][e] = __float_as_uint(fminf(__uint_as_float(r[c][e]), b.x));
+              r[c][e + 1] = __float_as_uint(fminf(__uint_as_float(r[c][e + 1]), b.y));
+              r[c][e + 2] = __float_as_uint(fminf(__uint_as_float(r[c][e + 2]), b.z));
+              r[c][e + 3] = __float_as_uint(fminf(__uint_as_float(r[c][e + 3]), b.w));
+            }
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
