@@ -38,7 +38,9 @@ def check(y, qx, s_tok, w, c):
 @pytest.mark.parametrize("M,K,Ns", [(1, 16, (16,)), (1, 4096, (4096,)), (1, 4096, (1024, 16, 528)), (2, 272, (144,)),
                                     (7, 1008, (256, 256)), (16, 16384, (512,)), (17, 2064, (1040,)), (33, 512, (400,)),
                                     (64, 4096, (1024, 1024)), (100, 1024, (4096, 1024, 1024)), (127, 528, (272,)),
-                                    (128, 4096, (512,)), (129, 4096, (512, 80)), (300, 1040, (656,)), (1000, 768, (2064,))])
+                                    (128, 4096, (512,)), (129, 4096, (512, 80)), (300, 1040, (656,)), (1000, 768, (2064,)),
+                                    (60, 528, (12288, 8208)), (300, 528, (6992,)), (1100, 784, (2064, 1040)),
+                                    (32, 512, (16384, 8208))])
 def test_against_64_bits(W, M, K, Ns):
     qx, s_tok, ws, cs = make(M, K, Ns, seed=M + K)
     ys = W.fp8_linear_w8a8_pertoken_group(qx, s_tok, ws, cs)
@@ -51,7 +53,8 @@ def test_against_64_bits(W, M, K, Ns):
     check(one, qx, s_tok, ws[0], cs[0])
 
 
-@pytest.mark.parametrize("M,K,N", [(1, 1024, 272), (5, 4096, 512), (40, 2048, 528), (150, 1024, 512), (600, 640, 304)])
+@pytest.mark.parametrize("M,K,N", [(1, 1024, 272), (5, 4096, 512), (40, 2048, 528), (150, 1024, 512), (600, 640, 304),
+                                   (100, 272, 20496), (1100, 640, 2320)])
 def test_exact_sums(W, M, K, N):
     g = torch.Generator(device="cuda").manual_seed(K + M)
     a = torch.randint(-4, 5, (M, K), generator=g, device="cuda").float()
@@ -67,7 +70,7 @@ def test_exact_sums(W, M, K, N):
 def test_a_scale_belongs_to_its_token_and_channel(W):
     """NaN or infinite scales reach their own row and column only; the bytes
     behind the output stay as they were."""
-    for M, N in ((3, 272), (200, 272)):
+    for M, N in ((3, 272), (200, 272), (1100, 2320), (70, 20496)):
         qx, s_tok, ws, cs = make(M, 512, (N,), seed=8)
         whole = torch.full((M + 1, N), -7.0, dtype=torch.bfloat16, device="cuda")
         s_tok[1] = float("nan")

@@ -1392,11 +1392,15 @@ cudaError_t launch_few(const GemmProblem& p, int sms, cudaStream_t st, int* tmap
   return launch_cluster(gemm_few_kernel, tiles * a.split, kThreads, a.stages * stage + kTail, a.split, st, maps, a);
 }
 
-// Few tokens: tiles of gemm_kernel that would fill less than half of the GPU.
+// Few tokens, or outputs whose 128 x 128 tiles are no more than the SMs.  us,
+// K = 4096, gemm_kernel / gemm_few_kernel: 512 x 4096 (128 tiles) 18.9 / 14.0, 512 x 6144
+// (192) 19.3 / 20.0, 1000 x 2048 (128) 18.2 / 13.8, 1000 x 2560 (160) 18.2 / 19.0,
+// 128 x 2 x 16384 (256) 28.4 / 32.3; of more tiles than SMs 1 x 3 x 16384 51.0 / 37.6,
+// 32 x 3 x 16384 45.5 / 40.5, 32 x 2 x 16384 27.3 / 27.2, 64 x 2 x 16384 27.5 / 28.9.
 bool use_few(const GemmProblem& p, int sms) {
   int64_t tiles = 0;
-  for (int g = 0; g < p.G; ++g) tiles += (p.M + 2 * BM - 1) / (2 * BM) * ((p.N[g] + 255) / 256);
-  return p.M <= BM || 4 * tiles <= sms;
+  for (int g = 0; g < p.G; ++g) tiles += (p.M + 127) / 128 * ((p.N[g] + few::BW - 1) / few::BW);
+  return p.M <= 32 || tiles <= sms;
 }
 
 cudaError_t launch_gemm_w8a8_token(const GemmProblem& p, int sms, cudaStream_t st, int* tmap_err) {
