@@ -579,6 +579,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       Units<kLens> units(a, tab);
       Item x;
       while (ok && units.next(x)) {
+        // The mask of a tile's keys lane + 32 e, asked for a V tile ahead: its
+        // latency would stand before the clearing of every tile.
+        uint32_t ahead[4];
+        const auto ask = [&](int tile) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = tile * kKeys + 32 * e + lane;
+            ahead[e] = 0;
+            if (j < x.len) ahead[e] = load_mask(a.kv_mask + x.b * a.mask_stride + j);
+          }
+        };
+        if constexpr (kMask) ask(x.t0);
         ok = walk(x, [&](bool is_v, int ring, int tile) {
           const uint32_t e = ring ? seen[1]++ : seen[0]++;
           const int st = stage_of(ring, e);
@@ -593,9 +605,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int j = tile * kKeys + 32 * e + lane;
               bool off = j < a.Lk && j >= x.len;
               if constexpr (kMask)
-                if (j < x.len) off = load_mask(a.kv_mask + x.b * a.mask_stride + j) == 0;
+                if (j < x.len) off = ahead[e] == 0;
               word[e] = __ballot_sync(0xFFFFFFFFu, off);
             }
+            if constexpr (kMask)
+              if (tile + 1 < x.t1) ask(tile + 1);
+            __syncwarp();   // lanes past the last key took another path
           }
           if (!pass && !mbar_wait_warp(full_bar(st), phase_of(e), abort, kWaitLimitNs)) return false;
           if (word[0] | word[1] | word[2] | word[3]) {
@@ -603,9 +618,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* v = smem + C::kRing + st * C::kTile + (lane & 7) * 16;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-#pragma unroll 1
+#pragma unroll
               for (int k = 0; k < 32; k += 4) {
-                if (!(word[e] >> k & 15)) continue;
                 const int r = k + (lane >> 3);
                 if (word[e] >> r & 1)
 #pragma unroll
