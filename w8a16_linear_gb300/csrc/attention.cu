@@ -33,7 +33,7 @@
 // Measured (GB300): 4096 queries over 20670 keys, 32 query and 8 key heads of 128:
 // 937 us = 1.48 PFLOP/s, 0.76 of the measured bf16 peak; 41340 queries over
 // prompts of 256 to 512 keys, 32 heads, E4M3 out: 276 us = 0.94 PFLOP/s; 8 single tokens
-// over 10335 to 20670 keys: 98 us = 5.2 TB/s, 0.77 of the measured copy, joining included.
+// over 10335 to 20670 keys: 96 us = 5.3 TB/s, 0.79 of the measured copy, joining included.
 // What bounds the first is the way from a tile's scores to the next tile's: 512
 // cycles of scores, some 1450 of softmax, 256 of P V and four hand-overs
 // of about 200, in which both slots together use the tensor core 2048 cycles;
