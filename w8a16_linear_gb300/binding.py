@@ -582,6 +582,16 @@ def _raw_stream(stream):
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory that a call on ``stream`` (None: the current one) allocates.  It
+    comes from that stream's pool: of another stream's, the allocator could hand
+    it to a tensor there while the call's kernels are still to use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _refuse(t, name, dtypes, shape=None, numel=None):
     """Raises what is wrong with ``t`` (wanted: a dense CUDA tensor of one of
     ``dtypes`` and of this shape or number of values)."""
@@ -627,12 +637,12 @@ def add_rms_norm_quant(x, residual, weight, eps=1e-6, s_in=None, out=None, s_tok
     if residual is not None:
         p_r = _like(residual, "residual", same, shape)
         if res_out is None:
-            res_out = torch.empty_like(x)
+            res_out = _empty(shape, dtype, x.device, stream)
         p_ro = _like(res_out, "res_out", same, shape)
     elif res_out is not None:
         raise W8Error(1, "res_out without a residual")
     if out is None:
-        out = torch.empty(shape, dtype=torch.uint8, device=x.device)
+        out = _empty(shape, torch.uint8, x.device, stream)
     p_q = _like(out, "out", _CODES, shape)
     if s_in is not None:
         if s_tok is not None:
@@ -640,7 +650,7 @@ def add_rms_norm_quant(x, residual, weight, eps=1e-6, s_in=None, out=None, s_tok
         p_in = _floats(s_in, "s_in", 1)
     else:
         if s_tok is None:
-            s_tok = torch.empty((M,), dtype=torch.float32, device=x.device)
+            s_tok = _empty((M,), torch.float32, x.device, stream)
         p_tok = _floats(s_tok, "s_tok", M)
     if h_out is not None:
         p_h = _like(h_out, "h_out", same, shape)
@@ -666,7 +676,7 @@ def fp8_linear_w8a8_pertoken_group(qx, s_tok, weights, channel_scales, outs=None
     p_w = [_like(w, "w", _CODES, (n, K)) for w, n in zip(weights, ns)]
     p_s = [_floats(c, "s_ch", n) for c, n in zip(channel_scales, ns)]
     if outs is None:
-        outs = [torch.empty((*lead, n), dtype=torch.bfloat16, device=qx.device) for n in ns]
+        outs = [_empty((*lead, n), torch.bfloat16, qx.device, stream) for n in ns]
     p_y = [_like(y, "y", (torch.bfloat16,), (*lead, n)) for y, n in zip(outs, ns)]
     ptrs = ctypes.c_void_p * G
     _check(lib().fp8_linear_w8a8_pertoken(qx.data_ptr(), M, K, _floats(s_tok, "s_tok", M), G, ptrs(*p_w),
@@ -755,7 +765,7 @@ def cross_attention(q, k, v, kv_len=None, kv_mask=None, scale=None, s_out=None, 
         kinds = _CODES
         p_s = _floats(s_out, "s_out", 1)
     if out is None:
-        out = torch.empty(shape, dtype=kinds[0], device=device)
+        out = _empty(shape, kinds[0], device, stream)
     elif out.shape != shape:
         raise W8Error(2, f"out: shape {tuple(out.shape)} differs from q {tuple(q.shape)}")
     so = _heads(out, "out", kinds, device)
@@ -766,7 +776,7 @@ def cross_attention(q, k, v, kv_len=None, kv_mask=None, scale=None, s_out=None, 
         n = ctypes.c_int64(0)
         _check(L.cross_attention_workspace(desc, ctypes.byref(n)))
         if n.value:
-            ws = torch.empty((n.value,), dtype=torch.float32, device=device)
+            ws = _empty((n.value,), torch.float32, device, stream)
     if ws is not None:
         n_ws = ws.numel()
         p_ws = _floats(ws, "ws", n_ws)
