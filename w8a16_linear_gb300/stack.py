@@ -160,7 +160,13 @@ class CrossSite:
 
     ``encode`` makes the keys and values, once for all denoising steps (or all
     tokens of an answer); ``run`` is one pass over ``M = batch * tokens`` rows.
-    Buffers are the site's own, so that a pass can be captured in a CUDA graph."""
+    Buffers are the site's own, so that a pass can be captured in a CUDA graph.
+    A graph holds K, V and their workspace by address, so a captured pass
+    makes the site keep those of its number of positions: ``encode`` writes
+    states of as many positions into them, and the graph then attends to
+    those (``encode`` has to follow the last pass over the old ones, as it does on one
+    stream); states of other lengths leave them alone.  The site has to live as
+    long as the graph."""
 
     def __init__(self, batch, tokens, hidden, heads, kv_heads, head_dim, device):
         self.B, self.L, self.H = batch, tokens, hidden
@@ -175,18 +181,26 @@ class CrossSite:
         self.attn = torch.empty((batch, tokens, heads, head_dim), **u8)
         self.y = torch.empty((M, hidden), **bf)
         self.k = self.v = self.ws = None
+        self.captured = {}                            # positions -> (k, v, ws) that a graph holds
 
     def encode(self, W, w, states):
         """Keys and values of ``states`` [batch, positions, E] (bfloat16)."""
         B, T, E = states.shape
         codes, s_tok, _ = W.add_rms_norm_quant(states.reshape(B * T, E), None, w.enc_norm)
-        kv = W.fp8_linear_w8a8_pertoken_group(codes, s_tok, [w.k[0], w.v[0]], [w.k[1], w.v[1]])
+        held = self.captured.get(T)
+        outs = [t.view(B * T, -1) for t in held[:2]] if held else None
+        kv = W.fp8_linear_w8a8_pertoken_group(codes, s_tok, [w.k[0], w.v[0]], [w.k[1], w.v[1]], outs=outs)
+        if held:
+            self.k, self.v, self.ws = held
+            return
         self.k, self.v = (t.view(B, T, self.kv_heads, self.D) for t in kv)
         self.ws = W.cross_attention_workspace(self.q.view(B, self.L, self.heads, self.D), self.k, self.v)
 
     def run(self, W, w, x, residual, kv_len=None, kv_mask=None):
         """One pass on the current stream: returns the out-projection's output
         (``y``) and the sum of ``x`` and ``residual`` (``res``), [M, hidden]."""
+        if torch.cuda.is_current_stream_capturing():
+            self.captured[self.k.shape[1]] = (self.k, self.v, self.ws)
         W.add_rms_norm_quant(x, residual, w.norm, out=self.codes, s_tok=self.s_tok, res_out=self.res)
         W.fp8_linear_w8a8_pertoken(self.codes, self.s_tok, w.q[0], w.q[1], out=self.q)
         q = self.q.view(self.B, self.L, self.heads, self.D)
