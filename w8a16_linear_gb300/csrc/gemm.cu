@@ -1184,10 +1184,12 @@ bool encode_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint6
   return r == CUDA_SUCCESS;
 }
 
+// max_smem is the most that any launch of `kern` takes: the attribute belongs to
+// the kernel, and another host thread may set it between this call and the launch.
 template <typename A>
-cudaError_t launch_cluster(void (*kern)(Maps, A), int grid, int threads, int smem, int cg,
+cudaError_t launch_cluster(void (*kern)(Maps, A), int grid, int threads, int smem, int max_smem, int cg,
                            cudaStream_t st, const Maps& maps, const A& args) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid, 1, 1);
@@ -1275,7 +1277,7 @@ cudaError_t launch(const GemmProblem& p, int sms, cudaStream_t st, int* tmap_err
   if (!kGlu && CG == 2 && tail > 0 && 2 * tail <= clusters) args.tail_split = 2;
   args.num_full = args.num_tiles - (args.tail_split > 1 ? tail : 0);
   args.num_units = args.num_full + (args.num_tiles - args.num_full) * args.tail_split;
-  return launch_cluster(gemm_kernel<MODE, CG>, clusters * CG, L::kThreads, L::kAlloc, CG, st, maps,
+  return launch_cluster(gemm_kernel<MODE, CG>, clusters * CG, L::kThreads, L::kAlloc, L::kAlloc, CG, st, maps,
                         args);
 }
 
@@ -1389,7 +1391,7 @@ cudaError_t launch_few(const GemmProblem& p, int sms, cudaStream_t st, int* tmap
   a.stages = ((tiles * a.split > sms ? kHalfSmem : kMaxSmem) - kTail) / stage;
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   // the partial sums go over the ring
-  return launch_cluster(gemm_few_kernel, tiles * a.split, kThreads, a.stages * stage + kTail, a.split, st, maps, a);
+  return launch_cluster(gemm_few_kernel, tiles * a.split, kThreads, a.stages * stage + kTail, kMaxSmem, a.split, st, maps, a);
 }
 
 // Few tokens, or outputs whose 128 x 128 tiles are no more than the SMs.  us,
