@@ -73,15 +73,27 @@ namespace w8 {
 
 EncodeTiledFn get_encode_tiled() {
   static EncodeTiledFn fn = nullptr;
+  static CUresult (*current_context)(CUcontext*) = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
+    auto entry = [](const char* name, unsigned version) -> void* {
+      void* p = nullptr;
+      cudaDriverEntryPointQueryResult q;
+      const bool found = cudaGetDriverEntryPointByVersion(name, &p, version, cudaEnableDefault, &q) == cudaSuccess &&
+                         q == cudaDriverEntryPointSuccess;
+      return found ? p : nullptr;
+    };
+    current_context = reinterpret_cast<CUresult (*)(CUcontext*)>(entry("cuCtxGetCurrent", 4000));
+    if (current_context) fn = reinterpret_cast<EncodeTiledFn>(entry("cuTensorMapEncodeTiled", 12000));
   });
+  if (!fn) return nullptr;
+  // Encoding needs a current context.  A host thread whose first CUDA work is
+  // this call has none yet; setting the device that it is on anyway binds one.
+  CUcontext ctx = nullptr;
+  if (current_context(&ctx) != CUDA_SUCCESS || !ctx) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return nullptr;
+  }
   return fn;
 }
 
