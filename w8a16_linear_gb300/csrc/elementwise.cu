@@ -348,6 +348,10 @@ int ln_stages(int K) {
 // Bytes of the modulation table (fl32(1 + scale), shift) of the kT = 64 forms.
 int ln_table_bytes(int K) { return K <= 4096 ? 8 * K : 0; }
 
+// The most that a launch takes of both.  A kernel's limit is set to this and not
+// to the launch's own size: another host thread may set it in between.
+constexpr int kLnMaxSmem = kLnRingBytes + 8 * 4096;
+
 __device__ uint32_t g_elem_err;                // kErrTimeout when a row-buffer wait gives up
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -753,7 +757,7 @@ cudaError_t launch_ln_modulate_quant(const uint16_t* x, int64_t M, int K, const 
 #define W8_LN_LAUNCH(T, V, SLOT)                                                                      \
   {                                                                                                  \
     auto k = K == 8 * T * V ? W8_LN_KERNEL(T, V, true) : W8_LN_KERNEL(T, V, false);                   \
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);      \
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kLnMaxSmem); \
     if (e != cudaSuccess) return e;                                                                  \
     std::atomic<int>& o = occ[3 * (SLOT) + out - 1];                                                 \
     int b = o.load(std::memory_order_relaxed);                                                       \
