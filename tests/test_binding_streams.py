@@ -41,3 +41,32 @@ def test_allocations_are_made_on_the_calls_stream(rec, call, n):
     call(rec.b, None)                                  # the current stream's own pool
     assert [s for _, s in rec.allocations] == [None] * n
     assert rec.library.calls[-1][1][-1] == 0
+
+
+def _scale():
+    return fake(1, dtype=torch.float32)
+
+
+def _w8a8(b, stream):
+    return b.fp8_linear_w8a8(fake(3, 64), fake(32, 64, dtype=torch.uint8), _scale(), _scale(), out=fake(3, 32), stream=stream)
+
+
+def _group(b, stream):
+    w = fake(32, 64, dtype=torch.uint8)
+    return b.qkv_shared_quant_gemm(b.MODE_A8, fake(3, 64), _scale(), [w, w], [_scale(), _scale()], outs=[fake(3, 32), fake(3, 32)],
+                                   stream=stream)
+
+
+def _gate_up(b, stream):
+    w, s = fake(32, 64, dtype=torch.uint8), _scale()
+    return b.gate_up_swiglu_fp8(fake(3, 64), s, w, w, s, s, s, out=fake(3, 32, dtype=torch.uint8), stream=stream)
+
+
+@pytest.mark.parametrize("call", [_w8a8, _group, _gate_up])
+def test_temporary_codes_are_allocated_on_the_calls_stream(rec, call):
+    st = FakeStream()
+    call(rec.b, st)
+    assert rec.allocations == [((3, 64), st)]
+    rec.allocations.clear()
+    call(rec.b, None)
+    assert rec.allocations == [((3, 64), None)]

@@ -54,3 +54,21 @@ def test_a_chain_on_a_stream_given_to_each_call(W):
         for a, b in zip(got, want):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
         assert all(bool((t == 9).all()) for t in others)
+
+
+def test_w8a8_from_bf16_without_a_workspace_on_its_own_stream(W):
+    """The codes of the activation stand in a workspace of the call's own."""
+    g = torch.Generator(device="cuda").manual_seed(23)
+    x = torch.randn((4000, 2048), generator=g, device="cuda").bfloat16()
+    m = (torch.randn((1024, 2048), generator=g, device="cuda") * 100).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    s = torch.full((1,), 0.01, device="cuda")
+    out = torch.empty((4000, 1024), dtype=torch.bfloat16, device="cuda")
+    want = W.fp8_linear_w8a8(x, m, s, s)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    for i in range(20):
+        W.fp8_linear_w8a8(x, m, s, s, out=out, stream=st)
+        others = [torch.full((4000, 2048), i, dtype=torch.uint8, device="cuda") for _ in range(3)]
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+        assert all(bool((t == i).all()) for t in others)

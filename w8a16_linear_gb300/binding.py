@@ -147,6 +147,16 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory that a call on ``stream`` (None: the current one) allocates.  It
+    comes from that stream's pool: of another stream's, the allocator could hand
+    it to a tensor there while the call's kernels are still to use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _dense(t, name):
     if not t.is_contiguous():
         raise W8Error(4, f"{name}: non-contiguous tensors are rejected")
@@ -288,7 +298,7 @@ def fp8_linear_w8a8(x, w, s_in, s_w, out=None, ws=None, stream=None):
         out = torch.empty(*x.shape[:-1], N, dtype=torch.bfloat16, device=x.device)
     _as_bf16(out, "out")
     if dt == DTYPE_BF16 and ws is None:
-        ws = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+        ws = _empty((M, K), torch.uint8, x.device, stream)
     _check(lib().fp8_linear_w8a8(_ptr(x2), dt, M, K, _ptr(wq), N, _ptr(_scalar(s_in, "s_in")),
                                  _ptr(_scalar(s_w, "s_w")), _ptr(out),
                                  _ptr(_as_u8(ws, "ws") if ws is not None else None), _stream(stream)))
@@ -329,7 +339,7 @@ def qkv_shared_quant_gemm(mode, x, s_in, weights, weight_scales, outs=None, ws=N
     for i, o in enumerate(outs):
         _as_bf16(o, f"y[{i}]")
     if mode == MODE_A8 and ws is None:
-        ws = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+        ws = _empty((M, K), torch.uint8, x.device, stream)
     if mode == MODE_A8 or ws is None:
         ws_p = _ptr(_as_u8(ws, "ws") if ws is not None else None)
     else:   # A16 with a workspace: room for the group's dequantized bf16 weights
@@ -461,7 +471,7 @@ def gate_up_swiglu_fp8(x, s_in, w_gate, w_up, s_w_gate, s_w_up, s_out, out=None,
         out = torch.empty(*x.shape[:-1], I, dtype=torch.uint8, device=x.device)
     o = _as_u8(out, "out")
     if dt == DTYPE_BF16 and ws is None:
-        ws = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+        ws = _empty((M, K), torch.uint8, x.device, stream)
     wsp = _ptr(_as_u8(ws, "ws") if ws is not None else None)
     if limit is None and alpha is None and beta is None:
         _check(lib().gate_up_swiglu_fp8(_ptr(x2), dt, M, K, _ptr(_scalar(s_in, "s_in")), _ptr(wg), _ptr(wu), I,
@@ -580,16 +590,6 @@ def _raw_stream(stream):
     if stream is not None:
         return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-
-
-def _empty(shape, dtype, device, stream):
-    """Memory that a call on ``stream`` (None: the current one) allocates.  It
-    comes from that stream's pool: of another stream's, the allocator could hand
-    it to a tensor there while the call's kernels are still to use it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _refuse(t, name, dtypes, shape=None, numel=None):
