@@ -586,33 +586,40 @@ _DTYPE16 = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
 _CODES = tuple(t for t in (torch.uint8, getattr(torch, "float8_e4m3fn", None)) if t is not None)
 
 
-def _raw_stream(stream):
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+def _raw_stream(stream, device):
+    """The stream's handle; ``device`` (the operands') has to be the current
+    device, on which the library launches, and the stream's."""
+    here = torch._C._cuda_getDevice()
+    if device.index != here or (stream is not None and stream.device != device):
+        raise W8Error(1, f"operands on {device}, launch on cuda:{here}"
+                         + ("" if stream is None else f" and a stream of {stream.device}"))
+    return torch._C._cuda_getCurrentRawStream(here) if stream is None else stream.cuda_stream
 
 
-def _refuse(t, name, dtypes, shape=None, numel=None):
-    """Raises what is wrong with ``t`` (wanted: a dense CUDA tensor of one of
-    ``dtypes`` and of this shape or number of values)."""
+def _refuse(t, name, dtypes, device, shape=None, numel=None):
+    """Raises what is wrong with ``t`` (wanted: a dense tensor on ``device``, of
+    one of ``dtypes`` and of this shape or number of values)."""
     _dense(t, name)
+    if t.device != device:
+        raise W8Error(1, f"{name}: on {t.device}, the other operands on {device}")
     if t.dtype not in dtypes:
         raise W8Error(5, f"{name}: expected {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     want = tuple(shape) if shape is not None else numel
     raise W8Error(2 if shape is not None else 5, f"{name}: shape {tuple(t.shape)}, expected {want}")
 
 
-def _like(t, name, dtypes, shape):
-    """data_ptr of ``t``, a dense CUDA tensor of one of ``dtypes`` and of ``shape``."""
-    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        _refuse(t, name, dtypes, shape=shape)
+def _like(t, name, dtypes, shape, device):
+    """data_ptr of ``t``, a dense tensor on ``device`` (a CUDA device) of one of
+    ``dtypes`` and of ``shape``."""
+    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous() or t.device != device:
+        _refuse(t, name, dtypes, device, shape=shape)
     return t.data_ptr()
 
 
-def _floats(t, name, n):
-    """data_ptr of ``t``, n dense float32 values on the device."""
-    if t.dtype is not torch.float32 or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
-        _refuse(t, name, (torch.float32,), numel=n)
+def _floats(t, name, n, device):
+    """data_ptr of ``t``, n dense float32 values on ``device``."""
+    if t.dtype is not torch.float32 or t.numel() != n or not t.is_contiguous() or t.device != device:
+        _refuse(t, name, (torch.float32,), device, numel=n)
     return t.data_ptr()
 
 
@@ -624,7 +631,7 @@ def add_rms_norm_quant(x, residual, weight, eps=1e-6, s_in=None, out=None, s_tok
     tokens' scales (None with ``s_in``) and the sum in 16 bits (None without a
     residual).  ``res_out`` may be ``residual`` itself; ``h_out`` receives the
     norm in 16 bits when given."""
-    dtype, shape = x.dtype, x.shape
+    dtype, shape, device = x.dtype, x.shape, x.device
     dt = _DTYPE16.get(dtype)
     if dt is None or not x.is_contiguous() or not x.is_cuda or not shape:
         _as_16(x, "x")
@@ -632,30 +639,30 @@ def add_rms_norm_quant(x, residual, weight, eps=1e-6, s_in=None, out=None, s_tok
     same = (dtype,)
     K = shape[-1]
     M = x.numel() // K if K else 0
-    p_w = _like(weight, "weight", same, (K,))
+    p_w = _like(weight, "weight", same, (K,), device)
     p_r = p_ro = p_in = p_tok = p_h = None
     if residual is not None:
-        p_r = _like(residual, "residual", same, shape)
+        p_r = _like(residual, "residual", same, shape, device)
         if res_out is None:
-            res_out = _empty(shape, dtype, x.device, stream)
-        p_ro = _like(res_out, "res_out", same, shape)
+            res_out = _empty(shape, dtype, device, stream)
+        p_ro = _like(res_out, "res_out", same, shape, device)
     elif res_out is not None:
         raise W8Error(1, "res_out without a residual")
     if out is None:
-        out = _empty(shape, torch.uint8, x.device, stream)
-    p_q = _like(out, "out", _CODES, shape)
+        out = _empty(shape, torch.uint8, device, stream)
+    p_q = _like(out, "out", _CODES, shape, device)
     if s_in is not None:
         if s_tok is not None:
             raise W8Error(11, "s_in and s_tok: one of them")
-        p_in = _floats(s_in, "s_in", 1)
+        p_in = _floats(s_in, "s_in", 1, device)
     else:
         if s_tok is None:
-            s_tok = _empty((M,), torch.float32, x.device, stream)
-        p_tok = _floats(s_tok, "s_tok", M)
+            s_tok = _empty((M,), torch.float32, device, stream)
+        p_tok = _floats(s_tok, "s_tok", M, device)
     if h_out is not None:
-        p_h = _like(h_out, "h_out", same, shape)
+        p_h = _like(h_out, "h_out", same, shape, device)
     _check(lib().add_rms_norm_quant(x.data_ptr(), p_r, dt, M, K, p_w, eps, p_in, p_tok, p_q, p_h, p_ro,
-                                    _raw_stream(stream)))
+                                    _raw_stream(stream, device)))
     return out, s_tok, res_out
 
 
@@ -663,7 +670,7 @@ def fp8_linear_w8a8_pertoken_group(qx, s_tok, weights, channel_scales, outs=None
     """G W8A8 projections of an activation whose tokens have scales of their own
     (``s_tok``, one float32 a token), on weights with one scale for each output
     channel."""
-    lead = qx.shape[:-1]
+    lead, device = qx.shape[:-1], qx.device
     if qx.dtype not in _CODES or not qx.is_contiguous() or not qx.is_cuda or not qx.shape:
         _as_u8(qx, "qx")
         raise W8Error(2, "qx: expected at least one dimension")
@@ -673,14 +680,14 @@ def fp8_linear_w8a8_pertoken_group(qx, s_tok, weights, channel_scales, outs=None
     if len(channel_scales) != G or (outs is not None and len(outs) != G):
         raise W8Error(2, f"{G} weights: as many sets of channel scales and outputs are wanted")
     ns = [w.shape[0] for w in weights]
-    p_w = [_like(w, "w", _CODES, (n, K)) for w, n in zip(weights, ns)]
-    p_s = [_floats(c, "s_ch", n) for c, n in zip(channel_scales, ns)]
+    p_w = [_like(w, "w", _CODES, (n, K), device) for w, n in zip(weights, ns)]
+    p_s = [_floats(c, "s_ch", n, device) for c, n in zip(channel_scales, ns)]
     if outs is None:
-        outs = [_empty((*lead, n), torch.bfloat16, qx.device, stream) for n in ns]
-    p_y = [_like(y, "y", (torch.bfloat16,), (*lead, n)) for y, n in zip(outs, ns)]
+        outs = [_empty((*lead, n), torch.bfloat16, device, stream) for n in ns]
+    p_y = [_like(y, "y", (torch.bfloat16,), (*lead, n), device) for y, n in zip(outs, ns)]
     ptrs = ctypes.c_void_p * G
-    _check(lib().fp8_linear_w8a8_pertoken(qx.data_ptr(), M, K, _floats(s_tok, "s_tok", M), G, ptrs(*p_w),
-                                          (ctypes.c_int64 * G)(*ns), ptrs(*p_s), ptrs(*p_y), _raw_stream(stream)))
+    _check(lib().fp8_linear_w8a8_pertoken(qx.data_ptr(), M, K, _floats(s_tok, "s_tok", M, device), G, ptrs(*p_w),
+                                          (ctypes.c_int64 * G)(*ns), ptrs(*p_s), ptrs(*p_y), _raw_stream(stream, device)))
     return outs
 
 
@@ -748,14 +755,14 @@ def cross_attention(q, k, v, kv_len=None, kv_mask=None, scale=None, s_out=None, 
     p_len = p_mask = p_s = p_ws = None
     mask_stride = n_ws = 0
     if kv_len is not None:
-        if kv_len.dtype is not torch.int32 or kv_len.numel() != B or not kv_len.is_contiguous() or not kv_len.is_cuda:
-            _refuse(kv_len, "kv_len", (torch.int32,), numel=B)
+        if kv_len.dtype is not torch.int32 or kv_len.numel() != B or not kv_len.is_contiguous() or kv_len.device != device:
+            _refuse(kv_len, "kv_len", (torch.int32,), device, numel=B)
         p_len = kv_len.data_ptr()
     if kv_mask is not None:
         if kv_mask.dtype not in (torch.bool, torch.uint8) or kv_mask.shape != (B, Lk):
             raise W8Error(5, f"kv_mask: expected bool or uint8 [{B}, {Lk}]")
-        if not kv_mask.is_cuda:
-            raise W8Error(1, "kv_mask: must be a CUDA tensor")
+        if kv_mask.device != device:
+            raise W8Error(1, "kv_mask: must be a CUDA tensor on q's device")
         if Lk > 1 and kv_mask.stride(1) != 1:
             raise W8Error(4, "kv_mask: a sample's keys must be contiguous")
         mask_stride = kv_mask.stride(0)
@@ -763,7 +770,7 @@ def cross_attention(q, k, v, kv_len=None, kv_mask=None, scale=None, s_out=None, 
     kinds = same
     if s_out is not None:
         kinds = _CODES
-        p_s = _floats(s_out, "s_out", 1)
+        p_s = _floats(s_out, "s_out", 1, device)
     if out is None:
         out = _empty(shape, kinds[0], device, stream)
     elif out.shape != shape:
@@ -779,9 +786,9 @@ def cross_attention(q, k, v, kv_len=None, kv_mask=None, scale=None, s_out=None, 
             ws = _empty((n.value,), torch.float32, device, stream)
     if ws is not None:
         n_ws = ws.numel()
-        p_ws = _floats(ws, "ws", n_ws)
+        p_ws = _floats(ws, "ws", n_ws, device)
     _check(L.cross_attention(desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), p_len, p_mask, p_s, out.data_ptr(), p_ws,
-                             n_ws, _raw_stream(stream)))
+                             n_ws, _raw_stream(stream, device)))
     return out
 
 
