@@ -721,14 +721,27 @@ def _heads(t, name, dtypes, device):
     return sb, sl, sh
 
 
+def _attention_inputs(q, k, v):
+    """(strides of q, k and v, sizes (B, Lq, Lk, Hq, Hkv, D), dtype code)."""
+    dt, device = _DTYPE16.get(q.dtype), q.device
+    if dt is None:
+        raise W8Error(5, f"q: expected bfloat16 or float16, got {q.dtype}")
+    same = (q.dtype,)
+    st = (*_heads(q, "q", same, device), *_heads(k, "k", same, device), *_heads(v, "v", same, device))
+    B, Lq, H, D = q.shape
+    if k.shape != v.shape or k.shape[0] != B or k.shape[3] != D:
+        raise W8Error(2, f"q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)} do not fit together")
+    return st, (B, Lq, k.shape[1], H, k.shape[2], D), dt
+
+
 def cross_attention_workspace(q, k, v):
     """float32 scratch for cross_attention(q, k, v, ..., ws=...) of these shapes
     (caller-side allocation; empty when none is needed)."""
+    st, sizes, dt = _attention_inputs(q, k, v)
+    B, Lq, _, H, _, D = sizes
     n = ctypes.c_int64(0)
-    B, Lq, H, D = q.shape
-    st = [_heads(t, name, tuple(_DTYPE16), q.device) for t, name in ((q, "q"), (k, "k"), (v, "v"))]
-    desc = _attention_desc(B, Lq, k.shape[1], H, k.shape[2], D, *st[0], *st[1], *st[2], *st[0], 0, _DTYPE16[q.dtype],
-                           D ** -0.5)
+    # the output's strides have no part in the size: those of a dense one
+    desc = _attention_desc(*sizes, *st, Lq * H * D, H * D, D, 0, dt, 1.0)
     _check(lib().cross_attention_workspace(desc, ctypes.byref(n)))
     return torch.empty((n.value,), dtype=torch.float32, device=q.device)
 
@@ -740,18 +753,9 @@ def cross_attention(q, k, v, kv_len=None, kv_mask=None, scale=None, s_out=None, 
     ``kv_mask`` (bool or uint8 [B, Lk], true where a key counts) limit the keys;
     a row without keys is 0.  ``scale`` defaults to D ** -0.5.  Returns [B, Lq, Hq, D]
     in q's dtype, or with ``s_out`` E4M3 codes."""
-    dt, device = _DTYPE16.get(q.dtype), q.device
-    if dt is None:
-        raise W8Error(5, f"q: expected bfloat16 or float16, got {q.dtype}")
-    same = (q.dtype,)
-    sq = _heads(q, "q", same, device)
-    sk = _heads(k, "k", same, device)
-    sv = _heads(v, "v", same, device)
-    shape = q.shape
-    B, Lq, H, D = shape
-    Lk, Hk = k.shape[1], k.shape[2]
-    if k.shape != v.shape or k.shape[0] != B or k.shape[3] != D:
-        raise W8Error(2, f"q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)} do not fit together")
+    st, sizes, dt = _attention_inputs(q, k, v)
+    shape, device = q.shape, q.device
+    B, Lk = sizes[0], sizes[2]
     p_len = p_mask = p_s = p_ws = None
     mask_stride = n_ws = 0
     if kv_len is not None:
@@ -767,7 +771,7 @@ def cross_attention(q, k, v, kv_len=None, kv_mask=None, scale=None, s_out=None, 
             raise W8Error(4, "kv_mask: a sample's keys must be contiguous")
         mask_stride = kv_mask.stride(0)
         p_mask = kv_mask.data_ptr()
-    kinds = same
+    kinds = (q.dtype,)
     if s_out is not None:
         kinds = _CODES
         p_s = _floats(s_out, "s_out", 1, device)
@@ -776,8 +780,7 @@ def cross_attention(q, k, v, kv_len=None, kv_mask=None, scale=None, s_out=None, 
     elif out.shape != shape:
         raise W8Error(2, f"out: shape {tuple(out.shape)} differs from q {tuple(q.shape)}")
     so = _heads(out, "out", kinds, device)
-    desc = _attention_desc(B, Lq, Lk, H, Hk, D, *sq, *sk, *sv, *so, mask_stride, dt,
-                           D ** -0.5 if scale is None else scale)
+    desc = _attention_desc(*sizes, *st, *so, mask_stride, dt, sizes[5] ** -0.5 if scale is None else scale)
     L = lib()
     if ws is None:
         n = ctypes.c_int64(0)
