@@ -378,11 +378,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Rows of a slot without a query (groups that do not divide 128) hold zeros:
   // no copy writes them, and a warp raises the maxima of all of its rows together, so
   // what an earlier kernel left there would decide on the other rows' roundings.
-  for (uint32_t at = a.q_bytes + 16 * threadIdx.x; at < kAtom; at += 16 * kThreads)
+  if (a.q_bytes < kAtom) {
+    for (uint32_t at = a.q_bytes + 16 * threadIdx.x; at < kAtom; at += 16 * kThreads)
 #pragma unroll
-    for (int k = 0; k < 2 * C::kAtoms; ++k)
-      *reinterpret_cast<uint4*>(smem + C::kQ + k * kAtom + at) = make_uint4(0, 0, 0, 0);
-  fence_proxy_async_smem();
+      for (int k = 0; k < 2 * C::kAtoms; ++k)
+        *reinterpret_cast<uint4*>(smem + C::kQ + k * kAtom + at) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
