@@ -15,11 +15,13 @@
  *  - Data pointers are DEVICE pointers owned by the caller; the library never
  *    allocates, frees or retains them.  Tensors are dense row-major:
  *    activations [M, K], weights [N, K] (the exported nn.Linear.weight),
- *    outputs [M, N].  There is no bias ([P1] Logs: bias=False).
+ *    outputs [M, N]; cross_attention alone takes strides.  There is no bias
+ *    ([P1] Logs: bias=False).
  *  - bf16 values travel as uint16_t bit patterns, E4M3 codes as uint8_t
  *    (OCP E4M3 "fn": 4 exponent bits, bias 7, 3 mantissa bits, max 448).
- *  - Scales are `const float*` to ONE float in device memory, never read on
- *    the host: reading a scale on the hot path would synchronise the device
+ *  - Scales are `const float*` to ONE float in device memory (arrays of them
+ *    where an entry has a scale for each token or channel), never read on the
+ *    host: reading a scale on the hot path would synchronise the device
  *    ([P4] What changed: the shared-scale invariant is checked at load, never
  *    in forward).
  *  - `stream` is a cudaStream_t (NULL = legacy default stream).  Every compute
@@ -28,6 +30,9 @@
  *  - Base pointers must be 16-byte aligned and K (and N for outputs) multiples
  *    of 16 (E4M3 rows) / 8 (bf16 rows) so that every row starts on a 16-byte
  *    boundary, as the tensor-memory-accelerator copies require.
+ *  - The operands and the stream belong to the calling thread's current
+ *    device.  Any host thread may call any entry, several at once too, on
+ *    streams and outputs of their own (fp8_linear_w8a8_noalloc aside).
  *  - M == 0 is a no-op that returns W8_OK without launching anything (zero-row
  *    inputs; [P2] Commits: the zero-row limitation it works around).
  *    Tensors of rank > 2 are flattened to [M, K] by the caller.
@@ -415,11 +420,16 @@ w8_status ln_modulate_quant(const uint16_t* x, int64_t M, int64_t K, const uint1
  *   s = *s_in, or with s_tok this row's max(fl32(max|h| / 448), 2^-126)
  *   q = E4M3_satRNE( fl32(h * fl32(1/s)) )
  * r is not rounded before the norm nor h before the quantization.  A row with
- * a NaN has a NaN scale and NaN codes; a zero row has zero codes.
+ * a NaN has a NaN scale and NaN codes; a zero row has zero codes.  The mean is
+ * binary32: a row whose squares sum past its range has i = 0 and zero codes.
+ * The codes take a product with the rounded reciprocal of s where
+ * fp8_quant_static takes the rounded quotient: within a few 2^-24 of a boundary
+ * between two codes the two may give either one.
  *   x, res, w   [M, K], [M, K], [K] of dtype (W8_DTYPE_BF16 or W8_DTYPE_F16),
  *               device; res may be NULL; 8 <= K <= 16384, K % 8 == 0
  *   eps         finite and >= 0 (0 on a zero row gives NaN, as the formula does)
- *   s_in        device float scalar, a calibrated scale; or NULL with s_tok
+ *   s_in        device float scalar, a calibrated scale of at least 2^-126
+ *               (a smaller one has no finite reciprocal); or NULL with s_tok
  *   s_tok       [M] floats, device, written: each token's own scale; or NULL
  *   q           E4M3 [M, K], device, written; NULL (with s_in and s_tok NULL):
  *               h only
@@ -472,9 +482,11 @@ typedef struct {
  * h / (Hq / Hkv):
  *   o[b,l,h] = sum_j p_j v[b,j] / sum_j p_j,  p_j = exp(scale * q[b,l,h] . k[b,j] - max)
  * over the keys j that count: j < kv_len[b] and kv_mask[b,j] != 0.  A row for
- * which no key counts is 0.  What K and V hold at keys that do not count (NaN
- * included) has no effect.  Scores, sums and the accumulator are binary32, p
- * is rounded to dtype for the product with V.
+ * which no key counts is 0, and so is one whose scores are all -inf.  What K and
+ * V hold at keys that do not count (NaN included) has no effect.  Scores, sums
+ * and the accumulator are binary32, p is rounded to dtype for the product with V
+ * (its sum is taken before that rounding).  Sums are of p_j up to 2^8 and divided
+ * at the end: 2^8 Lk max|v| has to stay within binary32.
  *   desc     host struct, read during the call only
  *   q        [B, Lq, Hq, D], k, v [B, Lk, Hkv, D] of dtype, device
  *   kv_len   [B] int32, device (clamped to 0 .. Lk), or NULL
@@ -482,12 +494,13 @@ typedef struct {
  *   s_out    NULL: out is of dtype, round16(o).  Device float scalar: out is
  *            E4M3_satRNE(o / s_out), the codes that an out-projection with that
  *            input scale reads; o / s_out is a binary32 product of the
- *            accumulator with 1 / sum and 1 / s_out, not rounded to dtype first
+ *            accumulator with 1 / sum and 1 / s_out (s_out at least 2^-126), not
+ *            rounded to dtype first
  *   out      [B, Lq, Hq, D] by o_stride, device, written
  *   ws       ws_floats floats, device, of which cross_attention_workspace()
  *            says how many the call needs (none when it says 0: may be NULL);
  *            its contents need no set-up and mean nothing afterwards
- * Equal calls give equal bits.  B == 0 or Lq == 0 launches nothing; Lk == 0
+ * Equal calls give equal bits, whatever ran before them.  B == 0 or Lq == 0 launches nothing; Lk == 0
  * writes zeros.
  * Errors: NULL, SHAPE (sizes, workspace too small), STRIDE, DTYPE, PARAM
  * (scale), ALIGN (16 bytes; kv_len and s_out 4), ARCH, CUDA.

@@ -30,10 +30,15 @@
 // maxima and sums need no shuffles), 8-11 epilogue, 12 and 15 MMA issue of slot 0 / 1,
 // 13 TMA loads, 14 clearing of masked V rows (0 * NaN would spoil the products).
 //
-// Measured (GB300): 4096 queries over 20670 keys, 32 query and 8 key heads of 128:
-// 937 us = 1.48 PFLOP/s, 0.76 of the measured bf16 peak; 41340 queries over
-// prompts of 256 to 512 keys, 32 heads, E4M3 out: 276 us = 0.94 PFLOP/s; 8 single tokens
-// over 10335 to 20670 keys: 96 us = 5.3 TB/s, 0.79 of the measured copy, joining included.
+// Measured (GB300; in a replayed graph / one call among others, where the clocks are
+// lower): 4096 queries over 20670 keys, 32 query and 8 key heads of 128:
+// 937 / 985 us = 1.48 / 1.41 PFLOP/s, 0.76 / 0.73 of the measured bf16 peak; 41340 queries
+// over prompts of 256 to 512 keys, 32 heads, E4M3 out: 277 / 262 us = 0.94 / 0.99 PFLOP/s;
+// 8 single tokens over 10335 to 20670 keys: 97 / 90-95 us = 5.2-5.6 TB/s, 0.78 to 0.84 of
+// the measured copy, joining included.
+// Registers: every form with 256 rows a unit spills (64 dimensions 72 to 148 bytes of
+// stores, 128 dimensions 112 to 176, the masked forms most), since the epilogue
+// holds a packed row beside 32 columns of the accumulator in its 88 registers.
 // What bounds the first is the way from a tile's scores to the next tile's: 512
 // cycles of scores, some 1450 of softmax, 256 of P V and four hand-overs
 // of about 200, in which both slots together use the tensor core 2048 cycles;
