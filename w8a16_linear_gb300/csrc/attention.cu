@@ -33,7 +33,7 @@
 // Measured (GB300; in a replayed graph / one call among others, where the clocks are
 // lower): 4096 queries over 20670 keys, 32 query and 8 key heads of 128:
 // 937 / 985 us = 1.48 / 1.41 PFLOP/s, 0.76 / 0.73 of the measured bf16 peak; 41340 queries
-// over prompts of 256 to 512 keys, 32 heads, E4M3 out: 277 / 262 us = 0.94 / 0.99 PFLOP/s;
+// over prompts of 256 to 512 keys, 32 heads, E4M3 out: 277 / 262-277 us = 0.94 / 0.94-0.99 PFLOP/s;
 // 8 single tokens over 10335 to 20670 keys: 97 / 90-95 us = 5.2-5.6 TB/s, 0.78 to 0.84 of
 // the measured copy, joining included.
 // Registers: every form with 256 rows a unit spills (64 dimensions 72 to 148 bytes of
