@@ -15,7 +15,7 @@
  *  - Data pointers are DEVICE pointers owned by the caller; the library never
  *    allocates, frees or retains them.  Tensors are dense row-major:
  *    activations [M, K], weights [N, K] (the exported nn.Linear.weight),
- *    outputs [M, N]; cross_attention alone takes strides.  There is no bias
+ *    outputs [M, N]; the attentions and the heads' norm and rotation alone take strides.  There is no bias
  *    ([P1] Logs: bias=False).
  *  - bf16 values travel as uint16_t bit patterns, E4M3 codes as uint8_t
  *    (OCP E4M3 "fn": 4 exponent bits, bias 7, 3 mantissa bits, max 448).
@@ -40,7 +40,7 @@
  *    argument returns its error code and enqueues nothing.  Thread-local
  *    detail is available from w8_last_error().
  *  - Kernels never trap.  A GEMM whose internal pipeline wait runs past its
- *    deadline (2 s), a cross_attention block or an ln_modulate_quant block
+ *    deadline (2 s), an attention block or an ln_modulate_quant block
  *    whose wait does, stops, records W8_ERR_TIMEOUT in a device error word and
  *    returns; w8_poll_device_error() reports and clears it.
  */
@@ -513,6 +513,143 @@ w8_status cross_attention(const w8_attention_desc* desc, const void* q, const vo
  * current device, with lengths or without (long key sides are cut into parts
  * whose results stand there until they are joined).  Errors as above. */
 w8_status cross_attention_workspace(const w8_attention_desc* desc, int64_t* floats);
+
+/* Heads of M tokens that are normed and rotated.  Strides are in elements, in
+ * the order (token, head); a head's dimensions are contiguous.  Each is a
+ * positive multiple of 8 (dimensions of one entry aside). */
+typedef struct {
+  int64_t M;             /* tokens; may be 0 */
+  int64_t Hq, Hkv, D;    /* heads of q (0: no q) and of k and v; 8 <= D <= 256, D % 8 == 0 */
+  int64_t q_stride[2], k_stride[2], v_stride[2], q_out_stride[2], k_out_stride[2];
+  int64_t pos_stride;    /* elements between the axes of positions */
+  int32_t dtype;         /* of q, k, v, the weights and outputs: W8_DTYPE_BF16 or W8_DTYPE_F16 */
+  int32_t rot;           /* dimensions that are rotated, the head's first: 0 <= rot <= D, rot % 16 == 0 */
+  int32_t interleaved;   /* pairs (2i, 2i + 1); 0: pairs (i, i + rot / 2) */
+  int32_t axes;          /* axes of a position, 1..3 */
+  int32_t axis_pairs[3]; /* pairs that each axis rotates, in this order; their sum is rot / 2 */
+  float eps;             /* of the norm, finite and >= 0 */
+  float amplitude;       /* factor of cosine and sine, finite and > 0 (usually 1) */
+} w8_rope_desc;
+
+/* A paged cache of keys and values, and the batch of sequences in it.  Position
+ * p of sequence b is cell p % page_size of the page page_table[b][p / page_size].
+ * Strides are in elements, in the order (page, position, head); a head's
+ * dimensions are contiguous.  Each is a positive multiple of 8, with E4M3 cells
+ * of 16 (dimensions of one entry aside). */
+typedef struct {
+  int64_t B;             /* sequences, at most 2^20; may be 0 */
+  int64_t pages;         /* of the cache, 1 .. 2^31 - 1 */
+  int64_t page_size;     /* positions of a page: a multiple of 8, at most 2^20 */
+  int64_t table_cols;    /* entries of the page table for each sequence; times page_size at most 2^26 */
+  int64_t table_stride;  /* entries between the sequences of the table */
+  int64_t Hkv, D;        /* 8 <= D <= 128, D % 8 == 0 (E4M3 cells: D % 16 == 0) */
+  int64_t k_stride[3], v_stride[3];
+  int32_t dtype;         /* of the cells: that of q, k, v, or W8_DTYPE_E4M3 */
+} w8_paged_desc;
+
+/*
+ * qk_norm_rope — root-mean-square norm of each head of the queries and keys,
+ * and their rotation by position.  For a head x of D values:
+ *   h = fl32(fl32(x * w) * rsqrt(fl32(sum x^2 * fl32(1/D)) + eps)), or h = x
+ *   (a, b) -> (a c - b s, b c + a s) for the pairs of its first rot dimensions,
+ *   c, s = amplitude * cos, sin(position * frequency_i);  the others keep h
+ * in binary32, rounded to dtype once.
+ *   desc       host struct, read during the call only
+ *   q, k       [M, Hq, D] and [M, Hkv, D], device; k may be NULL with Hkv == 0
+ *   positions  [axes, M] int32, device, of any sign; NULL where rot is 0
+ *   turns      [rot / 2], device: what a position adds to the phase of pair i in
+ *              units of 2^-64 turns, round(frequency_i * 2^64 / (2 pi)) modulo 2^64;
+ *              the phase is position * turns[i] modulo 2^64, whose upper 32 bits
+ *              are the angle.  NULL where rot is 0
+ *   q_weight, k_weight   [D] of dtype, device, or NULL: no norm of q / of k
+ *   q_out, k_out  by their strides, device, written; may be q and k themselves
+ * A norm or a rotation is wanted.  M == 0 launches nothing.
+ * Errors: NULL, SHAPE, STRIDE, DTYPE, PARAM (eps, amplitude, nothing to do),
+ * ALIGN (16 bytes; positions 4, turns 8), ARCH, CUDA.
+ */
+w8_status qk_norm_rope(const w8_rope_desc* desc, const void* q, const void* k, const int32_t* positions,
+                       const uint64_t* turns, const void* q_weight, const void* k_weight, void* q_out, void* k_out,
+                       void* stream);
+
+/*
+ * paged_kv_append — keys and values of new tokens into a paged cache, the keys
+ * (and, where given, the queries) normed and rotated on the way as by
+ * qk_norm_rope.  The M tokens are those of B sequences one after the other:
+ * sequence b has the tokens q_start[b] .. q_start[b+1] - 1, which are the last of
+ * its kv_len[b] positions.
+ *   rope       host struct; k_out_stride is not read; rot may be 0
+ *   cache      host struct; Hkv and D are those of rope
+ *   q          [M, Hq, D], or NULL with Hq == 0; q_out as for qk_norm_rope
+ *   k, v       [M, Hkv, D] of rope's dtype, device
+ *   positions  as for qk_norm_rope, or NULL: each token's position in its sequence
+ *              (axes must be 1)
+ *   k_cache, v_cache   device, written at the new tokens' cells alone
+ *   page_table [B] rows of table_cols int32, device
+ *   q_start    [B + 1] int32, device, ascending, or NULL: M / B tokens each
+ *   kv_len     [B] int32, device: positions with the new tokens
+ *   k_scale, v_scale   device float scalars of at least 2^-126, for E4M3 cells,
+ *              which hold E4M3_satRNE(fl32(x * fl32(1/scale))); else NULL
+ * No two tokens may have the same cell.  A position below 0, beyond the table or
+ * on a page outside 0 .. pages - 1 is not written; tokens of no sequence (before
+ * q_start[0], from q_start[B] on) are left out, their q_out too.
+ * B == 0 or M == 0 launches nothing.
+ * Errors: as for qk_norm_rope, and SHAPE (M not a multiple of B without q_start).
+ */
+w8_status paged_kv_append(const w8_rope_desc* rope, const w8_paged_desc* cache, const void* q, const void* k,
+                          const void* v, const int32_t* positions, const uint64_t* turns, const void* q_weight,
+                          const void* k_weight, void* k_cache, void* v_cache, const int32_t* page_table,
+                          const int32_t* q_start, const int32_t* kv_len, const float* k_scale, const float* v_scale,
+                          void* q_out, void* stream);
+
+/* Sizes and layout of the queries of a paged attention.  Strides as in
+ * w8_rope_desc. */
+typedef struct {
+  int64_t T;             /* tokens of all sequences; T * Hq at most 2^30; may be 0 */
+  int64_t Hq;            /* a multiple of the cache's Hkv, at most 128 times it */
+  int64_t max_q;         /* the most tokens of one sequence, at least 1 */
+  int64_t q_stride[2], o_stride[2];
+  int32_t dtype;         /* of q: W8_DTYPE_BF16 or W8_DTYPE_F16 */
+  int32_t causal;        /* a token sees the positions up to its own; 0: all kv_len of them */
+  float scale;           /* of the scores, finite and > 0 (usually 1 / sqrt(D)) */
+} w8_paged_attention_desc;
+
+/*
+ * paged_attention — softmax attention of new tokens over the cached positions
+ * of their sequences (their own among them), for a batch of sequences as
+ * paged_kv_append has it: token i of the n of sequence b is at position
+ * t = kv_len[b] - n + i and sees the positions j < kv_len[b], with causal
+ * those of them with j <= t:
+ *   o[i,h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q[i,h] . k_j - max)
+ * with the key head h / (Hq / Hkv).  A row that sees no position is 0, and so is one whose
+ * scores are all -inf.  What the cells of positions hold that a row does not see
+ * (NaN included) has no effect on it.  With E4M3 cells k_j and v_j are the
+ * codes' values times k_scale and v_scale.  Positions beyond the table do not
+ * exist; a page outside 0 .. pages - 1 stands for zeros.  Scores, sums and
+ * the accumulator are binary32, p is rounded to dtype for the product with V (its sum is
+ * taken before that); 2^8 times the sum of |v| over the positions has to stay
+ * within binary32.
+ *   q          [T, Hq, D], device
+ *   k_cache, v_cache, page_table, q_start, kv_len, k_scale, v_scale as for
+ *              paged_kv_append; sequences may share pages
+ *   s_out      NULL: out is of dtype.  Device float scalar (at least 2^-126): out
+ *              is E4M3_satRNE(o / s_out) as for cross_attention
+ *   out        [T, Hq, D] by o_stride, device, written for the first max_q tokens
+ *              of each sequence; the other rows are left as they were
+ *   ws         ws_floats floats, device, of which paged_attention_workspace() says
+ *              how many the call needs; its contents need no set-up and mean
+ *              nothing afterwards.  Calls that may run at the same time need one each
+ * Equal calls give equal bits.  B == 0 or T == 0 launches nothing.
+ * Errors: NULL, SHAPE (sizes, workspace too small), STRIDE, DTYPE, PARAM (scale),
+ * ALIGN (16 bytes; page_table, q_start, kv_len and scales 4), ARCH, CUDA.
+ */
+w8_status paged_attention(const w8_paged_attention_desc* desc, const w8_paged_desc* cache, const void* q,
+                          const void* k_cache, const void* v_cache, const int32_t* page_table, const int32_t* q_start,
+                          const int32_t* kv_len, const float* k_scale, const float* v_scale, const float* s_out,
+                          void* out, float* ws, int64_t ws_floats, void* stream);
+
+/* Floats of workspace that paged_attention needs for these sizes on the
+ * current device.  Errors as above. */
+w8_status paged_attention_workspace(const w8_paged_attention_desc* desc, const w8_paged_desc* cache, int64_t* floats);
 
 /*
  * step_policy_dispatch — host-only, pure function of (policy, step, num_steps).

@@ -13,5 +13,6 @@ from .binding import (  # noqa: F401
     ln_modulate_quant, ln_modulate_bf16,
     add_rms_norm_quant, fp8_linear_w8a8_pertoken, fp8_linear_w8a8_pertoken_group,
     cross_attention, cross_attention_workspace,
+    rope_frequencies, rope_turns, qk_norm_rope, paged_kv_append, paged_attention, paged_attention_workspace,
     swiglu_2in_fp8, swiglu_2in_bf16, swiglu_2in_ex_fp8, swiglu_2in_ex_16, step_policy_dispatch, step_policy_parse, check_group_scales,
 )

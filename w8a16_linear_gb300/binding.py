@@ -6,8 +6,10 @@ library is missing the calls raise instead of falling back to anything else.
 """
 
 import ctypes
+import math
 import os
 import struct
+from fractions import Fraction
 
 import torch
 
@@ -46,6 +48,26 @@ class AttentionDesc(ctypes.Structure):
     _fields_ = [("B", _i64), ("Lq", _i64), ("Lk", _i64), ("Hq", _i64), ("Hkv", _i64), ("D", _i64),
                 ("q_stride", _i64 * 3), ("k_stride", _i64 * 3), ("v_stride", _i64 * 3), ("o_stride", _i64 * 3),
                 ("mask_stride", _i64), ("dtype", _i32), ("scale", ctypes.c_float)]
+
+
+class RopeDesc(ctypes.Structure):
+    """Mirror of ``w8_rope_desc``."""
+    _fields_ = [("M", _i64), ("Hq", _i64), ("Hkv", _i64), ("D", _i64), ("q_stride", _i64 * 2), ("k_stride", _i64 * 2),
+                ("v_stride", _i64 * 2), ("q_out_stride", _i64 * 2), ("k_out_stride", _i64 * 2), ("pos_stride", _i64),
+                ("dtype", _i32), ("rot", _i32), ("interleaved", _i32), ("axes", _i32), ("axis_pairs", _i32 * 3),
+                ("eps", ctypes.c_float), ("amplitude", ctypes.c_float)]
+
+
+class PagedDesc(ctypes.Structure):
+    """Mirror of ``w8_paged_desc``."""
+    _fields_ = [("B", _i64), ("pages", _i64), ("page_size", _i64), ("table_cols", _i64), ("table_stride", _i64),
+                ("Hkv", _i64), ("D", _i64), ("k_stride", _i64 * 3), ("v_stride", _i64 * 3), ("dtype", _i32)]
+
+
+class PagedAttentionDesc(ctypes.Structure):
+    """Mirror of ``w8_paged_attention_desc``."""
+    _fields_ = [("T", _i64), ("Hq", _i64), ("max_q", _i64), ("q_stride", _i64 * 2), ("o_stride", _i64 * 2),
+                ("dtype", _i32), ("causal", _i32), ("scale", ctypes.c_float)]
 
 
 SIGNATURES = {
@@ -100,6 +122,10 @@ SIGNATURES = {
     "cross_attention": (ctypes.c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                        _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p]),
     "cross_attention_workspace": (ctypes.c_int, [_c_void_p, ctypes.POINTER(_i64)]),
+    "qk_norm_rope": (ctypes.c_int, [_c_void_p] * 10),
+    "paged_kv_append": (ctypes.c_int, [_c_void_p] * 18),
+    "paged_attention": (ctypes.c_int, [_c_void_p] * 13 + [_i64, _c_void_p]),
+    "paged_attention_workspace": (ctypes.c_int, [_c_void_p, _c_void_p, ctypes.POINTER(_i64)]),
     "step_policy_dispatch": (ctypes.c_int, [_c_void_p, _i32, _i32, ctypes.POINTER(_i32)]),
     "w8_check_group_scales": (ctypes.c_int, [ctypes.POINTER(_c_void_p), _i32]),
     "w8_step_policy_parse": (ctypes.c_int, [ctypes.c_char_p, ctypes.POINTER(StepPolicy),
@@ -791,6 +817,298 @@ def cross_attention(q, k, v, kv_len=None, kv_mask=None, scale=None, s_out=None, 
         n_ws = ws.numel()
         p_ws = _floats(ws, "ws", n_ws, device)
     _check(L.cross_attention(desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), p_len, p_mask, p_s, out.data_ptr(), p_ws,
+                             n_ws, _raw_stream(stream, device)))
+    return out
+
+
+# ---------------------------------------------------------------- a self-attention site over a paged cache
+
+# The library's descriptors as bytes (the fields of RopeDesc, PagedDesc and
+# PagedAttentionDesc, in their order)
+_rope_desc = struct.Struct("=15q7i2f4x").pack
+_paged_desc = struct.Struct("=13qi4x").pack
+_paged_attention_desc = struct.Struct("=7q2if4x").pack
+
+# 1 / (2 pi), to 50 digits
+_PER_TURN = Fraction("0.15915494309189533576888376337251436203445964574046")
+
+
+def rope_frequencies(dim, base=10000.0, factor=1.0, trained=None, fast=32.0, slow=1.0):
+    """Frequencies (float64 [dim / 2], radians a position) of a rotation of ``dim``
+    dimensions: base ** (-2 i / dim).  ``factor`` > 1 stretches them for contexts that
+    many times as long: all of them (positions are interpolated), or with
+    ``trained``, the context length of the training, by parts: a pair that turns more
+    than ``fast`` times over that length is kept, one that turns less than ``slow``
+    times is divided by ``factor``, with a linear ramp over the pairs between."""
+    if dim < 2 or dim % 2:
+        raise W8Error(2, f"dim={dim}: expected an even number of dimensions")
+    if not (base > 0 and factor > 0 and (trained is None or (trained > 0 and fast > slow > 0))):
+        raise W8Error(11, f"base={base}, factor={factor}, trained={trained}, fast={fast}, slow={slow}")
+    half = dim // 2
+    f = torch.tensor([base ** (-i / half) for i in range(half)], dtype=torch.float64)
+    if trained is None:
+        return f / factor
+    # the (fractional) pair that turns n times over the trained length
+    pair = [half * math.log(trained / (2 * math.pi * n)) / math.log(base) for n in (fast, slow)]
+    low, high = max(math.floor(pair[0]), 0), min(math.ceil(pair[1]), half - 1)
+    keep = 1.0 - ((torch.arange(half, dtype=torch.float64) - low) / max(high - low, 1e-3)).clamp(0.0, 1.0)
+    return f * keep + f / factor * (1.0 - keep)
+
+
+def rope_turns(frequencies, device="cuda"):
+    """What the rotating entries take: for each frequency (radians a position) the
+    part of a turn that one position adds, in units of 2^-64 turns (int64 bits),
+    rounded to the nearest.  Made once, on the host."""
+    f = frequencies.detach().cpu().tolist() if isinstance(frequencies, torch.Tensor) else list(frequencies)
+    if any(not math.isfinite(x) for x in f):
+        raise W8Error(11, "frequencies: not finite")
+    turns = [round(Fraction(x) * _PER_TURN * 2 ** 64) % 2 ** 64 for x in f]
+    return torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
+
+
+def _refuse_rows(t, name, dtypes, device, shape):
+    if t.dtype not in dtypes:
+        raise W8Error(5, f"{name}: expected {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if not t.is_cuda or t.device != device:
+        raise W8Error(1, f"{name}: must be a CUDA tensor on the other operands' device")
+    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+        raise W8Error(2, f"{name}: shape {tuple(t.shape)}, expected {['any' if w is None else w for w in shape]}")
+    raise W8Error(4, f"{name}: the head's dimensions must be contiguous")
+
+
+def _rows(t, name, dtypes, device, M, H, D):
+    """(row, head) strides of ``t``, [M, H, D] with dense D."""
+    if t.dtype not in dtypes or t.device != device or not t.is_cuda or t.shape != (M, H, D):
+        _refuse_rows(t, name, dtypes, device, (M, H, D))
+    sr, sh, sd = t.stride()
+    if sd != 1 and D > 1:
+        _refuse_rows(t, name, dtypes, device, (M, H, D))
+    return sr, sh
+
+
+def _ints(t, name, n, device):
+    """data_ptr of ``t``, n dense int32 values on ``device``."""
+    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous() or t.device != device or not t.is_cuda:
+        _refuse(t, name, (torch.int32,), device, numel=n)
+    return t.data_ptr()
+
+
+def _weight(t, name, dtype, D, device):
+    return None if t is None else _like(t, name, (dtype,), (D,), device)
+
+
+def _rotation(turns, positions, axes, M, device):
+    """(rot, axes' number and pairs, pointers of turns and positions, positions' pitch)."""
+    if turns is None:
+        if positions is not None or axes is not None:
+            raise W8Error(11, "positions and axes belong to a rotation (turns)")
+        return 0, 1, (0, 0, 0), None, None, 0
+    if turns.dtype is not torch.int64 or turns.dim() != 1 or not turns.is_contiguous() or turns.device != device \
+            or not turns.is_cuda:
+        _refuse(turns, "turns", (torch.int64,), device, shape=("pairs",))
+    pairs = turns.shape[0]
+    axes = (pairs,) if axes is None else tuple(axes)
+    if not 1 <= len(axes) <= 3:
+        raise W8Error(2, f"axes: {axes}, expected 1 to 3 numbers of pairs")
+    p_pos, pitch = None, 0
+    if positions is not None:
+        shape = (M,) if len(axes) == 1 and positions.dim() == 1 else (len(axes), M)
+        if positions.dtype is not torch.int32 or positions.shape != shape or positions.device != device \
+                or not positions.is_cuda:
+            _refuse_rows(positions, "positions", (torch.int32,), device, shape)
+        if M > 1 and positions.stride(-1) != 1:
+            raise W8Error(4, "positions: an axis's positions must be contiguous")
+        p_pos = positions.data_ptr()
+        pitch = positions.stride(0) if positions.dim() == 2 else 0
+    return 2 * pairs, len(axes), axes + (0,) * (3 - len(axes)), turns.data_ptr(), p_pos, pitch
+
+
+def qk_norm_rope(q, k, positions=None, turns=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, axes=None,
+                 amplitude=1.0, q_out=None, k_out=None, stream=None):
+    """Root-mean-square norm of every head of ``q`` [M, Hq, D] and ``k`` [M, Hkv, D]
+    (bfloat16 or float16, any strides that are multiples of 8 with contiguous D; ``k``
+    may be None) with the weights given ([D]), and the rotation of the first
+    2 * len(turns) dimensions by ``positions`` (int32 [M]; ``turns`` from rope_turns):
+    pairs (i, i + half), or (2i, 2i + 1) where ``interleaved``.  With ``axes``, how
+    many pairs each of up to three axes rotates, ``positions`` is [axes, M].
+    ``amplitude`` scales cosine and sine.  Returns ``(q_out, k_out)``, which may be
+    ``q`` and ``k`` themselves."""
+    dtype, device = q.dtype, q.device
+    dt = _DTYPE16.get(dtype)
+    if dt is None or not q.is_cuda or q.dim() != 3:
+        if dt is None:
+            raise W8Error(5, f"q: expected bfloat16 or float16, got {dtype}")
+        if not q.is_cuda:
+            raise W8Error(1, "q: must be a CUDA tensor")
+        raise W8Error(2, f"q: expected [tokens, heads, D], got {tuple(q.shape)}")
+    M, Hq, D = q.shape
+    same = (dtype,)
+    Hk = 0
+    sk = sko = (0, 0)
+    p_k = p_ko = None
+    if k is not None:
+        Hk = k.shape[1] if k.dim() == 3 else -1
+        sk = _rows(k, "k", same, device, M, Hk, D)
+        p_k = k.data_ptr()
+        if k_out is None:
+            k_out = _empty((M, Hk, D), dtype, device, stream)
+        sko = _rows(k_out, "k_out", same, device, M, Hk, D)
+        p_ko = k_out.data_ptr()
+    elif k_out is not None or k_weight is not None:
+        raise W8Error(1, "k_out or k_weight without k")
+    rot, n_axes, axes, p_turns, p_pos, pitch = _rotation(turns, positions, axes, M, device)
+    if turns is not None and positions is None:
+        raise W8Error(1, "positions: a rotation needs them")
+    if q_out is None:
+        q_out = _empty((M, Hq, D), dtype, device, stream)
+    desc = _rope_desc(M, Hq, Hk, D, *_rows(q, "q", same, device, M, Hq, D), *sk, 0, 0,
+                      *_rows(q_out, "q_out", same, device, M, Hq, D), *sko, pitch, dt, rot, bool(interleaved), n_axes, *axes,
+                      eps, amplitude)
+    _check(lib().qk_norm_rope(desc, q.data_ptr(), p_k, p_pos, p_turns, _weight(q_weight, "q_weight", dtype, D, device),
+                              _weight(k_weight, "k_weight", dtype, D, device), q_out.data_ptr(), p_ko,
+                              _raw_stream(stream, device)))
+    return q_out, k_out
+
+
+def _cells(t, name, kinds, device):
+    """(page, position, head) strides of a cache [pages, page_size, heads, D]."""
+    if t.dim() != 4 or t.dtype not in kinds or t.device != device or not t.is_cuda:
+        _refuse_rows(t, name, kinds, device, (None,) * 4)
+    sp, sl, sh, sd = t.stride()
+    if sd != 1 and t.shape[3] > 1:
+        _refuse_rows(t, name, kinds, device, (None,) * 4)
+    return sp, sl, sh
+
+
+def _paged(dtype, device, k_cache, v_cache, page_table):
+    """(descriptor of a paged cache beside tensors of ``dtype``, sequences, heads, D, page table's pointer)."""
+    codes = k_cache.dtype in _CODES
+    kinds = _CODES if codes else (dtype,)
+    sk = _cells(k_cache, "k_cache", kinds, device)
+    sv = sk if v_cache is None else _cells(v_cache, "v_cache", kinds, device)
+    if v_cache is not None and v_cache.shape != k_cache.shape:
+        raise W8Error(2, f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} differ")
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.device != device or not page_table.is_cuda:
+        _refuse_rows(page_table, "page_table", (torch.int32,), device, (None, None))
+    B, cols = page_table.shape
+    if cols > 1 and page_table.stride(1) != 1:
+        raise W8Error(4, "page_table: a sequence's pages must be contiguous")
+    pages, size, Hk, D = k_cache.shape
+    desc = _paged_desc(B, pages, size, cols, page_table.stride(0), Hk, D, *sk, *sv, DTYPE_E4M3 if codes else _DTYPE16[dtype])
+    return desc, B, Hk, D, page_table.data_ptr()
+
+
+def _scale_ptr(t, name, device):
+    return None if t is None else _floats(t, name, 1, device)
+
+
+def paged_kv_append(k, v, k_cache, v_cache, page_table, q_start, kv_len, turns=None, q=None, q_weight=None, k_weight=None,
+                    eps=1e-6, interleaved=False, positions=None, axes=None, amplitude=1.0, k_scale=None, v_scale=None,
+                    q_out=None, stream=None):
+    """Keys and values of new tokens (``k``, ``v`` [T, Hkv, D], bfloat16 or float16)
+    into their cells of a paged cache ``k_cache``, ``v_cache`` [pages, page_size, Hkv, D]
+    (of that type, or E4M3 codes with the scales ``k_scale`` and ``v_scale``); the
+    keys, and where given the queries ``q`` [T, Hq, D], are normed and rotated on
+    the way as by qk_norm_rope.  Sequence b has the tokens q_start[b] ..
+    q_start[b + 1] - 1 (int32 [B + 1]; None: T / B each), the last of its kv_len[b]
+    positions (int32 [B]); position p is cell p % page_size of page
+    page_table[b, p // page_size] (int32 [B, columns]).  ``positions`` (default: each
+    token's own) and ``axes`` are those of the rotation.  Any strides that are
+    multiples of 8 (E4M3 cells: 16) with contiguous D.  Positions without a page are not
+    written, tokens of no sequence left out.  Returns ``q_out`` (None without ``q``),
+    which may be ``q``."""
+    dtype, device = k.dtype, k.device
+    dt = _DTYPE16.get(dtype)
+    if dt is None:
+        raise W8Error(5, f"k: expected bfloat16 or float16, got {dtype}")
+    if not k.is_cuda:
+        raise W8Error(1, "k: must be a CUDA tensor")
+    cache, B, Hk, D, p_table = _paged(dtype, device, k_cache, v_cache, page_table)
+    T = k.shape[0] if k.dim() else 0
+    same = (dtype,)
+    sk, sv = _rows(k, "k", same, device, T, Hk, D), _rows(v, "v", same, device, T, Hk, D)
+    Hq, sq, sqo, p_q, p_qo = 0, (0, 0), (0, 0), None, None
+    if q is not None:
+        Hq = q.shape[1] if q.dim() == 3 else -1
+        sq = _rows(q, "q", same, device, T, Hq, D)
+        if q_out is None:
+            q_out = _empty((T, Hq, D), dtype, device, stream)
+        sqo = _rows(q_out, "q_out", same, device, T, Hq, D)
+        p_q, p_qo = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None or q_weight is not None:
+        raise W8Error(1, "q_out or q_weight without q")
+    rot, n_axes, axes, p_turns, p_pos, pitch = _rotation(turns, positions, axes, T, device)
+    desc = _rope_desc(T, Hq, Hk, D, *sq, *sk, *sv, *sqo, 0, 0, pitch, dt, rot, bool(interleaved), n_axes, *axes, eps,
+                      amplitude)
+    p_start = None if q_start is None else _ints(q_start, "q_start", B + 1, device)
+    _check(lib().paged_kv_append(desc, cache, p_q, k.data_ptr(), v.data_ptr(), p_pos, p_turns,
+                                 _weight(q_weight, "q_weight", dtype, D, device), _weight(k_weight, "k_weight", dtype, D, device),
+                                 k_cache.data_ptr(), v_cache.data_ptr(), p_table, p_start, _ints(kv_len, "kv_len", B, device),
+                                 _scale_ptr(k_scale, "k_scale", device), _scale_ptr(v_scale, "v_scale", device), p_qo,
+                                 _raw_stream(stream, device)))
+    return q_out
+
+
+def _paged_queries(q, k_cache, v_cache, page_table, max_q, causal, scale, o_stride=None):
+    dtype, device = q.dtype, q.device
+    dt = _DTYPE16.get(dtype)
+    if dt is None:
+        raise W8Error(5, f"q: expected bfloat16 or float16, got {dtype}")
+    if q.dim() != 3:
+        raise W8Error(2, f"q: expected [tokens, heads, D], got {tuple(q.shape)}")
+    if not q.is_cuda:
+        raise W8Error(1, "q: must be a CUDA tensor")
+    cache, B, _, D, p_table = _paged(dtype, device, k_cache, v_cache, page_table)
+    T, H = q.shape[0], q.shape[1]
+    sq = _rows(q, "q", (dtype,), device, T, H, D)
+    if max_q is None:
+        max_q = max(T, 1)
+    desc = _paged_attention_desc(T, H, max_q, *sq, *(o_stride or (H * D, D)), dt, bool(causal),
+                                 D ** -0.5 if scale is None else scale)
+    return desc, cache, B, p_table
+
+
+def paged_attention_workspace(q, k_cache, page_table, max_q=None):
+    """float32 scratch for paged_attention(q, k_cache, ..., max_q=max_q, ws=...) of
+    these shapes (caller-side allocation; empty when none is needed)."""
+    desc, cache, _, _ = _paged_queries(q, k_cache, None, page_table, max_q, True, 1.0)
+    n = ctypes.c_int64(0)
+    _check(lib().paged_attention_workspace(desc, cache, ctypes.byref(n)))
+    return torch.empty((n.value,), dtype=torch.float32, device=q.device)
+
+
+def paged_attention(q, k_cache, v_cache, page_table, q_start, kv_len, max_q=None, causal=True, scale=None, k_scale=None,
+                    v_scale=None, s_out=None, out=None, ws=None, stream=None):
+    """Softmax attention of new tokens ``q`` [T, Hq, D] (bfloat16 or float16) over
+    the cached positions of their sequences (Hq a multiple of the cache's Hkv); cache, ``page_table``,
+    ``q_start`` and ``kv_len`` as for paged_kv_append.  A token sees its sequence's kv_len positions, with
+    ``causal`` those up to its own; one that sees none gets 0.  ``max_q`` is the most tokens of
+    one sequence (default T; of a longer one the tokens from there on are left as they were, like those of no
+    sequence).  ``scale`` defaults to D ** -0.5; ``k_scale`` and ``v_scale`` are
+    those of E4M3 cells.  Returns [T, Hq, D] in q's dtype, or with ``s_out`` E4M3 codes."""
+    device, shape = q.device, q.shape
+    kinds = (q.dtype,) if s_out is None else _CODES
+    if out is None:
+        out = _empty(shape, kinds[0], device, stream)
+    if len(shape) != 3 or out.shape != shape or out.dtype not in kinds or out.device != device:
+        _refuse_rows(out, "out", kinds, device, shape)
+    if out.stride(2) != 1 and shape[2] > 1:
+        _refuse_rows(out, "out", kinds, device, shape)
+    desc, cache, B, p_table = _paged_queries(q, k_cache, v_cache, page_table, max_q, causal, scale, out.stride()[:2])
+    p_start = None if q_start is None else _ints(q_start, "q_start", B + 1, device)
+    L = lib()
+    p_ws, n_ws = None, 0
+    if ws is None:
+        n = ctypes.c_int64(0)
+        _check(L.paged_attention_workspace(desc, cache, ctypes.byref(n)))
+        if n.value:
+            ws = _empty((n.value,), torch.float32, device, stream)
+    if ws is not None:
+        n_ws = ws.numel()
+        p_ws = _floats(ws, "ws", n_ws, device)
+    _check(L.paged_attention(desc, cache, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), p_table, p_start,
+                             _ints(kv_len, "kv_len", B, device), _scale_ptr(k_scale, "k_scale", device),
+                             _scale_ptr(v_scale, "v_scale", device), _scale_ptr(s_out, "s_out", device), out.data_ptr(), p_ws,
                              n_ws, _raw_stream(stream, device)))
     return out
 

@@ -118,14 +118,16 @@ w8_status w8_device_check(void) {
 }
 
 w8_status w8_poll_device_error(void* stream) {
-  uint32_t err = 0, err2 = 0, err3 = 0;
+  uint32_t err = 0, err2 = 0, err3 = 0, err4 = 0;
   cudaError_t e = w8::gemm_read_error(static_cast<cudaStream_t>(stream), &err);
   if (e == cudaSuccess) e = w8::elementwise_read_error(static_cast<cudaStream_t>(stream), &err2);
   if (e == cudaSuccess) e = w8::attention_read_error(static_cast<cudaStream_t>(stream), &err3);
+  if (e == cudaSuccess) e = w8::paged_attention_read_error(static_cast<cudaStream_t>(stream), &err4);
   if (e != cudaSuccess) return fail(W8_ERR_CUDA, "reading device error word: %s", cudaGetErrorString(e));
   if (err & w8::kErrTimeout) return fail(W8_ERR_TIMEOUT, "a GEMM pipeline wait timed out");
   if (err2 & w8::kErrTimeout) return fail(W8_ERR_TIMEOUT, "a row-buffer wait of ln_modulate_quant timed out");
   if (err3 & w8::kErrTimeout) return fail(W8_ERR_TIMEOUT, "a pipeline wait of cross_attention timed out");
+  if (err4 & w8::kErrTimeout) return fail(W8_ERR_TIMEOUT, "a pipeline wait of paged_attention timed out");
   return ok();
 }
 
@@ -777,6 +779,284 @@ w8_status cross_attention(const w8_attention_desc* desc, const void* q, const vo
   cudaError_t e = w8::launch_cross_attention(p, sms, static_cast<cudaStream_t>(stream), &terr);
   if (terr) return fail(W8_ERR_ALIGN, "cross_attention: tensor map encoding rejected the operands");
   return cuda_status(e, "cross_attention launch");
+}
+
+// A row and head stride: positive multiples of 8 where there is more than one.
+static w8_status check_strides(const char* fn, const char* name, const int64_t* stride, int64_t rows, int64_t heads) {
+  const int64_t ext[2] = {rows, heads};
+  for (int i = 0; i < 2; ++i)
+    if (rows > 0 && heads > 0 && ext[i] > 1 && (stride[i] < 8 || stride[i] % 8 || stride[i] >= (1ll << 38)))
+      return fail(W8_ERR_STRIDE, "%s: stride %lld of %s (need a positive multiple of 8 elements)", fn,
+                  (long long)stride[i], name);
+  return W8_OK;
+}
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Sizes, strides and scalars of a norm and rotation of heads, without its pointers.
+static w8_status check_rope(const char* fn, const w8_rope_desc* d, bool paged, w8::RopeProblem* p) {
+  if (!d) return fail(W8_ERR_NULL, "%s: NULL descriptor", fn);
+  if (d->dtype != W8_DTYPE_BF16 && d->dtype != W8_DTYPE_F16)
+    return fail(W8_ERR_DTYPE, "%s: dtype %d is neither bf16 nor f16", fn, d->dtype);
+  if (d->M < 0 || d->M > (1ll << 30)) return fail(W8_ERR_SHAPE, "%s: M=%lld", fn, (long long)d->M);
+  if (d->Hq < 0 || d->Hkv < 0 || d->Hq > 65536 || d->Hkv > 65536 || d->Hq + d->Hkv < 1 || (paged && d->Hkv < 1))
+    return fail(W8_ERR_SHAPE, "%s: Hq=%lld Hkv=%lld", fn, (long long)d->Hq, (long long)d->Hkv);
+  if (d->D < 8 || d->D > 256 || d->D % 8)
+    return fail(W8_ERR_SHAPE, "%s: D=%lld (need 8 <= D <= 256, D %% 8 == 0)", fn, (long long)d->D);
+  if (d->rot < 0 || d->rot > d->D || d->rot % 16)
+    return fail(W8_ERR_SHAPE, "%s: rot=%d (need 0 <= rot <= D, rot %% 16 == 0)", fn, d->rot);
+  if (d->axes < 1 || d->axes > 3) return fail(W8_ERR_SHAPE, "%s: axes=%d", fn, d->axes);
+  int64_t pairs = 0;
+  for (int i = 0; i < d->axes; ++i) {
+    if (d->axis_pairs[i] < 0) return fail(W8_ERR_SHAPE, "%s: axis_pairs[%d]=%d", fn, i, d->axis_pairs[i]);
+    pairs += d->axis_pairs[i];
+  }
+  if (pairs != d->rot / 2)
+    return fail(W8_ERR_SHAPE, "%s: the axes rotate %lld pairs of %d", fn, (long long)pairs, d->rot / 2);
+  if (!std::isfinite(d->eps) || d->eps < 0.0f) return fail(W8_ERR_PARAM, "%s: eps=%g", fn, (double)d->eps);
+  if (!std::isfinite(d->amplitude) || !(d->amplitude > 0.0f))
+    return fail(W8_ERR_PARAM, "%s: amplitude=%g", fn, (double)d->amplitude);
+  w8_status st;
+  if ((st = check_strides(fn, "q", d->q_stride, d->M, d->Hq)) != W8_OK) return st;
+  if ((st = check_strides(fn, "k", d->k_stride, d->M, d->Hkv)) != W8_OK) return st;
+  if ((st = check_strides(fn, "q_out", d->q_out_stride, d->M, d->Hq)) != W8_OK) return st;
+  if (paged && (st = check_strides(fn, "v", d->v_stride, d->M, d->Hkv)) != W8_OK) return st;
+  if (!paged && (st = check_strides(fn, "k_out", d->k_out_stride, d->M, d->Hkv)) != W8_OK) return st;
+  if (d->axes > 1 && d->pos_stride < 1)
+    return fail(W8_ERR_STRIDE, "%s: pos_stride=%lld", fn, (long long)d->pos_stride);
+  std::memset(p, 0, sizeof(*p));
+  p->M = d->M;
+  p->Hq = (int)d->Hq;
+  p->Hkv = (int)d->Hkv;
+  p->D = (int)d->D;
+  p->rot = d->rot;
+  for (int i = 0; i < 2; ++i) {
+    p->qs[i] = d->q_stride[i];
+    p->ks[i] = d->k_stride[i];
+    p->vs[i] = d->v_stride[i];
+    p->qos[i] = d->q_out_stride[i];
+    p->kos[i] = d->k_out_stride[i];
+  }
+  p->f16 = d->dtype == W8_DTYPE_F16;
+  p->interleaved = d->interleaved != 0;
+  p->axes = d->axes;
+  for (int i = 0; i < d->axes; ++i) p->axis_pairs[i] = d->axis_pairs[i];
+  p->eps = d->eps;
+  p->amplitude = d->amplitude;
+  p->pos_stride = d->pos_stride;
+  return W8_OK;
+}
+
+// Sizes and strides of a paged cache beside 16-bit tensors of `dtype`.
+static w8_status check_paged(const char* fn, const w8_paged_desc* d, int32_t dtype, w8::PagedCache* c) {
+  if (!d) return fail(W8_ERR_NULL, "%s: NULL cache descriptor", fn);
+  if (d->dtype != dtype && d->dtype != W8_DTYPE_E4M3)
+    return fail(W8_ERR_DTYPE, "%s: cells of dtype %d beside tensors of dtype %d", fn, d->dtype, dtype);
+  const bool codes = d->dtype == W8_DTYPE_E4M3;
+  const int64_t unit = codes ? 16 : 8;
+  if (d->B < 0 || d->B > (1ll << 20)) return fail(W8_ERR_SHAPE, "%s: B=%lld", fn, (long long)d->B);
+  if (d->pages < 1 || d->pages > INT32_MAX) return fail(W8_ERR_SHAPE, "%s: pages=%lld", fn, (long long)d->pages);
+  if (d->page_size < 8 || d->page_size % 8 || d->page_size > (1ll << 20))
+    return fail(W8_ERR_SHAPE, "%s: page_size=%lld (need a multiple of 8)", fn, (long long)d->page_size);
+  if (d->table_cols < 0 || d->table_cols > (1ll << 26) || d->table_cols * d->page_size > (1ll << 26))
+    return fail(W8_ERR_SHAPE, "%s: %lld pages of %lld positions for a sequence (at most 2^26 positions)", fn,
+                (long long)d->table_cols, (long long)d->page_size);
+  if (d->B > 1 && d->table_stride < 0)
+    return fail(W8_ERR_STRIDE, "%s: table_stride=%lld", fn, (long long)d->table_stride);
+  if (d->D < unit || d->D > 128 || d->D % unit)
+    return fail(W8_ERR_SHAPE, "%s: D=%lld (need a multiple of %lld, at most 128)", fn, (long long)d->D, (long long)unit);
+  if (d->Hkv < 1 || d->Hkv > 65536) return fail(W8_ERR_SHAPE, "%s: Hkv=%lld", fn, (long long)d->Hkv);
+  const int64_t ext[3] = {d->pages, d->page_size, d->Hkv};
+  for (int t = 0; t < 2; ++t)
+    for (int i = 0; i < 3; ++i) {
+      const int64_t s = (t ? d->v_stride : d->k_stride)[i];
+      if (ext[i] > 1 && (s < unit || s % unit || s >= (1ll << 38)))
+        return fail(W8_ERR_STRIDE, "%s: stride %lld of %s (need a positive multiple of %lld elements)", fn, (long long)s,
+                    t ? "v_cache" : "k_cache", (long long)unit);
+    }
+  std::memset(c, 0, sizeof(*c));
+  c->B = (int)d->B;
+  c->pages = (int)d->pages;
+  c->page_size = (int)d->page_size;
+  c->cols = (int)d->table_cols;
+  c->table_stride = d->table_stride;
+  for (int i = 0; i < 3; ++i) {
+    c->ks[i] = d->k_stride[i];
+    c->vs[i] = d->v_stride[i];
+  }
+  c->codes = codes;
+  return W8_OK;
+}
+
+// The pointers of a paged cache and its batch.
+static w8_status set_paged(const char* fn, w8::PagedCache* c, const void* k_cache, const void* v_cache,
+                           const int32_t* page_table, const int32_t* q_start, const int32_t* kv_len,
+                           const float* k_scale, const float* v_scale, int64_t tokens) {
+  if (!k_cache || !v_cache || !kv_len || (c->cols > 0 && !page_table))
+    return fail(W8_ERR_NULL, "%s: NULL cache, page_table or kv_len", fn);
+  if (c->codes ? !k_scale || !v_scale : k_scale || v_scale)
+    return fail(c->codes ? W8_ERR_NULL : W8_ERR_PARAM, "%s: k_scale and v_scale belong to E4M3 cells", fn);
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned4(page_table) || !aligned4(q_start) || !aligned4(kv_len) ||
+      !aligned4(k_scale) || !aligned4(v_scale))
+    return fail(W8_ERR_ALIGN, "%s: caches must be 16-byte aligned, tables and scales 4", fn);
+  if (!q_start && tokens % c->B)
+    return fail(W8_ERR_SHAPE, "%s: %lld tokens of %d sequences without q_start", fn, (long long)tokens, c->B);
+  c->k = const_cast<void*>(k_cache);
+  c->v = const_cast<void*>(v_cache);
+  c->table = page_table;
+  c->q_start = q_start;
+  c->kv_len = kv_len;
+  c->k_scale = k_scale;
+  c->v_scale = v_scale;
+  return W8_OK;
+}
+
+// The pointers that both norm-and-rotation entries have.
+static w8_status set_rope(const char* fn, w8::RopeProblem* p, const void* q, const void* k, const int32_t* positions,
+                          const uint64_t* turns, const void* q_weight, const void* k_weight, void* q_out,
+                          bool own_positions) {
+  if ((p->Hq > 0 && (!q || !q_out)) || (p->Hkv > 0 && !k)) return fail(W8_ERR_NULL, "%s: NULL pointer", fn);
+  if (p->rot > 0 && (!turns || (!positions && !own_positions)))
+    return fail(W8_ERR_NULL, "%s: a rotation needs turns and positions", fn);
+  if (p->rot > 0 && !positions && p->axes != 1)
+    return fail(W8_ERR_SHAPE, "%s: %d axes without positions", fn, p->axes);
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(q_weight) || !aligned16(k_weight) ||
+      !aligned4(positions) || (reinterpret_cast<uintptr_t>(turns) & 7u))
+    return fail(W8_ERR_ALIGN, "%s: tensors must be 16-byte aligned, turns 8, positions 4", fn);
+  p->q = q;
+  p->k = k;
+  p->positions = p->rot > 0 ? positions : nullptr;
+  p->turns = turns;
+  p->q_weight = q_weight;
+  p->k_weight = k_weight;
+  p->norm_q = p->Hq > 0 && q_weight;
+  p->norm_k = p->Hkv > 0 && k_weight;
+  p->q_out = q_out;
+  return W8_OK;
+}
+
+w8_status qk_norm_rope(const w8_rope_desc* desc, const void* q, const void* k, const int32_t* positions,
+                       const uint64_t* turns, const void* q_weight, const void* k_weight, void* q_out, void* k_out,
+                       void* stream) {
+  w8::RopeProblem p;
+  w8_status st = check_rope("qk_norm_rope", desc, false, &p);
+  if (st != W8_OK) return st;
+  if (p.rot == 0 && !q_weight && !k_weight) return fail(W8_ERR_PARAM, "qk_norm_rope: neither a norm nor a rotation");
+  if (p.M == 0) return ok();
+  if ((st = set_rope("qk_norm_rope", &p, q, k, positions, turns, q_weight, k_weight, q_out, false)) != W8_OK) return st;
+  if (p.Hkv > 0 && !k_out) return fail(W8_ERR_NULL, "qk_norm_rope: NULL k_out");
+  if (!aligned16(k_out)) return fail(W8_ERR_ALIGN, "qk_norm_rope: k_out must be 16-byte aligned");
+  p.k_out = k_out;
+  int sms = 0;
+  if ((st = device_info(&sms)) != W8_OK) return st;
+  return cuda_status(w8::launch_norm_rope(p, nullptr, sms, static_cast<cudaStream_t>(stream)), "qk_norm_rope launch");
+}
+
+w8_status paged_kv_append(const w8_rope_desc* rope, const w8_paged_desc* cache, const void* q, const void* k,
+                          const void* v, const int32_t* positions, const uint64_t* turns, const void* q_weight,
+                          const void* k_weight, void* k_cache, void* v_cache, const int32_t* page_table,
+                          const int32_t* q_start, const int32_t* kv_len, const float* k_scale, const float* v_scale,
+                          void* q_out, void* stream) {
+  w8::RopeProblem p;
+  w8::PagedCache c;
+  w8_status st = check_rope("paged_kv_append", rope, true, &p);
+  if (st != W8_OK) return st;
+  if ((st = check_paged("paged_kv_append", cache, rope->dtype, &c)) != W8_OK) return st;
+  if (cache->Hkv != rope->Hkv || cache->D != rope->D)
+    return fail(W8_ERR_SHAPE, "paged_kv_append: keys [%lld, %lld] for a cache of [%lld, %lld]", (long long)rope->Hkv,
+                (long long)rope->D, (long long)cache->Hkv, (long long)cache->D);
+  if (p.M == 0 || c.B == 0) return ok();
+  if ((st = set_rope("paged_kv_append", &p, q, k, positions, turns, q_weight, k_weight, q_out, true)) != W8_OK) return st;
+  if ((st = set_paged("paged_kv_append", &c, k_cache, v_cache, page_table, q_start, kv_len, k_scale, v_scale, p.M)) !=
+      W8_OK)
+    return st;
+  if (!v) return fail(W8_ERR_NULL, "paged_kv_append: NULL v");
+  if (!aligned16(v)) return fail(W8_ERR_ALIGN, "paged_kv_append: v must be 16-byte aligned");
+  p.v = v;
+  int sms = 0;
+  if ((st = device_info(&sms)) != W8_OK) return st;
+  return cuda_status(w8::launch_norm_rope(p, &c, sms, static_cast<cudaStream_t>(stream)), "paged_kv_append launch");
+}
+
+// Sizes, strides and scalars of a paged attention, without its pointers.
+static w8_status check_paged_attention(const char* fn, const w8_paged_attention_desc* d, const w8_paged_desc* cache,
+                                       w8::PagedAttnProblem* p, w8::PagedCache* c) {
+  if (!d) return fail(W8_ERR_NULL, "%s: NULL descriptor", fn);
+  if (d->dtype != W8_DTYPE_BF16 && d->dtype != W8_DTYPE_F16)
+    return fail(W8_ERR_DTYPE, "%s: dtype %d is neither bf16 nor f16", fn, d->dtype);
+  w8_status st = check_paged(fn, cache, d->dtype, c);
+  if (st != W8_OK) return st;
+  if (d->Hq < 1 || d->Hq > (1ll << 23) || d->Hq % cache->Hkv || d->Hq / cache->Hkv > 128)
+    return fail(W8_ERR_SHAPE, "%s: Hq=%lld Hkv=%lld (need Hq a multiple of Hkv, at most 128 times it)", fn,
+                (long long)d->Hq, (long long)cache->Hkv);
+  if (d->T < 0 || d->T > (1ll << 30) || d->T * d->Hq > (1ll << 30))
+    return fail(W8_ERR_SHAPE, "%s: T=%lld Hq=%lld (at most 2^30 rows)", fn, (long long)d->T, (long long)d->Hq);
+  if (d->max_q < 1) return fail(W8_ERR_SHAPE, "%s: max_q=%lld", fn, (long long)d->max_q);
+  const int64_t max_q = d->max_q < d->T ? d->max_q : d->T;
+  // work items are counted in 32 bits
+  if ((double)c->B * (double)d->Hq * (double)max_q > (double)(1ll << 30))
+    return fail(W8_ERR_SHAPE, "%s: B * Hq * max_q is above 2^30", fn);
+  if (!std::isfinite(d->scale) || !(d->scale > 0.0f)) return fail(W8_ERR_PARAM, "%s: scale=%g", fn, (double)d->scale);
+  if ((st = check_strides(fn, "q", d->q_stride, d->T, d->Hq)) != W8_OK) return st;
+  if ((st = check_strides(fn, "out", d->o_stride, d->T, d->Hq)) != W8_OK) return st;
+  std::memset(p, 0, sizeof(*p));
+  p->T = d->T;
+  p->Hq = (int)d->Hq;
+  p->Hkv = (int)cache->Hkv;
+  p->D = (int)cache->D;
+  p->max_q = (int)max_q;
+  for (int i = 0; i < 2; ++i) {
+    p->qs[i] = d->q_stride[i];
+    p->os[i] = d->o_stride[i];
+  }
+  p->f16 = d->dtype == W8_DTYPE_F16;
+  p->causal = d->causal != 0;
+  p->scale = d->scale;
+  return W8_OK;
+}
+
+w8_status paged_attention_workspace(const w8_paged_attention_desc* desc, const w8_paged_desc* cache, int64_t* floats) {
+  if (!floats) return fail(W8_ERR_NULL, "paged_attention_workspace: NULL result");
+  w8::PagedAttnProblem p;
+  w8::PagedCache c;
+  w8_status st = check_paged_attention("paged_attention_workspace", desc, cache, &p, &c);
+  if (st != W8_OK) return st;
+  *floats = 0;
+  if (c.B == 0 || p.T == 0) return ok();
+  int sms = 0;
+  if ((st = device_info(&sms)) != W8_OK) return st;
+  *floats = w8::paged_attention_ws_floats(p, c, sms);
+  return ok();
+}
+
+w8_status paged_attention(const w8_paged_attention_desc* desc, const w8_paged_desc* cache, const void* q,
+                          const void* k_cache, const void* v_cache, const int32_t* page_table, const int32_t* q_start,
+                          const int32_t* kv_len, const float* k_scale, const float* v_scale, const float* s_out,
+                          void* out, float* ws, int64_t ws_floats, void* stream) {
+  w8::PagedAttnProblem p;
+  w8::PagedCache c;
+  w8_status st = check_paged_attention("paged_attention", desc, cache, &p, &c);
+  if (st != W8_OK) return st;
+  if (c.B == 0 || p.T == 0) return ok();
+  if (!q || !out) return fail(W8_ERR_NULL, "paged_attention: NULL pointer");
+  if ((st = set_paged("paged_attention", &c, k_cache, v_cache, page_table, q_start, kv_len, k_scale, v_scale, p.T)) != W8_OK)
+    return st;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(ws) || !aligned4(s_out))
+    return fail(W8_ERR_ALIGN, "paged_attention: q, out and ws must be 16-byte aligned");
+  int sms = 0;
+  if ((st = device_info(&sms)) != W8_OK) return st;
+  const int64_t need = w8::paged_attention_ws_floats(p, c, sms);
+  if (need > 0 && !ws) return fail(W8_ERR_NULL, "paged_attention: needs a workspace of %lld floats", (long long)need);
+  if (ws_floats < need)
+    return fail(W8_ERR_SHAPE, "paged_attention: workspace of %lld floats, %lld needed", (long long)ws_floats, (long long)need);
+  p.q = q;
+  p.s_out = s_out;
+  p.out = out;
+  p.ws = ws;
+  int terr = 0;
+  cudaError_t e = w8::launch_paged_attention(p, c, sms, static_cast<cudaStream_t>(stream), &terr);
+  if (terr) return fail(W8_ERR_ALIGN, "paged_attention: tensor map encoding rejected the operands");
+  return cuda_status(e, "paged_attention launch");
 }
 
 w8_status step_policy_dispatch(const w8_step_policy* policy, int32_t step, int32_t num_steps,

@@ -104,6 +104,49 @@ cudaError_t launch_cross_attention(const AttnProblem& p, int sms, cudaStream_t s
 // Reads and clears the attention kernels' device error word (synchronises `st`).
 cudaError_t attention_read_error(cudaStream_t st, uint32_t* err);
 
+// ---- norms and rotation of heads, and their way into a paged cache (rope.cu)
+struct PagedCache {              // validated by the caller
+  int B, pages, page_size, cols; // sequences, pages of the cache, positions of a page, columns of the table
+  int64_t table_stride;          // entries between the sequences of the table
+  int64_t ks[3], vs[3];          // element strides: page, position, head
+  bool codes;                    // E4M3 cells
+  void *k, *v;
+  const int32_t *table, *q_start, *kv_len;   // q_start null: T / B tokens of each sequence
+  const float *k_scale, *v_scale;            // of codes
+};
+struct RopeProblem {             // validated by the caller
+  int64_t M;
+  int Hq, Hkv, D, rot;
+  int64_t qs[2], ks[2], vs[2], qos[2], kos[2];   // element strides: row, head
+  bool f16, interleaved, norm_q, norm_k;
+  int axes, axis_pairs[3];
+  float eps, amplitude;
+  const void *q, *k, *v, *q_weight, *k_weight;
+  const int32_t* positions;      // [axes, M], rows pos_stride apart, or null: the sequence's own (append)
+  int64_t pos_stride;
+  const uint64_t* turns;         // [rot / 2]
+  void *q_out, *k_out;
+};
+// cache null: k goes to k_out, there is no v.  Else k and v go into the cache.
+cudaError_t launch_norm_rope(const RopeProblem& p, const PagedCache* cache, int sms, cudaStream_t st);
+
+// ---- attention over a paged cache (paged_attention.cu)
+struct PagedAttnProblem {        // validated by the caller
+  int64_t T;
+  int Hq, Hkv, D, max_q;
+  int64_t qs[2], os[2];          // element strides: row, head
+  bool f16, causal;
+  float scale;
+  const void* q;
+  const float* s_out;            // not null: E4M3 output
+  void* out;
+  float* ws;                     // paged_attention_ws_floats() floats
+};
+int64_t paged_attention_ws_floats(const PagedAttnProblem& p, const PagedCache& c, int sms);
+cudaError_t launch_paged_attention(const PagedAttnProblem& p, const PagedCache& c, int sms, cudaStream_t st, int* tmap_err);
+// Reads and clears the paged attention kernels' device error word (synchronises `st`).
+cudaError_t paged_attention_read_error(cudaStream_t st, uint32_t* err);
+
 // Launches a one-thread kernel whose mbarrier wait times out (0.2 s).
 cudaError_t launch_selftest_timeout(cudaStream_t st);
 
