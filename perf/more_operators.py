@@ -234,8 +234,9 @@ def _run_own(s):
         return {"q": q, "k": k}
     if s["op"] == "append":
         q = W.paged_kv_append(s["k"], s["v"], s["k_cache"], s["v_cache"], s["page_table"], s["q_start"], s["kv_len"],
-                              turns=s["turns"], q=s["q"], q_weight=s["q_weight"], k_weight=s["k_weight"], eps=EPS,
-                              interleaved=s["interleaved"], k_scale=s["k_scale"], v_scale=s["v_scale"], q_out=s["q_out"])
+                              turns=s["turns"], q=s["q"], q_weight=s["q_weight"] if s["queries"] else None,
+                              k_weight=s["k_weight"], eps=EPS, interleaved=s["interleaved"], k_scale=s["k_scale"],
+                              v_scale=s["v_scale"], q_out=s["q_out"])
         return {"q": q, **_caches(s)}
     out = W.paged_attention(s["q"], s["k_cache"], s["v_cache"], s["page_table"], s["q_start"], s["kv_len"],
                             max_q=max(s["new_lens"]), causal=s["causal"], k_scale=s["k_scale"], v_scale=s["v_scale"],
