@@ -109,6 +109,23 @@ __device__ __forceinline__ float ld_f32(const float* p) {
   return v;
 }
 
+__device__ __forceinline__ int ld_i32(const int32_t* p) {
+  int v;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// 16 bytes that are read once.  Not the read-only path: an output may be the
+// input's own memory.
+__device__ __forceinline__ uint4 ld16_once(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
 // One whole 32-byte sector from one thread (32-byte aligned).
 __device__ __forceinline__ void st_global_32(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e,
                                              uint32_t f, uint32_t g, uint32_t h) {

@@ -35,17 +35,6 @@ namespace {
 constexpr int kMaxThreads = 512;              // K <= 8 * 4 * 512 = 16384
 constexpr float kTinyScale = 1.17549435e-38f; // 2^-126: a zero row's scale, so that its codes are zero
 
-// 16 bytes that are read once.  Not the read-only path: res_out may be the
-// residual's own memory.
-__device__ __forceinline__ uint4 ld16_once(const uint16_t* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
-               : "memory");
-  return v;
-}
-
 struct NormArgs {
   const uint16_t *x, *res, *w;
   int64_t M;

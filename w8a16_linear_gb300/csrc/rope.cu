@@ -33,22 +33,6 @@ namespace {
 constexpr int kWarps = 4;          // of a block
 constexpr int kAhead = 4;          // loads of a lane in flight
 
-// 16 bytes that are read once.  Not the read-only path: an output may be the
-// input's own memory.
-__device__ __forceinline__ uint4 ld16_once(const uint16_t* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ int ld_i32(const int32_t* p) {
-  int v;
-  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
-
 struct RopeArgs {
   RopeProblem p;
   PagedCache c;
