@@ -31,184 +31,213 @@ namespace w8 {
 namespace {
 
 constexpr int kWarps = 4;          // of a block
-constexpr int kAhead = 4;          // loads of a lane in flight
+constexpr int kAhead = 2;          // chunks of heads that are loaded ahead
 
 struct RopeArgs {
   RopeProblem p;
   PagedCache c;
-  int split;        // warps of a token
+  int split, per;   // warps of a token, chunks of heads of each
   float inv_d;
 };
 
-// kLanes: lanes of a head (a power of two; 8 dimensions each).  kPaged: k and v
-// go into the cache; else k to k_out.
+// Four 16-bit values as two packed words.
+__device__ __forceinline__ uint2 ld8_once(const uint16_t* p) {
+  uint2 v;
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
+  return v;
+}
+
+// kLanes: lanes of a head (a power of two), of eight dimensions each: 8 u .. 8 u + 7
+// in lane u, or where pairs are half-split four of either half, 4 u .. and rot / 2 + 4 u ..,
+// so that a pair is in one lane.  kPaged: k and v go into the cache; else k to k_out.
 template <bool kF16, int kLanes, bool kInterleaved, bool kPaged>
-__global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, 8) norm_rope_kernel(const __grid_constant__ RopeArgs a) {
   griddep_launch_dependents();
   constexpr int kHeads = 32 / kLanes;                       // heads that a warp has at a time
   const RopeProblem& p = a.p;
   const int lane = threadIdx.x & 31, sub = lane % kLanes, head0 = lane / kLanes;
   const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int64_t t = w / a.split;
+  const int64_t t = a.split == 1 ? w : w / a.split;
   const int part = (int)(w - t * a.split);
   const bool on = 8 * sub < p.D;                            // lanes beyond D hold nothing
   griddep_wait();   // from here on what earlier kernels wrote may be read
   if (t >= p.M) return;
 
-  // Where the token stands: its sequence, and there its position and cell.
-  int64_t pos = 0, cell_k = -1, cell_v = -1;
+  // The lane's dimensions: four from d0 and four from d1.
+  const bool turned = 8 * sub < p.rot;
+  const bool split_pairs = !kInterleaved && turned;
+  const int d0 = split_pairs ? 4 * sub : 8 * sub, d1 = split_pairs ? (p.rot >> 1) + 4 * sub : 8 * sub + 4;
+  auto load = [&](const uint16_t* from) {
+    if (kInterleaved) return ld16_once(from + 8 * sub);
+    const uint2 lo = ld8_once(from + d0), hi = ld8_once(from + d1);
+    return make_uint4(lo.x, lo.y, hi.x, hi.y);
+  };
+  // The token's heads, kHeads of a kind at a time: queries, keys and, into a cache, values.
+  const int q_chunks = (p.Hq + kHeads - 1) / kHeads, k_chunks = (p.Hkv + kHeads - 1) / kHeads;
+  const int chunks = q_chunks + k_chunks * (kPaged ? 2 : 1);
+  const uint16_t* q_at = static_cast<const uint16_t*>(p.q) + t * p.qs[0] + head0 * p.qs[1];
+  const uint16_t* k_at = static_cast<const uint16_t*>(p.k) + t * p.ks[0] + head0 * p.ks[1];
+  const uint16_t* v_at = static_cast<const uint16_t*>(p.v) + t * p.vs[0] + head0 * p.vs[1];
+  const int end = min(chunks, (part + 1) * a.per);
+  uint4 next[kAhead];
+  auto fetch = [&](int first) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int c = first + u, ck = c - q_chunks, cv = ck - k_chunks;
+      next[u] = make_uint4(0, 0, 0, 0);
+      if (!on || c >= end) continue;
+      if (c < q_chunks) {
+        if (c * kHeads + head0 < p.Hq) next[u] = load(q_at + c * kHeads * p.qs[1]);
+      } else if (ck < k_chunks) {
+        if (ck * kHeads + head0 < p.Hkv) next[u] = load(k_at + ck * kHeads * p.ks[1]);
+      } else if (kPaged && cv < k_chunks) {
+        if (cv * kHeads + head0 < p.Hkv) next[u] = load(v_at + cv * kHeads * p.vs[1]);
+      }
+    }
+  };
+  fetch(part * a.per);   // before the places and angles, which they do not need
+
+  // Where the token stands: its sequence, its position there, and that one's page.
+  int64_t pos = 0;
+  int page = -1, slot = 0;
   if (kPaged) {
     const PagedCache& c = a.c;
-    int b;
+    int b, kv;
     int64_t begin, end;
-    if (c.q_start) {
+    if (c.q_start && c.B < 32) {   // a lane for each sequence: one round trip
+      const int start = ld_i32(c.q_start + min(lane, c.B)), len = ld_i32(c.kv_len + min(lane, c.B - 1));
+      b = __popc(__ballot_sync(0xFFFFFFFFu, lane >= 1 && lane <= c.B && start <= t));
+      begin = __shfl_sync(0xFFFFFFFFu, start, b);
+      end = __shfl_sync(0xFFFFFFFFu, start, min(b + 1, c.B));
+      kv = __shfl_sync(0xFFFFFFFFu, len, min(b, c.B - 1));
+      if (b >= c.B || t < begin || t >= end) return;        // of no sequence
+    } else if (c.q_start) {
       int n = 0;   // sequences that begin at t or before it, the first aside
       for (int k = lane + 1; k <= c.B; k += 32) n += ld_i32(c.q_start + k) <= t;
       b = __reduce_add_sync(0xFFFFFFFFu, n);
-      if (b >= c.B) return;                                 // behind the last sequence
+      if (b >= c.B) return;
       begin = ld_i32(c.q_start + b);
       end = ld_i32(c.q_start + b + 1);
+      kv = ld_i32(c.kv_len + b);
       if (t < begin || t >= end) return;
     } else {
-      const int64_t per = p.M / c.B;
-      b = (int)(t / per);
-      end = (b + 1) * per;
+      const int per = (int)(p.M / c.B);
+      b = (int)t / per;
+      end = (int64_t)(b + 1) * per;
+      kv = ld_i32(c.kv_len + b);
     }
-    pos = ld_i32(c.kv_len + b) - (end - t);
-    const int64_t page_at = pos / c.page_size;
-    if (pos >= 0 && page_at < c.cols) {
-      const int page = ld_i32(c.table + b * c.table_stride + page_at);
-      const int64_t slot = pos - page_at * c.page_size;
-      if (page >= 0 && page < c.pages) {
-        cell_k = page * c.ks[0] + slot * c.ks[1];
-        cell_v = page * c.vs[0] + slot * c.vs[1];
-      }
+    pos = kv - (end - t);
+    if (pos >= 0 && pos < (int64_t)c.cols * c.page_size) {
+      const int page_at = (int)pos / c.page_size;
+      slot = (int)pos - page_at * c.page_size;
+      page = ld_i32(c.table + b * c.table_stride + page_at);   // used with the first key: in flight until then
     }
   }
 
-  // Cosines and sines of the lane's dimensions.
-  constexpr int kTurns = kInterleaved ? 4 : 8;
-  float cs[kTurns], sn[kTurns];
-  const bool turned = 8 * sub < p.rot;
-  const int half = p.rot >> 1;
-  const bool second = !kInterleaved && 8 * sub >= half;     // of a half-split pair
-  const int partner = kInterleaved || !turned ? lane : second ? lane - (half >> 3) : lane + (half >> 3);
+  // Cosines and sines of the lane's pairs.
+  float cs[4] = {1.0f, 1.0f, 1.0f, 1.0f}, sn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (turned) {
-    const int pair0 = kInterleaved ? 4 * sub : 8 * sub - (second ? half : 0);
     int64_t at[3] = {pos, pos, pos};
     if (p.positions)
 #pragma unroll
       for (int x = 0; x < 3; ++x)
         if (x < p.axes) at[x] = ld_i32(p.positions + x * p.pos_stride + t);
 #pragma unroll
-    for (int j = 0; j < kTurns; ++j) {
-      const int i = pair0 + j;
+    for (int j = 0; j < 4; ++j) {
+      const int i = 4 * sub + j;
       const int64_t q = i < p.axis_pairs[0] ? at[0] : i < p.axis_pairs[0] + p.axis_pairs[1] ? at[1] : at[2];
       const uint64_t phase = (uint64_t)q * __ldg(p.turns + i);
       sincospif((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, &sn[j], &cs[j]);   // 2^-31 of a half turn
       cs[j] *= p.amplitude;
-      sn[j] *= second ? -p.amplitude : p.amplitude;         // b takes + a s, a takes - b s
+      sn[j] *= p.amplitude;
     }
   }
+  auto put = [&](uint16_t* to, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+    if (kInterleaved) {
+      *reinterpret_cast<uint4*>(to + 8 * sub) = make_uint4(w0, w1, w2, w3);
+    } else {
+      *reinterpret_cast<uint2*>(to + d0) = make_uint2(w0, w1);
+      *reinterpret_cast<uint2*>(to + d1) = make_uint2(w2, w3);
+    }
+  };
   uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
-  if (on && p.norm_q) wq = ldg16(static_cast<const uint16_t*>(p.q_weight) + 8 * sub);
-  if (on && p.norm_k) wk = ldg16(static_cast<const uint16_t*>(p.k_weight) + 8 * sub);
-  float inv_ks = 1.0f, inv_vs = 1.0f;
-  if (kPaged && a.c.codes) {
-    inv_ks = __frcp_rn(ld_f32(a.c.k_scale));
-    inv_vs = __frcp_rn(ld_f32(a.c.v_scale));
-  }
+  if (on && p.norm_q) wq = load(static_cast<const uint16_t*>(p.q_weight));
+  if (on && p.norm_k) wk = load(static_cast<const uint16_t*>(p.k_weight));
 
-  // The token's heads: queries, keys and, into a cache, values.
-  const int heads = p.Hq + p.Hkv + (kPaged ? p.Hkv : 0);
-  const int chunks = (heads + kHeads - 1) / kHeads;
-  for (int first = part * kAhead; first < chunks; first += a.split * kAhead) {
+  for (int first = part * a.per; first < end; first += kAhead) {
     uint4 x[kAhead];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int h = (first + u) * kHeads + head0;
-      x[u] = make_uint4(0, 0, 0, 0);
-      if (!on || h >= heads) continue;
-      const uint16_t* from;
-      if (h < p.Hq) from = static_cast<const uint16_t*>(p.q) + t * p.qs[0] + h * p.qs[1];
-      else if (h < p.Hq + p.Hkv) from = static_cast<const uint16_t*>(p.k) + t * p.ks[0] + (h - p.Hq) * p.ks[1];
-      else from = static_cast<const uint16_t*>(p.v) + t * p.vs[0] + (h - p.Hq - p.Hkv) * p.vs[1];
-      x[u] = ld16_once(from + 8 * sub);
-    }
+    for (int u = 0; u < kAhead; ++u) x[u] = next[u];
+    fetch(first + kAhead);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      if (first + u >= chunks) break;                       // the same for the whole warp
-      const int h = (first + u) * kHeads + head0;
-      const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
+      // kinds and counts of a chunk are the same for the whole warp
+      const int c = first + u, ck = c - q_chunks, cv = ck - k_chunks;
+      if (c >= end) break;
+      const bool is_q = c < q_chunks, is_v = kPaged && cv >= 0;
+      const int h = (is_q ? c : is_v ? cv : ck) * kHeads + head0;
+      const bool there = on && h < (is_q ? p.Hq : p.Hkv);
       const uint32_t xw[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-      float v[8];
+      uint32_t out[4] = {xw[0], xw[1], xw[2], xw[3]};
+      F2 v[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const F2 f = unpack16<kF16>(xw[c]);
-        v[2 * c] = f.x;
-        v[2 * c + 1] = f.y;
-      }
-      if (p.norm_q || p.norm_k) {
-        float ss = 0.0f;
+      for (int e = 0; e < 4; ++e) v[e] = unpack16<kF16>(xw[e]);
+      if (!is_v) {
+        if (is_q ? p.norm_q : p.norm_k) {
+          F2 s2 = mul2(v[0], v[0]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
+          for (int e = 1; e < 4; ++e) s2 = fma2(v[e], v[e], s2);
+          float ss = __fadd_rn(s2.x, s2.y);
 #pragma unroll
-        for (int o = kLanes / 2; o >= 1; o /= 2) ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, o));
-        if (is_q ? p.norm_q : p.norm_k && !is_v) {
-          const float inv = rsqrtf(fmaf(ss, a.inv_d, p.eps));
+          for (int o = kLanes / 2; o >= 1; o /= 2) ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, o));
+          const F2 inv = splat(rsqrtf(fmaf(ss, a.inv_d, p.eps)));
           const uint32_t ww[4] = {is_q ? wq.x : wk.x, is_q ? wq.y : wk.y, is_q ? wq.z : wk.z, is_q ? wq.w : wk.w};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const F2 f = unpack16<kF16>(ww[c]);
-            v[2 * c] = __fmul_rn(__fmul_rn(v[2 * c], f.x), inv);
-            v[2 * c + 1] = __fmul_rn(__fmul_rn(v[2 * c + 1], f.y), inv);
+          for (int e = 0; e < 4; ++e) v[e] = mul2(mul2(v[e], unpack16<kF16>(ww[e])), inv);
+        }
+        if (turned) {
+          if (kInterleaved) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[e] = fma2(v[e], splat(cs[e]), mul2(F2{v[e].y, v[e].x}, F2{-sn[e], sn[e]}));
+          } else {   // pairs of v[0], v[1] and v[2], v[3]
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const F2 c2 = F2{cs[2 * e], cs[2 * e + 1]}, s2 = F2{sn[2 * e], sn[2 * e + 1]};
+              const F2 lo = v[e], hi = v[e + 2];
+              v[e] = fma2(lo, c2, mul2(neg(hi), s2));
+              v[e + 2] = fma2(hi, c2, mul2(lo, s2));
+            }
           }
         }
-      }
-      float y[8];
-      if (kInterleaved) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          y[2 * j] = v[2 * j];
-          y[2 * j + 1] = v[2 * j + 1];
-          if (turned && !is_v) {
-            y[2 * j] = fmaf(v[2 * j], cs[j % kTurns], -__fmul_rn(v[2 * j + 1], sn[j % kTurns]));
-            y[2 * j + 1] = fmaf(v[2 * j + 1], cs[j % kTurns], __fmul_rn(v[2 * j], sn[j % kTurns]));
-          }
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float other = __shfl_sync(0xFFFFFFFFu, v[e], partner);
-          y[e] = v[e];
-          if (turned && !is_v) y[e] = fmaf(v[e], cs[e % kTurns], -__fmul_rn(other, sn[e % kTurns]));
-        }
+        for (int e = 0; e < 4; ++e) out[e] = cvt16x2(kF16, v[e].x, v[e].y);
       }
-      if (!on || h >= heads) continue;
-      uint16_t* to = nullptr;
+      if (!there) continue;
       if (is_q) {
-        to = static_cast<uint16_t*>(p.q_out) + t * p.qos[0] + h * p.qos[1];
+        put(static_cast<uint16_t*>(p.q_out) + t * p.qos[0] + h * p.qos[1], out[0], out[1], out[2], out[3]);
       } else if (!kPaged) {
-        to = static_cast<uint16_t*>(p.k_out) + t * p.kos[0] + (h - p.Hq) * p.kos[1];
+        put(static_cast<uint16_t*>(p.k_out) + t * p.kos[0] + h * p.kos[1], out[0], out[1], out[2], out[3]);
       } else {
-        const int64_t cell = is_v ? cell_v : cell_k;
-        if (cell < 0) continue;                             // a position without a page
-        const int64_t at = cell + (is_v ? (h - p.Hq - p.Hkv) * a.c.vs[2] : (h - p.Hq) * a.c.ks[2]) + 8 * sub;
+        if (page < 0 || page >= a.c.pages) continue;        // a position without a page
+        const int64_t* cs3 = is_v ? a.c.vs : a.c.ks;
+        const int64_t at = page * cs3[0] + slot * cs3[1] + h * cs3[2];
+        void* cache = is_v ? a.c.v : a.c.k;
         if (a.c.codes) {
-          const float f = is_v ? inv_vs : inv_ks;
+          const F2 f = splat(__frcp_rn(ld_f32(is_v ? a.c.v_scale : a.c.k_scale)));
           uint32_t q[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) q[c] = cvt_e4m3x2(__fmul_rn(y[2 * c], f), __fmul_rn(y[2 * c + 1], f));
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? a.c.v : a.c.k) + at) =
-              make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
-          continue;
+          for (int e = 0; e < 4; ++e) {
+            const F2 y = mul2(v[e], f);
+            q[e] = cvt_e4m3x2(y.x, y.y);
+          }
+          uint8_t* to = static_cast<uint8_t*>(cache) + at;
+          *reinterpret_cast<uint32_t*>(to + d0) = q[0] | (q[1] << 16);
+          *reinterpret_cast<uint32_t*>(to + d1) = q[2] | (q[3] << 16);
+        } else {
+          put(static_cast<uint16_t*>(cache) + at, out[0], out[1], out[2], out[3]);
         }
-        to = static_cast<uint16_t*>(is_v ? a.c.v : a.c.k) + at - 8 * sub;
       }
-      uint32_t q[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) q[c] = is_v ? xw[c] : cvt16x2(kF16, y[2 * c], y[2 * c + 1]);
-      *reinterpret_cast<uint4*>(to + 8 * sub) = make_uint4(q[0], q[1], q[2], q[3]);
     }
   }
 }
@@ -252,12 +281,13 @@ cudaError_t launch_norm_rope(const RopeProblem& p, const PagedCache* cache, int 
   if (cache) a.c = *cache;
   a.inv_d = 1.0f / (float)p.D;
   const int lanes = p.D <= 64 ? 8 : p.D <= 128 ? 16 : 32;
-  const int heads = p.Hq + p.Hkv * (cache ? 2 : 1);
-  const int chunks = (heads * lanes + 31) / 32, rounds = (chunks + kAhead - 1) / kAhead;   // that one warp would make
-  int64_t split = 16ll * sms / p.M;                            // 16 warps an SM
-  split = split < 1 ? 1 : split > rounds ? rounds : split;
-  a.split = (int)split;
-  const int64_t blocks = (p.M * split + kWarps - 1) / kWarps;
+  const int per = 32 / lanes;                                  // heads of a chunk
+  const int chunks = (p.Hq + per - 1) / per + (p.Hkv + per - 1) / per * (cache ? 2 : 1);
+  int64_t split = 64ll * sms / p.M;                            // 64 warps an SM
+  split = split < 1 ? 1 : split > chunks ? chunks : split;
+  a.per = (int)((chunks + split - 1) / split);
+  a.split = (chunks + a.per - 1) / a.per;
+  const int64_t blocks = (p.M * a.split + kWarps - 1) / kWarps;
   return p.f16 ? launch_type<true>(a, cache != nullptr, blocks, st) : launch_type<false>(a, cache != nullptr, blocks, st);
 }
 
