@@ -17,7 +17,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libw8lin.so")
-SOURCES = ["api.cu", "attention.cu", "elementwise.cu", "gemm.cu", "noalloc.cu", "paged_attention.cu", "policy.cu",
+SOURCES = ["api.cu", "attention.cu", "elementwise.cu", "gemm.cu", "noalloc.cu", "paged_attention.cu", "paged_few.cu", "policy.cu",
            "rmsnorm.cu", "rope.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

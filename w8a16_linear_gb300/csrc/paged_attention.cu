@@ -43,19 +43,17 @@
 
 #include "attention_common.cuh"
 #include "internal.h"
+#include "paged_common.cuh"
 #include "ptx.cuh"
 #include "swiglu_spec.cuh"
 
 namespace w8 {
 
-__device__ uint32_t g_paged_err;   // kErrTimeout when a pipeline wait gives up
-
 namespace {
 
-// Sequences that are kept in shared memory; of more, units are never cut.
-constexpr int kMaxSeqs = 512;
-constexpr int kThreads = 512;
-constexpr int kInfo = 8;           // words about a share for the joining kernel
+// With 256 rows a unit cutting costs the time of about 10 tiles, with 128 rows about 8
+// (measured for cross attention, whose tiles these are).
+constexpr Cutting kCutShared{8, 1.0f, 10.0f}, kCutSplit{4, 1.4f, 8.0f};
 
 template <int DP, bool kCodes, bool kShared>
 struct Cfg {
@@ -84,273 +82,6 @@ struct Cfg {
   static constexpr int kAlloc = kDirty + 4 + 1024;       // slack for 1024-byte alignment
   static_assert(kAlloc <= 232448, "shared memory budget");
 };
-
-// Words of kState: how the work is shared out, and where this CTA begins.
-enum { kShares, kTotal, kZeros, kAtB, kAtHk, kAtBlk, kAtTile };
-
-struct PagedArgs {
-  int B, T, Hkv, G, D;
-  int rows_l;                 // tokens per slot: 128 / G
-  int per;                    // tokens of a unit
-  int max_q;
-  int blocks;                 // units of a sequence and key head at most
-  int items;                  // B * Hkv * blocks
-  uint64_t by_bh, by_hkv, by_page;   // 2^64 / d rounded up, 0 for d = 1
-  int causal;
-  int may_cut;
-  int pages, page_size, cols, box, boxes;   // rows of a copy, copies of a tile and 64 dimensions
-  int64_t table_stride;
-  const int32_t *table, *q_start, *kv_len;
-  const float *k_scale, *v_scale;           // of codes
-  const uint8_t* v;           // the cache and its strides in bytes, for spoil()
-  int64_t vs[3];
-  float scale_log2;
-  const float* s_out;         // not null: E4M3 output
-  void* out;
-  int64_t o_l, o_h;           // element strides of the output
-  int wide;                   // output rows are 32-byte aligned and whole multiples of 32 bytes
-  int tma_out;                // a warp's 32 rows are whole tokens, which one bulk copy can write
-  float* part;                // may_cut: two partial results of each CTA, normalised
-  float* part_lse;            // and the log2 of their sums
-  int* info;                  // and kInfo words about each share
-};
-
-struct PagedMaps {
-  CUtensorMap q, k, v, o;
-};
-
-// What is known of a sequence: the row of its first token, its tokens (of those
-// that are worked on), the position of the first and the positions that there are.
-struct Seq {
-  int row0, tokens, base, len;
-};
-
-__device__ __forceinline__ Seq load_seq(const PagedArgs& a, int b) {
-  int q0, q1;
-  if (a.q_start) {
-    q0 = min(max(ld_i32(a.q_start + b), 0), a.T);
-    q1 = min(max(ld_i32(a.q_start + b + 1), q0), a.T);
-  } else {
-    q0 = a.T / a.B * b;
-    q1 = q0 + a.T / a.B;
-  }
-  const int kv = min(max(ld_i32(a.kv_len + b), 0), 1 << 30);
-  return Seq{q0, min(q1 - q0, a.max_q), kv - (q1 - q0), min(kv, a.cols * a.page_size)};
-}
-
-// One unit of work (or the part of one that is a CTA's).
-struct Item {
-  int b, hk;
-  int row0, left; // row of its first token; its tokens
-  int pos0;       // position of the first
-  int limit;      // positions that some token sees, and that the first sees
-  int lim0;
-  int len;
-  int t0, t1;     // key tiles
-  int part;       // the partial result it writes, or -1: its output rows
-  __device__ __forceinline__ int n() const { return t1 - t0; }
-};
-
-// Positions that the tokens before token `end` of a sequence see, `base` being the first one's.
-__device__ __forceinline__ int seen(const PagedArgs& a, int base, int len, int end) {
-  return a.causal ? min(max(base + end, 0), len) : len;
-}
-
-// A CTA's units, in the order in which each of its roles goes through them.
-struct Units {
-  const PagedArgs& a;
-  const Seq* seqs;            // in shared memory, or null
-  const uint32_t* tiles;
-  const volatile int* state;
-  uint32_t cur, end;          // the next item, or cut: the next tile and the share's end
-  int b, hk, blk, t;          // cut: where that tile is
-  uint32_t begin;
-  bool cut;
-
-  __device__ __forceinline__ Units(const PagedArgs& args, const Seq* s, const uint32_t* tl, const volatile int* st)
-      : a(args), seqs(s), tiles(tl), state(st) {
-    cut = a.may_cut && state[kShares] > 0;
-    if (cut) {
-      const uint32_t shares = (uint32_t)state[kShares], total = (uint32_t)state[kTotal];
-      begin = cur = blockIdx.x < shares ? share_begin(total, blockIdx.x, shares) : total;
-      end = blockIdx.x < shares ? share_begin(total, blockIdx.x + 1, shares) : total;
-      b = state[kAtB], hk = state[kAtHk], blk = state[kAtBlk], t = state[kAtTile];
-    } else {
-      cur = blockIdx.x;
-    }
-  }
-  // The unit of block `at`; false where the sequence has no such tokens.
-  __device__ __forceinline__ bool fill(Item& x, int at) const {
-    const Seq s = seqs ? seqs[x.b] : load_seq(a, x.b);
-    const int first = at * a.per;
-    if (first >= s.tokens) return false;
-    x.left = min(a.per, s.tokens - first);
-    x.row0 = s.row0 + first;
-    x.pos0 = s.base + first;
-    x.len = s.len;
-    x.limit = seen(a, s.base, s.len, first + x.left);
-    x.lim0 = seen(a, s.base, s.len, first + 1);
-    x.t0 = 0;
-    x.t1 = (x.limit + kKeys - 1) / kKeys;
-    return true;
-  }
-  __device__ __forceinline__ bool next(Item& x) {
-    x.part = -1;
-    if (!cut) {
-      while (cur < (uint32_t)a.items) {
-        const int q = quotient((int)cur, a.by_bh), r = (int)cur - q * (a.B * a.Hkv);
-        x.b = quotient(r, a.by_hkv);
-        x.hk = r - x.b * a.Hkv;
-        cur += gridDim.x;
-        if (fill(x, a.blocks - 1 - q)) return true;   // the longest first
-      }
-      return false;
-    }
-    if (cur >= end) return false;
-    for (;;) {                                        // the unit that holds tile `cur`
-      x.b = b;
-      if (!fill(x, blk)) {
-        blk = 0;
-        if (++hk == a.Hkv) {
-          hk = 0;
-          while (++b < a.B - 1 && tiles[b] == 0) {
-          }
-        }
-      } else if (x.t1 == 0) {
-        ++blk;
-      } else {
-        break;
-      }
-    }
-    x.hk = hk;
-    const int all = x.t1;
-    x.t0 = t;
-    x.t1 = (int)min((uint32_t)all, (uint32_t)t + (end - cur));
-    if (x.n() < all) x.part = 2 * blockIdx.x + (cur == begin ? 0 : 1);
-    cur += (uint32_t)x.n();
-    t = x.t1;
-    if (t == all) {
-      t = 0;
-      ++blk;
-    }
-    return true;
-  }
-};
-
-__device__ __forceinline__ void record_timeout(volatile int* abort) {
-  *abort = 1;
-  atomicOr(&g_paged_err, kErrTimeout);
-}
-
-// Whether a half of one of the words (two 16-bit values each) is not finite.
-template <bool kF16>
-__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
-  constexpr uint32_t kExp = kF16 ? 0x7C007C00u : 0x7F807F80u, kOne = kF16 ? 0x04000400u : 0x00800080u;
-  return ((w & kExp) + kOne) & 0x80008000u;
-}
-
-// How the work is shared out, from the sequences in shared memory (all threads).
-// Whole units or even shares of their tiles: by an estimate of either's time, in tiles of
-// one CTA.  Cutting costs the writing and joining of the partial results: with 256
-// rows a unit the time of about 10 tiles, with 128 rows about 8, and the tiles get slower as
-// more CTAs load at once (measured for cross attention, whose tiles these are).
-template <bool kShared>
-__device__ __forceinline__ void share_out(const PagedArgs& a, const Seq* seqs, uint32_t* tiles, uint32_t* first, int* state) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int b = warp; b < a.B; b += kThreads / 32) {
-    const Seq s = seqs[b];
-    uint32_t sum = 0;
-    for (int f = lane * a.per; f < s.tokens; f += 32 * a.per)
-      sum += (uint32_t)(seen(a, s.base, s.len, min(f + a.per, s.tokens)) + kKeys - 1) / kKeys;
-    sum = __reduce_add_sync(0xFFFFFFFFu, sum);
-    if (lane == 0) tiles[b] = sum;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    uint32_t total = 0, items = 0, longest = 0, zeros = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-      const int b = b0 + lane;
-      uint32_t mine = 0;
-      if (b < a.B) {
-        const Seq s = seqs[b];
-        mine = tiles[b] * (uint32_t)a.Hkv;
-        const uint32_t units = (uint32_t)(s.tokens + a.per - 1) / (uint32_t)a.per;
-        items += units * (uint32_t)a.Hkv;
-        if (units) {
-          longest = max(longest, (uint32_t)(seen(a, s.base, s.len, s.tokens) + kKeys - 1) / kKeys);
-          zeros |= seen(a, s.base, s.len, min(a.per, s.tokens)) == 0;
-        }
-      }
-      uint32_t to = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, to, o);
-        if (lane >= o) to += v;
-      }
-      if (b < a.B) first[b] = total + to - mine;
-      total += __shfl_sync(0xFFFFFFFFu, to, 31);
-    }
-    items = __reduce_add_sync(0xFFFFFFFFu, items);
-    longest = __reduce_max_sync(0xFFFFFFFFu, longest);
-    zeros = __reduce_or_sync(0xFFFFFFFFu, zeros);
-    const uint32_t ctas = gridDim.x;
-    const uint32_t share = max((total + ctas - 1) / ctas, kShared ? 8u : 4u);
-    const float whole = items <= ctas ? (float)longest : fmaxf((float)longest, (float)total / (float)ctas + 0.5f * (float)longest);
-    const float mine = kShared ? (float)share + 10.0f : 1.4f * (float)share + 8.0f;
-    const uint32_t shares = mine < whole ? (total + share - 1) / share : 0;
-    int at_b = 0, at_hk = 0, at_blk = 0, at_t = 0, at_tiles = 0;
-    if (blockIdx.x < shares) {
-      const uint32_t p = share_begin(total, blockIdx.x, shares);
-      int n = 0;                               // sequences that begin at tile p or before it, the first aside
-      for (int k = lane + 1; k < a.B; k += 32) n += first[k] <= p;
-      at_b = __reduce_add_sync(0xFFFFFFFFu, n);
-      const Seq s = seqs[at_b];
-      const uint32_t at = p - first[at_b];
-      at_hk = (int)(at / tiles[at_b]);
-      uint32_t rest = at - (uint32_t)at_hk * tiles[at_b];
-      for (int blk0 = 0;; blk0 += 32) {        // its unit, 32 at a time
-        const int f = (blk0 + lane) * a.per;
-        const uint32_t mine_t = f < s.tokens ? (uint32_t)(seen(a, s.base, s.len, min(f + a.per, s.tokens)) + kKeys - 1) / kKeys : 0;
-        uint32_t to = mine_t;
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-          const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, to, o);
-          if (lane >= o) to += v;
-        }
-        const uint32_t over = __ballot_sync(0xFFFFFFFFu, to > rest);
-        if (over) {
-          const int l = __ffs(over) - 1;
-          at_blk = blk0 + l;
-          at_t = (int)(rest - __shfl_sync(0xFFFFFFFFu, to - mine_t, l));
-          at_tiles = (int)__shfl_sync(0xFFFFFFFFu, mine_t, l);
-          break;
-        }
-        rest -= __shfl_sync(0xFFFFFFFFu, to, 31);
-        if ((blk0 + 32) * a.per >= s.tokens) break;   // never: the sequence has the tile
-      }
-      if (lane == 0) {
-        int* info = a.info + blockIdx.x * kInfo;
-        const int f = at_blk * a.per;
-        info[1] = at_t;
-        info[2] = at_tiles;
-        info[3] = at_hk;
-        info[4] = s.row0 + f;
-        info[5] = min(a.per, s.tokens - f);
-        info[6] = (int)total;
-      }
-    }
-    if (lane == 0) {
-      a.info[blockIdx.x * kInfo] = (int)shares;
-      state[kShares] = (int)shares;
-      state[kTotal] = (int)total;
-      state[kZeros] = (int)zeros;
-      state[kAtB] = at_b;
-      state[kAtHk] = at_hk;
-      state[kAtBlk] = at_blk;
-      state[kAtTile] = at_t;
-    }
-  }
-}
 
 // kShared: both slots work on the same key tiles (256 query rows); otherwise
 // they take the even and odd tiles of the same 128 rows.
@@ -443,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = threadIdx.x; b < a.B; b += kThreads) seqs[b] = load_seq(a, b);
     if (a.may_cut) {
       __syncthreads();
-      share_out<kShared>(a, seqs, tiles, reinterpret_cast<uint32_t*>(smem + C::kFirst), state);
+      share_out(a, seqs, tiles, reinterpret_cast<uint32_t*>(smem + C::kFirst), state, kShared ? kCutShared : kCutSplit);
     }
   }
   tc_fence_before();
@@ -671,29 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!pass && !mbar_wait_warp(full_bar(st), phase_of(e), abort, kWaitLimitNs)) return false;
           const int key0 = tile * kKeys;
           if (is_v && key0 + kKeys > x.lim0) {
-            // eight lanes to a row's 128 bytes, four rows at a time
-            uint8_t* v = smem + C::kRing + st * C::kTile + (lane & 7) * 16;
-            const int from = max(x.lim0 - key0, 0), to = x.limit - key0;   // rows that some see; behind them none
-            for (int r0 = from & ~3; r0 < kKeys; r0 += 4) {
-              const int r = r0 + (lane >> 3);
-#pragma unroll
-              for (int at = 0; at < C::kAtoms; ++at) {
-                uint4* p = reinterpret_cast<uint4*>(v + at * kAtom + r * 128);
-                if (r >= to) {
-                  *p = make_uint4(0, 0, 0, 0);
-                } else if (r >= from) {
-                  const uint4 w = *p;
-                  if (not_finite<kF16>(w.x) | not_finite<kF16>(w.y) | not_finite<kF16>(w.z) | not_finite<kF16>(w.w)) {
-                    const auto finite = [](uint32_t u) {
-                      const uint32_t bad = not_finite<kF16>(u);
-                      return u & ~((bad >> 15 & 1u ? 0xFFFFu : 0u) | (bad >> 31 ? 0xFFFF0000u : 0u));
-                    };
-                    *p = make_uint4(finite(w.x), finite(w.y), finite(w.z), finite(w.w));
-                    *dirty = 1;
-                  }
-                }
-              }
-            }
+            if (clear_rows<kF16, C::kAtoms>(smem + C::kRing + st * C::kTile, lane, x.lim0 - key0, x.limit - key0)) *dirty = 1;
             fence_proxy_async_smem();
             __syncwarp();
           }
@@ -950,51 +659,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         return false;
       ++raws;
       ++filled[ring];
-      constexpr int kLanes = DP / 16;            // lanes of a row
-      const uint8_t* src = smem + C::kRaw + rs * C::kRawTile + (warp & 3) * 32 * DP + lane * 16;
-      uint8_t* dst = smem + C::kRing + st * C::kTile;
-      const int c16 = lane % kLanes, key0 = tile * kKeys;
-      const int from = x.lim0 - key0, to = x.limit - key0;
-      const bool edge = is_v && key0 + kKeys > x.lim0;
-#pragma unroll 2
-      for (int k = 0; k < kLanes; ++k) {         // 32 / kLanes rows at a time
-        const int r = (warp & 3) * 32 + k * (32 / kLanes) + lane / kLanes;
-        const uint4 c = *reinterpret_cast<const uint4*>(src + k * 512);
-        uint32_t w[8];
-        const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          w[q] = cvt_e4m3x2_to_f16x2((uint16_t)(cw[q >> 1] >> (16 * (q & 1))));
-          if (!kF16 && !is_v) {
-            float lo, hi;
-            f16x2_to_f32(w[q], lo, hi);
-            w[q] = cvt_bf16x2(lo, hi);
-          }
-        }
-        if (edge && r >= from) {
-          if (r >= to) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) w[q] = 0;
-          } else {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const uint32_t bad = not_finite<true>(w[q]);
-              if (bad) {
-                w[q] &= ~((bad >> 15 & 1u ? 0xFFFFu : 0u) | (bad >> 31 ? 0xFFFF0000u : 0u));
-                *dirty = 1;
-              }
-            }
-          }
-        }
-        // Eight lanes' first stores have eight different places modulo 128 bytes
-        // (a row's two halves begin with the other one of their two).
-        uint8_t* at = dst + (c16 >> 2) * kAtom + r * 128;
-        const int turn = c16 >> 2 & 1, ch = 2 * (c16 & 3);
-        *reinterpret_cast<uint4*>(at + (((ch + turn) ^ (r & 7)) << 4)) =
-            turn ? make_uint4(w[4], w[5], w[6], w[7]) : make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(at + (((ch + 1 - turn) ^ (r & 7)) << 4)) =
-            turn ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(w[4], w[5], w[6], w[7]);
-      }
+      const uint8_t* raw = smem + C::kRaw + rs * C::kRawTile;
+      uint8_t* to = smem + C::kRing + st * C::kTile;
+      const int key0 = tile * kKeys;
+      if (!is_v) convert_rows<DP, kF16>(raw, to, warp & 3, lane, kKeys, kKeys);
+      else if (convert_rows<DP, true>(raw, to, warp & 3, lane, key0 + kKeys > x.lim0 ? x.lim0 - key0 : kKeys, x.limit - key0)) *dirty = 1;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -1259,11 +928,12 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedArgs a, int 
 // ------------------------------------------------------------------ host side
 
 struct Plan {
+  int few;          // rows of a unit where they are few (paged_few.cu), else 0
   bool shared;      // 256 rows a unit, else 128 rows over even and odd tiles
   bool may_cut;
   int DP, G, rows_l, blocks, ctas;
   int64_t items;
-  int unit_rows() const { return shared ? 2 * kRows : kRows; }
+  int unit_rows() const { return few ? few : shared ? 2 * kRows : kRows; }
   int64_t part_rows() const { return may_cut ? 2ll * ctas * unit_rows() : 0; }
 };
 
@@ -1273,16 +943,18 @@ Plan make_plan(const PagedAttnProblem& p, const PagedCache& c, int sms) {
   Plan x;
   x.DP = p.D <= 64 ? 64 : 128;
   x.G = p.Hq / p.Hkv;
-  x.rows_l = kRows / x.G;
+  const int64_t rows = (int64_t)p.max_q * x.G;
+  x.few = rows <= 16 ? 16 : rows <= 32 ? 32 : 0;
+  x.rows_l = (x.few ? x.few : kRows) / x.G;
   const int slots = (p.max_q + x.rows_l - 1) / x.rows_l;
   x.shared = slots > 1;
   x.blocks = x.shared ? (slots + 1) / 2 : 1;
   x.items = (int64_t)c.B * p.Hkv * x.blocks;
-  const int64_t tiles = ((int64_t)c.cols * c.page_size + kKeys - 1) / kKeys, least = x.shared ? 8 : 4;
+  const Cutting cost = x.few ? kCutFew : x.shared ? kCutShared : kCutSplit;
+  const int64_t tiles = ((int64_t)c.cols * c.page_size + kKeys - 1) / kKeys;
   const double total = (double)x.items * (double)tiles;
-  const double cut = x.shared ? least + 10.0 : 1.4 * least + 8.0;
-  x.may_cut = c.B <= kMaxSeqs && (double)tiles > cut && total < (double)(1ll << 31);
-  int64_t ctas = x.may_cut ? ((int64_t)total + least - 1) / least : x.items;
+  x.may_cut = c.B <= kMaxSeqs && (double)tiles > cost.slope * cost.least + cost.plus && total < (double)(1ll << 31);
+  int64_t ctas = x.may_cut ? ((int64_t)total + cost.least - 1) / cost.least : x.items;
   if (x.may_cut && ctas < x.items) ctas = x.items;
   x.ctas = (int)(ctas < sms ? ctas : sms);
   return x;
@@ -1373,6 +1045,9 @@ cudaError_t launch_paged_attention(const PagedAttnProblem& p, const PagedCache& 
   a.k_scale = c.k_scale;
   a.v_scale = c.v_scale;
   const int64_t cell = c.codes ? 1 : 2;
+  a.q = p.q;
+  a.q_l = p.qs[0];
+  a.q_h = p.qs[1];
   a.v = static_cast<const uint8_t*>(c.v);
   for (int i = 0; i < 3; ++i) a.vs[i] = c.vs[i] * cell;
   a.scale_log2 = p.scale * 1.4426950408889634f;
@@ -1403,9 +1078,10 @@ cudaError_t launch_paged_attention(const PagedAttnProblem& p, const PagedCache& 
     const int64_t* t = kv ? c.vs : c.ks;
     const cuuint64_t dims[4] = {D, (cuuint64_t)p.Hkv, (cuuint64_t)c.page_size, (cuuint64_t)c.pages};
     const int64_t s[3] = {t[2], t[1], t[0]};
-    const cuuint32_t box[4] = {c.codes ? (cuuint32_t)x.DP : 64, 1, (cuuint32_t)a.box, 1};
+    const bool operand = !c.codes || (x.few && !kv);   // a copy that the tensor core reads as it is
+    const cuuint32_t box[4] = {!c.codes ? 64 : operand ? 128 : (cuuint32_t)x.DP, 1, (cuuint32_t)a.box, 1};
     ok = ok && encode(kv ? &maps.v : &maps.k, c.codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : type16, kv ? c.v : c.k, 4, dims, s, box,
-                      c.codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                      operand ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                       c.codes ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
   }
   a.tma_out = x.shared && 32 % x.G == 0 && p.D * bytes % 16 == 0 && !odd(a.o_l, p.T, 16) && !odd(a.o_h, p.Hq, 16);
@@ -1420,18 +1096,16 @@ cudaError_t launch_paged_attention(const PagedAttnProblem& p, const PagedCache& 
     *tmap_err = 1;
     return cudaSuccess;
   }
+  if (x.few) return launch_paged_few(maps, a, x.few, x.DP, p.f16, c.codes, x.ctas, st);
   if (x.DP == 64) return p.f16 ? launch_type<64, true>(maps, a, c.codes, x.shared, x.ctas, st) : launch_type<64, false>(maps, a, c.codes, x.shared, x.ctas, st);
   return p.f16 ? launch_type<128, true>(maps, a, c.codes, x.shared, x.ctas, st) : launch_type<128, false>(maps, a, c.codes, x.shared, x.ctas, st);
 }
 
 cudaError_t paged_attention_read_error(cudaStream_t st, uint32_t* err) {
-  uint32_t zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(err, g_paged_err, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, st);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-  if (e == cudaSuccess && *err) {
-    e = cudaMemcpyToSymbolAsync(g_paged_err, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-  }
+  uint32_t few = 0;
+  cudaError_t e = read_paged_error(st, err);
+  if (e == cudaSuccess) e = paged_few_read_error(st, &few);
+  *err |= few;
   return e;
 }
 
