@@ -22,7 +22,7 @@ constexpr int kThreads = 512;
 constexpr int kInfo = 8;           // words about a share for the joining kernel
 
 // Words of kState: how the work is shared out, and where this CTA begins.
-enum { kShares, kTotal, kZeros, kAtB, kAtHk, kAtBlk, kAtTile };
+enum { kShares, kBegin, kEnd, kZeros, kAtB, kAtHk, kAtBlk, kAtTile };
 
 struct PagedArgs {
   int B, T, Hkv, G, D;
@@ -114,9 +114,8 @@ struct Units {
       : a(args), seqs(s), tiles(tl), state(st) {
     cut = a.may_cut && state[kShares] > 0;
     if (cut) {
-      const uint32_t shares = (uint32_t)state[kShares], total = (uint32_t)state[kTotal];
-      begin = cur = blockIdx.x < shares ? share_begin(total, blockIdx.x, shares) : total;
-      end = blockIdx.x < shares ? share_begin(total, blockIdx.x + 1, shares) : total;
+      begin = cur = (uint32_t)state[kBegin];
+      end = (uint32_t)state[kEnd];
       b = state[kAtB], hk = state[kAtHk], blk = state[kAtBlk], t = state[kAtTile];
     } else {
       cur = blockIdx.x;
@@ -236,6 +235,7 @@ __device__ __forceinline__ bool convert_rows(const uint8_t* raw, uint8_t* tile, 
   constexpr int kLanes = DP / 16;            // lanes of a row
   const uint8_t* src = raw + quarter * 32 * DP + lane * 16;
   const int c16 = lane % kLanes;
+  const bool edge = from < quarter * 32 + 32;
   bool bad = false;
 #pragma unroll 4
   for (int k = 0; k < kLanes; ++k) {         // 32 / kLanes rows at a time
@@ -252,7 +252,7 @@ __device__ __forceinline__ bool convert_rows(const uint8_t* raw, uint8_t* tile, 
         w[q] = cvt_bf16x2(lo, hi);
       }
     }
-    if (r >= from) {
+    if (edge && r >= from) {
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         if (r < to && not_finite<kHalf>(w[q])) bad = true;
@@ -364,7 +364,8 @@ __device__ __forceinline__ void share_out(const PagedArgs& a, const Seq* seqs, u
     if (lane == 0) {
       a.info[blockIdx.x * kInfo] = (int)shares;
       state[kShares] = (int)shares;
-      state[kTotal] = (int)total;
+      state[kBegin] = (int)(blockIdx.x < shares ? share_begin(total, blockIdx.x, shares) : total);
+      state[kEnd] = (int)(blockIdx.x < shares ? share_begin(total, blockIdx.x + 1, shares) : total);
       state[kZeros] = (int)zeros;
       state[kAtB] = at_b;
       state[kAtHk] = at_hk;

@@ -46,13 +46,13 @@ struct Few {
   // Stages of a group's ring: of K and V in turn (16 bits), or of V and of K's codes.
   static constexpr int kR = kCodes ? (DP == 128 ? 1 : 2) : (DP == 128 ? 3 : 5);
   static constexpr int kRK = kCodes ? 2 : 0;
-  static constexpr int kRaws = !kCodes ? 0 : DP == 128 ? 3 : 6;
+  static constexpr int kRaws = !kCodes ? 0 : DP == 64 ? 3 : N == 16 ? 2 : 1;   // and of V's codes, of a group
   static constexpr int kRing = 0;
   static constexpr int kKRing = kRing + 2 * kR * kTile;  // rows of 128 bytes
   static constexpr int kRaw = kKRing + 2 * kRK * kAtom;
   static constexpr int kQRows = kCodes ? 3 * N : N;
   static constexpr int kQAtom = kQRows * 128;
-  static constexpr int kQ = kRaw + kRaws * kRawTile;
+  static constexpr int kQ = kRaw + 2 * kRaws * kRawTile;
   static constexpr int kP = kQ + (kCodes ? 1 : kAtoms) * kQAtom;     // of each group 2 x N x 128 bytes
   static constexpr int kStat = kP + 2 * 2 * N * 128;     // m[2][N], l[2][4][N], tops[2][4][N], factor[2][N], running m[2][N], f[2][N]
   static constexpr int kSeq = kStat + (2 + 8 + 8 + 2 + 2 + 2) * N * 4;
@@ -60,9 +60,9 @@ struct Few {
   static constexpr int kFirst = kTiles + kMaxSeqs * 4;
   static constexpr int kState = kFirst + (kMaxSeqs + 4) * 4;
   static constexpr int kBar = kState + 16 * 4;
-  // full[2R], empty[2R], clean[2R], k_full[2RK], k_empty[2RK], raw_full[RW], raw_empty[RW], q_full, q_empty,
+  // full[2R], empty[2R], clean[2R], k_full[2RK], k_empty[2RK], raw_full[2RW], raw_empty[2RW], q_full, q_empty,
   // s_full[2], p_full[2], o_full[2], l_full[2], o_free[2], drain[2]
-  static constexpr int kNumBars = 6 * kR + 4 * kRK + 2 * kRaws + 14;
+  static constexpr int kNumBars = 6 * kR + 4 * kRK + 4 * kRaws + 14;
   static constexpr int kTmemSlot = kBar + kNumBars * 8;
   static constexpr int kAbort = kTmemSlot + 4;
   static constexpr int kDirty = kAbort + 4;
@@ -73,11 +73,22 @@ struct Few {
   static_assert(kRing + 2 * kR * kTile + kAtom <= kAlloc - 1024, "128 rows of the last stage");
 };
 
-// Warps: 0-7 softmax, 8-11 epilogue and conversion, 12 and 15 MMA issue, 13 and 16 copies of K and V,
-// 14 clearing or the queries' terms.
-constexpr int kFewThreads = 17 * 32;
+// Warps: 0-7 softmax, 8-11 epilogue and conversion of the first group's V, 12 and 15 MMA
+// issue, 13 and 16 copies of K and V, 14 clearing, or the queries' terms and with 17-19 the
+// conversion of the second group's V.
+template <bool kCodes>
+constexpr int kFewThreads = (kCodes ? 20 : 17) * 32;
 
 constexpr uint32_t kFewTmem = 256;   // columns: S^T of the groups from 0 and 96, O^T from 192 and 224
+
+// mbar_wait that asks some times before it lets the thread sleep: a sleeping
+// thread is woken late, and every hand-over between roles is on a tile's way.
+__device__ __forceinline__ bool mbar_wait_awake(uint32_t bar, uint32_t parity, volatile int* abort) {
+#pragma unroll 1
+  for (int k = 0; k < 256; ++k)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, abort, kWaitLimitNs);
+}
 
 // Whether any of the 128 threads of a group says so (named barrier `id`).
 __device__ __forceinline__ bool group_any(int id, bool mine) {
@@ -103,8 +114,80 @@ __device__ __forceinline__ float warp_max(float v) {
   return __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF));
 }
 
+// The sequences to shared memory and, where units may be cut, how the work is
+// shared out (see share_out): by one warp, since a sequence is one unit of a key head.
+__device__ __forceinline__ void share_out_few(const PagedArgs& a, Seq* seqs, uint32_t* tiles, uint32_t* first, int* state) {
+  const int lane = threadIdx.x & 31;
+  uint32_t total = 0, units = 0, longest = 0, zeros = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int b = b0 + lane;
+    uint32_t mine = 0;
+    if (b < a.B) {
+      const Seq s = load_seq(a, b);
+      seqs[b] = s;
+      if (s.tokens > 0) {
+        mine = (uint32_t)(seen(a, s.base, s.len, s.tokens) + kKeys - 1) / kKeys;
+        ++units;
+        zeros |= mine == 0;
+      }
+      tiles[b] = mine;
+    }
+    if (!a.may_cut) continue;
+    longest = max(longest, mine);
+    mine *= (uint32_t)a.Hkv;
+    uint32_t to = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, to, o);
+      if (lane >= o) to += v;
+    }
+    if (b < a.B) first[b] = total + to - mine;
+    total += __shfl_sync(0xFFFFFFFFu, to, 31);
+  }
+  if (!a.may_cut) return;
+  __syncwarp();
+  units = __reduce_add_sync(0xFFFFFFFFu, units) * (uint32_t)a.Hkv;
+  longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+  zeros = __reduce_or_sync(0xFFFFFFFFu, zeros);
+  const uint32_t ctas = gridDim.x;
+  const uint32_t share = max((total + ctas - 1) / ctas, (uint32_t)kCutFew.least);
+  const float even = (float)total / (float)ctas;
+  const float whole = units <= ctas ? (float)longest : fmaxf((float)longest, even + 0.5f * (float)longest);
+  const bool cut = kCutFew.slope * (float)share + kCutFew.plus < whole;
+  const uint32_t shares = cut ? (total + share - 1) / share : 0;
+  if (lane == 0) {
+    a.info[blockIdx.x * kInfo] = (int)shares;
+    state[kShares] = (int)shares;
+    state[kZeros] = (int)zeros;
+  }
+  if (blockIdx.x >= shares) {
+    if (lane == 0) state[kBegin] = state[kEnd] = (int)total;
+    return;
+  }
+  const uint32_t p = share_begin(total, blockIdx.x, shares);
+  int n = 0;                                 // sequences that begin at tile p or before it, the first aside
+  for (int k = lane + 1; k < a.B; k += 32) n += first[k] <= p;
+  const int b = __reduce_add_sync(0xFFFFFFFFu, n);
+  if (lane != 0) return;
+  const Seq s = seqs[b];
+  const uint32_t at = p - first[b], hk = at / tiles[b], t = at - hk * tiles[b];
+  state[kBegin] = (int)p;
+  state[kEnd] = (int)share_begin(total, blockIdx.x + 1, shares);
+  state[kAtB] = b;
+  state[kAtHk] = (int)hk;
+  state[kAtBlk] = 0;
+  state[kAtTile] = (int)t;
+  int* info = a.info + blockIdx.x * kInfo;
+  info[1] = (int)t;
+  info[2] = (int)tiles[b];
+  info[3] = (int)hk;
+  info[4] = s.row0;
+  info[5] = s.tokens;
+  info[6] = (int)total;
+}
+
 template <int DP, bool kF16, bool kCodes, int N>
-__global__ void __launch_bounds__(kFewThreads, 1)
+__global__ void __launch_bounds__(kFewThreads<kCodes>, 1)
     paged_few_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant__ PagedArgs a) {
   using C = Few<DP, kCodes, N>;
   constexpr int R = C::kR, RK = C::kRK, RW = C::kRaws;
@@ -123,8 +206,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   auto k_full = [&](int s) { return bar(6 * R + s); };
   auto k_empty = [&](int s) { return bar(6 * R + 2 * RK + s); };
   auto raw_full = [&](int r) { return bar(6 * R + 4 * RK + r); };
-  auto raw_empty = [&](int r) { return bar(6 * R + 4 * RK + RW + r); };
-  constexpr int kRest = 6 * R + 4 * RK + 2 * RW;
+  auto raw_empty = [&](int r) { return bar(6 * R + 4 * RK + 2 * RW + r); };
+  constexpr int kRest = 6 * R + 4 * RK + 4 * RW;
   const uint32_t q_full = bar(kRest), q_empty = bar(kRest + 1);
   auto s_full = [&](int i) { return bar(kRest + 2 + i); };
   auto p_full = [&](int i) { return bar(kRest + 4 + i); };
@@ -158,7 +241,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       mbar_init(k_full(s), 1);
       mbar_init(k_empty(s), 1);
     }
-    for (int r = 0; r < RW; ++r) {
+    for (int r = 0; r < 2 * RW; ++r) {
       mbar_init(raw_full(r), 1);
       mbar_init(raw_empty(r), 4);
     }
@@ -186,20 +269,14 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   // Rows without a query hold zeros (of codes their writer clears them): no copy writes them.
   const uint32_t q_bytes = (uint32_t)(a.G * a.rows_l * 128);
   if (!kCodes && q_bytes < (uint32_t)C::kQAtom) {
-    for (uint32_t at = q_bytes + 16 * threadIdx.x; at < (uint32_t)C::kQAtom; at += 16 * kFewThreads)
+    for (uint32_t at = q_bytes + 16 * threadIdx.x; at < (uint32_t)C::kQAtom; at += 16 * kFewThreads<kCodes>)
 #pragma unroll
       for (int k = 0; k < C::kAtoms; ++k)
         *reinterpret_cast<uint4*>(smem + C::kQ + k * C::kQAtom + at) = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
   }
   griddep_wait();   // from here on what earlier kernels wrote may be read
-  if (seqs) {
-    for (int b = threadIdx.x; b < a.B; b += kFewThreads) seqs[b] = load_seq(a, b);
-    if (a.may_cut) {
-      __syncthreads();
-      share_out(a, seqs, tiles, reinterpret_cast<uint32_t*>(smem + C::kFirst), state, kCutFew);
-    }
-  }
+  if (warp == 0 && seqs) share_out_few(a, seqs, tiles, reinterpret_cast<uint32_t*>(smem + C::kFirst), state);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -220,6 +297,27 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     return page;
   };
 
+  // A quarter of a tile of V's codes of group i from its raw ring to the operands' ring, as
+  // binary16 in the 128-byte swizzle; `count` is of the group's tiles.
+  auto convert = [&](const Item& x, int i, int tile, int quarter, uint32_t count) {
+    constexpr int kW = RW ? RW : 1;
+    const int rs = i * kW + (int)(count % kW), st = i * R + (int)(count % R);
+    if (!mbar_wait_lanes(raw_full(rs), (count / kW) & 1, abort) ||
+        !mbar_wait_lanes(empty_bar(st), ((count / R) & 1) ^ 1, abort))
+      return false;
+    const int key0 = tile * kKeys;
+    if (convert_rows<DP, true>(smem + C::kRaw + rs * C::kRawTile, smem + C::kRing + st * C::kTile, quarter, lane,
+                               key0 + kKeys > x.lim0 ? x.lim0 - key0 : kKeys, x.limit - key0))
+      *dirty = 1;
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(clean_bar(st));
+      mbar_arrive(raw_empty(rs));
+    }
+    return true;
+  };
+
   if (warp == 13 || warp == 16) {
     // ---------------------------------------------------------------- copies of K (and Q), and of V
     const bool is_v = warp == 16;
@@ -229,7 +327,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     constexpr int kStages = kCodes ? 0 : R;
     const int S = kCodes ? (is_v ? RW : RK) : kStages, step = kCodes ? 1 : 2;
     uint32_t entry[2] = {!kCodes && is_v ? 1u : 0u, !kCodes && is_v ? 1u : 0u}, qcount = 0;
-    const auto stage_of = [&](int i, uint32_t e) { return (kCodes && is_v ? 0 : i * S) + (int)(e % (uint32_t)S); };
+    const auto stage_of = [&](int i, uint32_t e) { return i * S + (int)(e % (uint32_t)S); };
     const auto full_of = [&](int st) { return kCodes ? (is_v ? raw_full(st) : k_full(st)) : full_bar(st); };
     const auto empty_of = [&](int st) { return kCodes ? (is_v ? raw_empty(st) : k_empty(st)) : empty_bar(st); };
     const uint32_t stage_bytes = kCodes ? (is_v ? C::kRawTile : kAtom) : C::kTile, row_bytes = kCodes && is_v ? DP : 128;
@@ -241,7 +339,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       if (x.n() == 0) continue;
       int page = ask_page(x, x.t0);
       if (!kCodes && !is_v) {
-        ok = mbar_wait_warp(q_empty, (qcount & 1) ^ 1, abort, kWaitLimitNs);
+        ok = mbar_wait_lanes(q_empty, (qcount & 1) ^ 1, abort);
         if (!ok) break;
         ++qcount;
         if (lane == 0) {
@@ -254,13 +352,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll 1
       for (int t = x.t0; t < x.t1; ++t) {
         const int next = ask_page(x, t + 1);     // a tile ahead
-        // the raw ring is one for both groups: all entries are counted in the first's place
-        const int i = (t - x.t0) & 1, c = kCodes && is_v ? 0 : i;
-        const uint32_t e = c ? entry[1] : entry[0];
+        const int i = (t - x.t0) & 1;
+        const uint32_t e = i ? entry[1] : entry[0];
         const int st = stage_of(i, e);
-        ok = mbar_wait_warp(empty_of(st), ((e / (uint32_t)S) & 1) ^ 1, abort, kWaitLimitNs);
+        ok = mbar_wait_lanes(empty_of(st), ((e / (uint32_t)S) & 1) ^ 1, abort);
         if (!ok) break;
-        if (c) entry[1] += step;
+        if (i) entry[1] += step;
         else entry[0] += step;
         if (lane == 0) mbar_arrive_expect_tx(full_of(st), stage_bytes);
         __syncwarp();
@@ -289,7 +386,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         const int n = x.n();
         if (n == 0) continue;
         // also by a group without a tile: its word on Q below belongs to this Q
-        ok = mbar_wait(q_full, qcount & 1, abort, kWaitLimitNs);
+        ok = mbar_wait_awake(q_full, qcount & 1, abort);
         if (!ok) break;
         tc_fence_after();
         const uint64_t qd = sw128_kmajor_desc(sbase + C::kQ);
@@ -297,7 +394,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           const bool first = j == i, last = j + 2 >= n;
           if constexpr (kCodes) {
             const int st = i * RK + (int)(k_entry % RK);
-            ok = mbar_wait(k_full(st), (k_entry / RK) & 1, abort, kWaitLimitNs);
+            ok = mbar_wait_awake(k_full(st), (k_entry / RK) & 1, abort);
             if (!ok) break;
             ++k_entry;
             tc_fence_after();
@@ -308,7 +405,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             mma_commit(k_empty(st));
           } else {
             const int st = i * R + (int)(entry % R);
-            ok = mbar_wait(clean_bar(st), (entry / R) & 1, abort, kWaitLimitNs);
+            ok = mbar_wait_awake(clean_bar(st), (entry / R) & 1, abort);
             if (!ok) break;
             ++entry;
             tc_fence_after();
@@ -323,11 +420,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           if (last) mma_commit(q_empty);
 
           const int st = i * R + (int)(entry % R);
-          ok = mbar_wait(clean_bar(st), (entry / R) & 1, abort, kWaitLimitNs);
+          ok = mbar_wait_awake(clean_bar(st), (entry / R) & 1, abort);
           if (!ok) break;
           ++entry;
-          if (first) ok = mbar_wait(o_free(i), (icount++ & 1) ^ 1, abort, kWaitLimitNs);   // the epilogue has read O_i
-          ok = ok && mbar_wait(p_full(i), pcount & 1, abort, kWaitLimitNs);
+          if (first) ok = mbar_wait_awake(o_free(i), (icount++ & 1) ^ 1, abort);   // the epilogue has read O_i
+          ok = ok && mbar_wait_awake(p_full(i), pcount & 1, abort);
           if (!ok) break;
           ++pcount;
           tc_fence_after();
@@ -348,18 +445,19 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       volatile int never = 0;
       if (!mbar_wait(drain_bar(i), 0, &never, kWaitLimitNs)) atomicOr(&g_paged_err, kErrTimeout);
     }
-  } else if (warp == 14) {
+  } else if (warp == 14 || warp > 16) {
     bool ok = true;
     Units units(a, seqs, tiles, state);
     Item x;
     if constexpr (kCodes) {
       // ---------------------------------------------------------------- queries as E4M3 terms
       // Row r's terms are rows r, N + r and 2 N + r of the operand, four dimensions a lane.
-      uint32_t qcount = 0;
+      uint32_t qcount = 0, tiles_done = 0;
       const float scale = a.scale_log2 * ld_f32(a.k_scale);
       while (ok && units.next(x)) {
         if (x.n() == 0) continue;
-        ok = mbar_wait_warp(q_empty, (qcount & 1) ^ 1, abort, kWaitLimitNs);
+        if (warp == 14) {
+        ok = mbar_wait_lanes(q_empty, (qcount & 1) ^ 1, abort);
         if (!ok) break;
         const uint16_t* q = static_cast<const uint16_t*>(a.q) + (int64_t)x.row0 * a.q_l + (int64_t)x.hk * a.G * a.q_h + 4 * lane;
         const int valid = x.left * a.G;
@@ -405,6 +503,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
+        }
+#pragma unroll 1
+        for (int t = x.t0 + 1; ok && t < x.t1; t += 2) ok = convert(x, 1, t, warp == 14 ? 0 : warp - 16, tiles_done++);
       }
     } else {
       // ---------------------------------------------------------------- V rows that not all rows see
@@ -415,7 +516,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           const int i = (k >> 1) & 1;
           const uint32_t e = i ? entry[1]++ : entry[0]++;
           const int st = i * R + (int)(e % R), key0 = (x.t0 + (k >> 1)) * kKeys;
-          ok = mbar_wait_warp(full_bar(st), (e / R) & 1, abort, kWaitLimitNs);
+          ok = mbar_wait_lanes(full_bar(st), (e / R) & 1, abort);
           if (!ok) break;
           if ((k & 1) && key0 + kKeys > x.lim0) {
             if (clear_rows<kF16, C::kAtoms>(smem + C::kRing + st * C::kTile, lane, x.lim0 - key0, x.limit - key0)) *dirty = 1;
@@ -573,7 +674,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         if (lane == r) mine = t;
       }
       // the epilogue has read the previous item's sums
-      ok = ok && mbar_wait_warp(o_free(i), (icount & 1) ^ 1, abort, kWaitLimitNs);
+      ok = ok && mbar_wait_lanes(o_free(i), (icount & 1) ^ 1, abort);
       ++icount;
       if (!ok) continue;
       if (lane < N) {
@@ -591,7 +692,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     float inv_s = 1.0f, v_scale = 1.0f;
     if (a.s_out) inv_s = __frcp_rn(ld_f32(a.s_out));
     if constexpr (kCodes) v_scale = ld_f32(a.v_scale);
-    uint32_t icount[2] = {0, 0}, raws = 0, filled[2] = {0, 0};
+    uint32_t icount[2] = {0, 0}, tiles_done = 0;
     bool ok = true;
 
     auto put = [&](int64_t at, float y) {
@@ -620,31 +721,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       }
       return rows;
     };
-    // A quarter of a tile of V's codes from the raw ring to the operands' ring, as
-    // binary16 in the 128-byte swizzle: this warp's 32 rows, 16 codes of a lane at a time.
-    auto convert = [&](const Item& x, int i, int tile) {
-      constexpr int kW = RW ? RW : 1;
-      const int rs = (int)(raws % kW);
-      const uint32_t e = filled[i];
-      const int st = i * R + (int)(e % R);
-      if (!mbar_wait_warp(raw_full(rs), (raws / kW) & 1, abort, kWaitLimitNs) ||
-          !mbar_wait_warp(empty_bar(st), ((e / R) & 1) ^ 1, abort, kWaitLimitNs))
-        return false;
-      ++raws;
-      ++filled[i];
-      const int key0 = tile * kKeys;
-      if (convert_rows<DP, true>(smem + C::kRaw + rs * C::kRawTile, smem + C::kRing + st * C::kTile, warp & 3, lane,
-                                 key0 + kKeys > x.lim0 ? x.lim0 - key0 : kKeys, x.limit - key0))
-        *dirty = 1;
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(clean_bar(st));
-        mbar_arrive(raw_empty(rs));
-      }
-      return true;
-    };
-
     if (a.may_cut && state[kShares] > 0 && state[kZeros]) {   // units without a tile: their rows are zeros
       for (int it = blockIdx.x; it < a.B * a.Hkv; it += gridDim.x) {
         Item x;
@@ -666,13 +742,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       }
       if constexpr (kCodes) {
 #pragma unroll 1
-        for (int t = x.t0; ok && t < x.t1; ++t) ok = convert(x, (t - x.t0) & 1, t);
+        for (int t = x.t0; ok && t < x.t1; t += 2) ok = convert(x, 0, t, warp & 3, tiles_done++);
         if (!ok) break;
       }
       const bool two = x.n() > 1;
       for (int i = 0; i < (two ? 2 : 1) && ok; ++i) {
-        if (!mbar_wait_warp(l_full(i), icount[i] & 1, abort, kWaitLimitNs) ||
-            !mbar_wait_warp(o_full(i), icount[i] & 1, abort, kWaitLimitNs))
+        if (!mbar_wait_lanes(l_full(i), icount[i] & 1, abort) ||
+            !mbar_wait_lanes(o_full(i), icount[i] & 1, abort))
           ok = false;
         ++icount[i];
       }
@@ -819,7 +895,7 @@ cudaError_t launch_kernel(const PagedMaps& maps, const PagedArgs& a, int grid, c
   }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(kFewThreads, 1, 1);
+  cfg.blockDim = dim3(kFewThreads<kCodes>, 1, 1);
   cfg.dynamicSmemBytes = C::kAlloc;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
