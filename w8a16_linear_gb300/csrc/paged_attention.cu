@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!pass && !mbar_wait_warp(full_bar(st), phase_of(e), abort, kWaitLimitNs)) return false;
           const int key0 = tile * kKeys;
           if (is_v && key0 + kKeys > x.lim0) {
-            if (clear_rows<kF16, C::kAtoms>(smem + C::kRing + st * C::kTile, lane, x.lim0 - key0, x.limit - key0)) *dirty = 1;
+            if (clear_rows<kF16, false, C::kAtoms>(smem + C::kRing + st * C::kTile, lane, x.lim0 - key0, x.limit - key0)) *dirty = 1;
             fence_proxy_async_smem();
             __syncwarp();
           }
@@ -1078,7 +1078,7 @@ cudaError_t launch_paged_attention(const PagedAttnProblem& p, const PagedCache& 
     const int64_t* t = kv ? c.vs : c.ks;
     const cuuint64_t dims[4] = {D, (cuuint64_t)p.Hkv, (cuuint64_t)c.page_size, (cuuint64_t)c.pages};
     const int64_t s[3] = {t[2], t[1], t[0]};
-    const bool operand = !c.codes || (x.few && !kv);   // a copy that the tensor core reads as it is
+    const bool operand = !c.codes || x.few;   // the tensor core reads the copy as it is
     const cuuint32_t box[4] = {!c.codes ? 64 : operand ? 128 : (cuuint32_t)x.DP, 1, (cuuint32_t)a.box, 1};
     ok = ok && encode(kv ? &maps.v : &maps.k, c.codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : type16, kv ? c.v : c.k, 4, dims, s, box,
                       operand ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,

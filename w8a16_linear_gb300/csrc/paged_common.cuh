@@ -200,14 +200,20 @@ __device__ __forceinline__ uint32_t finite(uint32_t w) {
   return w & ~((bad >> 15 & 1u ? 0xFFFFu : 0u) | (bad >> 31 ? 0xFFFF0000u : 0u));
 }
 
-// V rows of a 16-bit tile in shared memory that not every row of a unit sees (one
-// warp; eight lanes to a row's 128 bytes, four rows at a time): rows `to` and on, which none
+// The same for four E4M3 codes: those of NaN.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
+// V rows of a tile in shared memory that not every row of a unit sees (one warp;
+// eight lanes to a row's 128 bytes, four rows at a time): rows `to` and on, which none
 // sees, are cleared; of rows from .. to - 1 the values that are not finite.  Whether this
 // lane met one of those.
-template <bool kF16, int kAtoms>
+template <bool kF16, bool kCells8, int kAtoms>
 __device__ __forceinline__ bool clear_rows(uint8_t* tile, int lane, int from, int to) {
+  const auto bad_of = [](uint32_t w) { return kCells8 ? nan_codes(w) : not_finite<kF16>(w); };
+  const auto kept = [](uint32_t w) { return kCells8 ? w & ~((nan_codes(w) >> 7) * 0xFFu) : finite<kF16>(w); };
   bool bad = false;
   uint8_t* v = tile + (lane & 7) * 16;
+#pragma unroll 1
   for (int r0 = max(from, 0) & ~3; r0 < kKeys; r0 += 4) {
     const int r = r0 + (lane >> 3);
 #pragma unroll
@@ -217,8 +223,8 @@ __device__ __forceinline__ bool clear_rows(uint8_t* tile, int lane, int from, in
         *p = make_uint4(0, 0, 0, 0);
       } else if (r >= from) {
         const uint4 w = *p;
-        if (not_finite<kF16>(w.x) | not_finite<kF16>(w.y) | not_finite<kF16>(w.z) | not_finite<kF16>(w.w)) {
-          *p = make_uint4(finite<kF16>(w.x), finite<kF16>(w.y), finite<kF16>(w.z), finite<kF16>(w.w));
+        if (bad_of(w.x) | bad_of(w.y) | bad_of(w.z) | bad_of(w.w)) {
+          *p = make_uint4(kept(w.x), kept(w.y), kept(w.z), kept(w.w));
           bad = true;
         }
       }

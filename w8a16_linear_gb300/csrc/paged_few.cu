@@ -14,12 +14,13 @@
 // The CTA's two groups of four softmax warps take the even and the odd tiles,
 // with accumulators of their own, which the epilogue joins.
 //
-// E4M3 cells.  K goes to the tensor core as it is: the queries are split into
-// three E4M3 terms, q = (t0 + t1 / 16 + t2 / 256) 2^e with 2^e from the row's
-// largest value, which leaves less than 2^-12 of each value (nothing of a bf16
-// one) or 2^-27 of the largest; the terms are 3 N rows, and the softmax threads add
-// their scores.  V has to be beside 16-bit weights: four warps write its codes
-// to the operands' ring as binary16 (exact), and P is binary16 too.
+// E4M3 cells go to the tensor core as they are.  What stands beside them is split
+// into three E4M3 terms, x = (t0 + t1 / 16 + t2 / 256) 2^e, which leaves less than 2^-12 of
+// each value or 2^-18 in units of the terms: the queries, with 2^e from the row's largest
+// value (2^-27 of which is left of the smallest ones; nothing of a bf16 value), and P, whose largest
+// is kept between 2^6 and 2^8 (so that 2^-24 of it is left).  Terms are rows of their own,
+// 3 N, and the softmax and epilogue threads add the three results.  A group's scores of a tile
+// are started before the products of the one before: two sets of S^T and P.
 //
 // Bound by the bytes of K and V.  Roundings below 32 bits: P (its sum l is taken
 // before) and the output.
@@ -40,46 +41,45 @@ namespace {
 
 template <int DP, bool kCodes, int N>
 struct Few {
-  static constexpr int kAtoms = DP / 64;
-  static constexpr int kTile = kAtoms * kAtom;           // bytes of 128 rows of K or V in 16 bits
-  static constexpr int kRawTile = kKeys * DP;            // of V's codes
-  // Stages of a group's ring: of K and V in turn (16 bits), or of V and of K's codes.
-  static constexpr int kR = kCodes ? (DP == 128 ? 1 : 2) : (DP == 128 ? 3 : 5);
-  static constexpr int kRK = kCodes ? 2 : 0;
-  static constexpr int kRaws = !kCodes ? 0 : DP == 64 ? 3 : N == 16 ? 2 : 1;   // and of V's codes, of a group
-  static constexpr int kRing = 0;
-  static constexpr int kKRing = kRing + 2 * kR * kTile;  // rows of 128 bytes
-  static constexpr int kRaw = kKRing + 2 * kRK * kAtom;
-  static constexpr int kQRows = kCodes ? 3 * N : N;
-  static constexpr int kQAtom = kQRows * 128;
-  static constexpr int kQ = kRaw + 2 * kRaws * kRawTile;
-  static constexpr int kP = kQ + (kCodes ? 1 : kAtoms) * kQAtom;     // of each group 2 x N x 128 bytes
-  static constexpr int kStat = kP + 2 * 2 * N * 128;     // m[2][N], l[2][4][N], tops[2][4][N], factor[2][N], running m[2][N], f[2][N]
+  static constexpr int kAtoms = kCodes ? 1 : DP / 64;    // 128-byte spans of a row of K and V
+  static constexpr int kTile = kAtoms * kAtom;           // bytes of 128 rows of them
+  // Stages of a group's ring: of K and V in turn, or of E4M3 cells of each (of 16 bits
+  // there is no room for two whole rings).
+  static constexpr int kR = kCodes ? 0 : DP == 128 ? 3 : 5;
+  static constexpr int kRK = kCodes ? (N == 16 ? 3 : 2) : 0, kRV = kCodes ? 2 : 0;
+  static constexpr int kStages = kCodes ? kRK + kRV : kR;
+  static constexpr int kCols = kCodes ? 3 * N : N;       // rows of Q and P, columns of S^T and O^T
+  static constexpr int kAhead = kCodes && N == 16 ? 2 : 1;   // sets of S^T and P of a group
+  static constexpr int kRing = 0;                        // codes: K's stages, then V's, of each group
+  static constexpr int kQAtom = kCols * 128;
+  static constexpr int kQ = kRing + 2 * kStages * kTile;
+  static constexpr int kPAtom = kCols * 128;             // 128 bytes a row: 64 keys in 16 bits, 128 codes
+  static constexpr int kPSet = (kCodes ? 1 : 2) * kPAtom;
+  static constexpr int kP = kQ + kAtoms * kQAtom;
+  static constexpr int kStat = kP + 2 * kAhead * kPSet;  // m[2][N], l[2][4][N], tops[2][4][N], factor[2][N], running m[2][N], f[2][N]
   static constexpr int kSeq = kStat + (2 + 8 + 8 + 2 + 2 + 2) * N * 4;
   static constexpr int kTiles = kSeq + kMaxSeqs * 16;
   static constexpr int kFirst = kTiles + kMaxSeqs * 4;
   static constexpr int kState = kFirst + (kMaxSeqs + 4) * 4;
   static constexpr int kBar = kState + 16 * 4;
-  // full[2R], empty[2R], clean[2R], k_full[2RK], k_empty[2RK], raw_full[2RW], raw_empty[2RW], q_full, q_empty,
-  // s_full[2], p_full[2], o_full[2], l_full[2], o_free[2], drain[2]
-  static constexpr int kNumBars = 6 * kR + 4 * kRK + 4 * kRaws + 14;
+  // full[2 S], empty[2 S], clean[2 S], q_full, q_empty, s_full[2][A], p_full[2][A], done[2][A],
+  // o_full[2], l_full[2], o_free[2], drain[2]
+  static constexpr int kNumBars = 6 * kStages + 2 + 6 * kAhead + 8;
   static constexpr int kTmemSlot = kBar + kNumBars * 8;
   static constexpr int kAbort = kTmemSlot + 4;
   static constexpr int kDirty = kAbort + 4;
   static constexpr int kAlloc = kDirty + 4 + 1024;       // slack for 1024-byte alignment
+  static constexpr int kTmemCols = kCodes ? 512 : 128;   // of each group: S^T of the sets, O^T
   static_assert(kAlloc <= 232448, "shared memory budget");
+  static_assert(2 * (kAhead + 1) * kCols <= kTmemCols, "TMEM");
   // Heads of 64 dimensions: the MMA's other 64 rows of V^T are what stands behind
   // the tile; their lanes are never read, but the ring must not end the memory.
-  static_assert(kRing + 2 * kR * kTile + kAtom <= kAlloc - 1024, "128 rows of the last stage");
+  static_assert(kRing + 2 * kStages * kTile + kAtom <= kAlloc - 1024, "128 rows of the last stage");
 };
 
-// Warps: 0-7 softmax, 8-11 epilogue and conversion of the first group's V, 12 and 15 MMA
-// issue, 13 and 16 copies of K and V, 14 clearing, or the queries' terms and with 17-19 the
-// conversion of the second group's V.
-template <bool kCodes>
-constexpr int kFewThreads = (kCodes ? 20 : 17) * 32;
-
-constexpr uint32_t kFewTmem = 256;   // columns: S^T of the groups from 0 and 96, O^T from 192 and 224
+// Warps: 0-7 softmax, 8-11 epilogue, 12 and 15 MMA issue, 13 and 16 copies of K and V,
+// 14 clearing, 17 the queries' terms.
+constexpr int kFewThreads = 18 * 32;
 
 // mbar_wait that asks some times before it lets the thread sleep: a sleeping
 // thread is woken late, and every hand-over between roles is on a tile's way.
@@ -187,13 +187,13 @@ __device__ __forceinline__ void share_out_few(const PagedArgs& a, Seq* seqs, uin
 }
 
 template <int DP, bool kF16, bool kCodes, int N>
-__global__ void __launch_bounds__(kFewThreads<kCodes>, 1)
+__global__ void __launch_bounds__(kFewThreads, 1)
     paged_few_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant__ PagedArgs a) {
   using C = Few<DP, kCodes, N>;
-  constexpr int R = C::kR, RK = C::kRK, RW = C::kRaws;
-  constexpr bool kP16 = kF16 || kCodes;            // P and V are binary16
-  constexpr uint32_t kIdescS = kCodes ? make_idesc(0, 0, kKeys, 3 * N) : make_idesc(kF16 ? 0 : 1, kF16 ? 0 : 1, kKeys, N);
-  constexpr uint32_t kIdescO = make_idesc(kP16 ? 0 : 1, kP16 ? 0 : 1, 128, N) | (1u << 15);   // A is MN-major
+  constexpr int R = C::kR, RK = C::kRK, RV = C::kRV, S = C::kStages, A = C::kAhead;
+  constexpr uint32_t kFmt = kCodes || kF16 ? 0 : 1;  // E4M3 of its kind, binary16 of the other
+  constexpr uint32_t kIdescS = make_idesc(kFmt, kFmt, kKeys, C::kCols);
+  constexpr uint32_t kIdescO = make_idesc(kFmt, kFmt, 128, C::kCols) | (1u << 15);   // A is MN-major
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -201,20 +201,19 @@ __global__ void __launch_bounds__(kFewThreads<kCodes>, 1)
   const uint32_t bar0 = sbase + C::kBar;
   auto bar = [&](int k) { return bar0 + 8u * (uint32_t)k; };
   auto full_bar = [&](int s) { return bar(s); };
-  auto empty_bar = [&](int s) { return bar(2 * R + s); };
-  auto clean_bar = [&](int s) { return bar(4 * R + s); };
-  auto k_full = [&](int s) { return bar(6 * R + s); };
-  auto k_empty = [&](int s) { return bar(6 * R + 2 * RK + s); };
-  auto raw_full = [&](int r) { return bar(6 * R + 4 * RK + r); };
-  auto raw_empty = [&](int r) { return bar(6 * R + 4 * RK + 2 * RW + r); };
-  constexpr int kRest = 6 * R + 4 * RK + 4 * RW;
-  const uint32_t q_full = bar(kRest), q_empty = bar(kRest + 1);
-  auto s_full = [&](int i) { return bar(kRest + 2 + i); };
-  auto p_full = [&](int i) { return bar(kRest + 4 + i); };
-  auto o_full = [&](int i) { return bar(kRest + 6 + i); };
-  auto l_full = [&](int i) { return bar(kRest + 8 + i); };
-  auto o_free = [&](int i) { return bar(kRest + 10 + i); };
-  auto drain_bar = [&](int i) { return bar(kRest + 12 + i); };
+  auto empty_bar = [&](int s) { return bar(2 * S + s); };
+  auto clean_bar = [&](int s) { return bar(4 * S + s); };
+  constexpr int kRest = 6 * S + 2;
+  const uint32_t q_full = bar(6 * S), q_empty = bar(6 * S + 1);
+  // of the group's tile t, by its set
+  auto s_full = [&](int i, uint32_t t) { return bar(kRest + i * A + (int)(t % A)); };
+  auto p_full = [&](int i, uint32_t t) { return bar(kRest + 2 * A + i * A + (int)(t % A)); };
+  auto done_bar = [&](int i, uint32_t t) { return bar(kRest + 4 * A + i * A + (int)(t % A)); };
+  const auto set_phase = [](uint32_t t) { return (t / A) & 1; };
+  auto o_full = [&](int i) { return bar(kRest + 6 * A + i); };
+  auto l_full = [&](int i) { return bar(kRest + 6 * A + 2 + i); };
+  auto o_free = [&](int i) { return bar(kRest + 6 * A + 4 + i); };
+  auto drain_bar = [&](int i) { return bar(kRest + 6 * A + 6 + i); };
   volatile int* abort = reinterpret_cast<volatile int*>(smem + C::kAbort);
   volatile int* dirty = reinterpret_cast<volatile int*>(smem + C::kDirty);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kTmemSlot);
@@ -232,24 +231,15 @@ __global__ void __launch_bounds__(kFewThreads<kCodes>, 1)
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 2 * R; ++s) {
-      mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), 1);
-      mbar_init(clean_bar(s), kCodes ? 4 : 1);
-    }
-    for (int s = 0; s < 2 * RK; ++s) {
-      mbar_init(k_full(s), 1);
-      mbar_init(k_empty(s), 1);
-    }
-    for (int r = 0; r < 2 * RW; ++r) {
-      mbar_init(raw_full(r), 1);
-      mbar_init(raw_empty(r), 4);
-    }
+    for (int s = 0; s < 6 * S; ++s) mbar_init(bar(s), 1);
     mbar_init(q_full, 1);
     mbar_init(q_empty, 2);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(s_full(i), 1);
-      mbar_init(p_full(i), 4);
+      for (uint32_t t = 0; t < A; ++t) {
+        mbar_init(s_full(i, t), 1);
+        mbar_init(p_full(i, t), 4);
+        mbar_init(done_bar(i, t), 1);
+      }
       mbar_init(o_full(i), 1);
       mbar_init(l_full(i), 4);
       mbar_init(o_free(i), 4);
@@ -263,13 +253,13 @@ __global__ void __launch_bounds__(kFewThreads<kCodes>, 1)
     prefetch_tensormap(&maps.v);
   }
   if (warp == 12) {
-    tmem_alloc(sbase + C::kTmemSlot, kFewTmem);
+    tmem_alloc(sbase + C::kTmemSlot, C::kTmemCols);
     tmem_relinquish();
   }
   // Rows without a query hold zeros (of codes their writer clears them): no copy writes them.
   const uint32_t q_bytes = (uint32_t)(a.G * a.rows_l * 128);
   if (!kCodes && q_bytes < (uint32_t)C::kQAtom) {
-    for (uint32_t at = q_bytes + 16 * threadIdx.x; at < (uint32_t)C::kQAtom; at += 16 * kFewThreads<kCodes>)
+    for (uint32_t at = q_bytes + 16 * threadIdx.x; at < (uint32_t)C::kQAtom; at += 16 * kFewThreads)
 #pragma unroll
       for (int k = 0; k < C::kAtoms; ++k)
         *reinterpret_cast<uint4*>(smem + C::kQ + k * C::kQAtom + at) = make_uint4(0, 0, 0, 0);
@@ -281,12 +271,19 @@ __global__ void __launch_bounds__(kFewThreads<kCodes>, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const auto s_col = [&](int i) { return tmem + (uint32_t)(96 * i); };
-  const auto o_col = [&](int i) { return tmem + 192u + (uint32_t)(32 * i); };
+  const auto s_col = [&](int i, uint32_t t) { return tmem + (uint32_t)(i * (A + 1) * C::kCols) + (t % A) * C::kCols; };
+  const auto o_col = [&](int i) { return tmem + (uint32_t)((i * (A + 1) + A) * C::kCols); };
+  // The stage of a group's entry: of its one ring (K and V in turn), or of its ring of K or of V.
+  const auto stage_of = [](bool is_v, int i, uint32_t e) {
+    return kCodes ? (is_v ? 2 * RK + i * RV + (int)(e % (RV ? RV : 1)) : i * RK + (int)(e % (RK ? RK : 1))) : i * R + (int)(e % (R ? R : 1));
+  };
+  const auto stage_phase = [](bool is_v, uint32_t e) {
+    constexpr uint32_t k = kCodes ? RK : R, v = kCodes ? RV : R;
+    return (is_v ? e / v : e / k) & 1;
+  };
   const auto group_tiles = [](int n, int i) { return (n + 1 - i) / 2; };
 
-  // Each group has rings of its own, of its K and V tiles in turn: a waiter has
-  // to see every filling of its stages.
+  // Each group has rings of its own: a waiter has to see every filling of its stages.
   //
   // The page of box `lane` of a tile as the table has it (checked when it is used:
   // the load is in flight until then), or one behind the last: a copy then writes zeros.
@@ -297,41 +294,14 @@ __global__ void __launch_bounds__(kFewThreads<kCodes>, 1)
     return page;
   };
 
-  // A quarter of a tile of V's codes of group i from its raw ring to the operands' ring, as
-  // binary16 in the 128-byte swizzle; `count` is of the group's tiles.
-  auto convert = [&](const Item& x, int i, int tile, int quarter, uint32_t count) {
-    constexpr int kW = RW ? RW : 1;
-    const int rs = i * kW + (int)(count % kW), st = i * R + (int)(count % R);
-    if (!mbar_wait_lanes(raw_full(rs), (count / kW) & 1, abort) ||
-        !mbar_wait_lanes(empty_bar(st), ((count / R) & 1) ^ 1, abort))
-      return false;
-    const int key0 = tile * kKeys;
-    if (convert_rows<DP, true>(smem + C::kRaw + rs * C::kRawTile, smem + C::kRing + st * C::kTile, quarter, lane,
-                               key0 + kKeys > x.lim0 ? x.lim0 - key0 : kKeys, x.limit - key0))
-      *dirty = 1;
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(clean_bar(st));
-      mbar_arrive(raw_empty(rs));
-    }
-    return true;
-  };
-
   if (warp == 13 || warp == 16) {
     // ---------------------------------------------------------------- copies of K (and Q), and of V
     const bool is_v = warp == 16;
     const CUtensorMap* map = is_v ? &maps.v : &maps.k;
-    // The ring that a group's copies go to: of S stages of `stage` bytes, this warp's
-    // entries `step` apart (16 bits: K and V in turn).
-    constexpr int kStages = kCodes ? 0 : R;
-    const int S = kCodes ? (is_v ? RW : RK) : kStages, step = kCodes ? 1 : 2;
+    // entries of a group's ring; where K and V share it this warp's are every other one
+    constexpr uint32_t step = kCodes ? 1 : 2;
     uint32_t entry[2] = {!kCodes && is_v ? 1u : 0u, !kCodes && is_v ? 1u : 0u}, qcount = 0;
-    const auto stage_of = [&](int i, uint32_t e) { return i * S + (int)(e % (uint32_t)S); };
-    const auto full_of = [&](int st) { return kCodes ? (is_v ? raw_full(st) : k_full(st)) : full_bar(st); };
-    const auto empty_of = [&](int st) { return kCodes ? (is_v ? raw_empty(st) : k_empty(st)) : empty_bar(st); };
-    const uint32_t stage_bytes = kCodes ? (is_v ? C::kRawTile : kAtom) : C::kTile, row_bytes = kCodes && is_v ? DP : 128;
-    const uint32_t ring = sbase + (kCodes ? (is_v ? C::kRaw : C::kKRing) : C::kRing) + lane * a.box * row_bytes;
+    const uint32_t ring = sbase + C::kRing + lane * a.box * 128;
     bool ok = true;
     Units units(a, seqs, tiles, state);
     Item x;
@@ -354,19 +324,19 @@ __global__ void __launch_bounds__(kFewThreads<kCodes>, 1)
         const int next = ask_page(x, t + 1);     // a tile ahead
         const int i = (t - x.t0) & 1;
         const uint32_t e = i ? entry[1] : entry[0];
-        const int st = stage_of(i, e);
-        ok = mbar_wait_lanes(empty_of(st), ((e / (uint32_t)S) & 1) ^ 1, abort);
+        const int st = stage_of(is_v, i, e);
+        ok = mbar_wait_lanes(empty_bar(st), stage_phase(is_v, e) ^ 1, abort);
         if (!ok) break;
         if (i) entry[1] += step;
         else entry[0] += step;
-        if (lane == 0) mbar_arrive_expect_tx(full_of(st), stage_bytes);
+        if (lane == 0) mbar_arrive_expect_tx(full_bar(st), C::kTile);
         __syncwarp();
         if (lane < a.boxes) {
           const int key = t * kKeys + lane * a.box, slot = key - quotient(key, a.by_page) * a.page_size;
           if (page < 0 || page > a.pages) page = a.pages;
-          const uint32_t dst = ring + st * stage_bytes;
-          tma_load_4d(dst, map, full_of(st), 0, x.hk, slot, page);
-          if (!kCodes && C::kAtoms == 2) tma_load_4d(dst + kAtom, map, full_of(st), 64, x.hk, slot, page);
+          const uint32_t dst = ring + st * C::kTile;
+          tma_load_4d(dst, map, full_bar(st), 0, x.hk, slot, page);
+          if (C::kAtoms == 2) tma_load_4d(dst + kAtom, map, full_bar(st), 64, x.hk, slot, page);
         }
         __syncwarp();
         page = next;
@@ -377,67 +347,68 @@ __global__ void __launch_bounds__(kFewThreads<kCodes>, 1)
     // ---------------------------------------------------------------- MMA issue, a thread for each group
     if (elect_one()) {
       const int i = warp == 12 ? 0 : 1;
-      uint32_t entry = 0, k_entry = 0;           // of this group's rings
-      uint32_t qcount = 0, pcount = 0, icount = 0;
+      uint32_t tile = 0;                         // of the group's
+      uint32_t qcount = 0, icount = 0;
       bool ok = true;
+      const uint64_t qd = sw128_kmajor_desc(sbase + C::kQ);
+      // Scores of the group's tile t.
+      auto scores = [&](uint32_t t) {
+        const uint32_t e = kCodes ? t : 2 * t;
+        const int st = stage_of(false, i, e);
+        // a ring of both goes by way of the clearing warp, which has to see every filling of it
+        if (!mbar_wait_awake(kCodes ? full_bar(st) : clean_bar(st), stage_phase(false, e), abort)) return false;
+        tc_fence_after();
+        const uint64_t kd = sw128_kmajor_desc(sbase + C::kRing + st * C::kTile);
+        if constexpr (kCodes) {
+#pragma unroll
+          for (int k = 0; k < DP / 32; ++k) mma_f8f6f4(s_col(i, t), kd + 2 * k, qd + 2 * k, kIdescS, k != 0);
+        } else {
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k)      // descriptors count in 16 bytes
+            mma_f16(s_col(i, t), kd + (((k >> 2) * kAtom + 32 * (k & 3)) >> 4), qd + (((k >> 2) * C::kQAtom + 32 * (k & 3)) >> 4),
+                    kIdescS, k != 0);
+        }
+        mma_commit(s_full(i, t));
+        mma_commit(empty_bar(st));
+        return true;
+      };
       Units units(a, seqs, tiles, state);
       Item x;
       while (ok && units.next(x)) {
-        const int n = x.n();
-        if (n == 0) continue;
+        if (x.n() == 0) continue;
+        const int n = group_tiles(x.n(), i);
         // also by a group without a tile: its word on Q below belongs to this Q
-        ok = mbar_wait_awake(q_full, qcount & 1, abort);
+        ok = mbar_wait_awake(q_full, qcount++ & 1, abort);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t qd = sw128_kmajor_desc(sbase + C::kQ);
-        for (int j = i; ok && j < n; j += 2) {
-          const bool first = j == i, last = j + 2 >= n;
-          if constexpr (kCodes) {
-            const int st = i * RK + (int)(k_entry % RK);
-            ok = mbar_wait_awake(k_full(st), (k_entry / RK) & 1, abort);
-            if (!ok) break;
-            ++k_entry;
-            tc_fence_after();
-            const uint64_t kd = sw128_kmajor_desc(sbase + C::kKRing + st * kAtom);
-#pragma unroll
-            for (int k = 0; k < DP / 32; ++k) mma_f8f6f4(s_col(i), kd + 2 * k, qd + 2 * k, kIdescS, k != 0);
-            mma_commit(s_full(i));
-            mma_commit(k_empty(st));
-          } else {
-            const int st = i * R + (int)(entry % R);
-            ok = mbar_wait_awake(clean_bar(st), (entry / R) & 1, abort);
-            if (!ok) break;
-            ++entry;
-            tc_fence_after();
-            const uint64_t kd = sw128_kmajor_desc(sbase + C::kRing + st * C::kTile);
-#pragma unroll
-            for (int k = 0; k < DP / 16; ++k)     // descriptors count in 16 bytes
-              mma_f16(s_col(i), kd + (((k >> 2) * kAtom + 32 * (k & 3)) >> 4), qd + (((k >> 2) * C::kQAtom + 32 * (k & 3)) >> 4),
-                      kIdescS, k != 0);
-            mma_commit(s_full(i));
-            mma_commit(empty_bar(st));
-          }
-          if (last) mma_commit(q_empty);
-
-          const int st = i * R + (int)(entry % R);
-          ok = mbar_wait_awake(clean_bar(st), (entry / R) & 1, abort);
+        int started = 0;                         // tiles whose scores are under way
+        for (int j = 0; ok && j < n; ++j, ++tile) {
+          // The set of S^T that tile j + A's scores go to has been read: P of tile j was waited for.
+          for (; ok && started < n && started < j + A; ++started) ok = scores(tile + (uint32_t)(started - j));
           if (!ok) break;
-          ++entry;
-          if (first) ok = mbar_wait_awake(o_free(i), (icount++ & 1) ^ 1, abort);   // the epilogue has read O_i
-          ok = ok && mbar_wait_awake(p_full(i), pcount & 1, abort);
+          if (started == n && j + A >= n && j == max(n - A, 0)) mma_commit(q_empty);
+          const uint32_t e = kCodes ? tile : 2 * tile + 1;
+          const int st = stage_of(true, i, e);
+          ok = mbar_wait_awake(clean_bar(st), stage_phase(true, e), abort);
+          if (j == 0) ok = ok && mbar_wait_awake(o_free(i), (icount++ & 1) ^ 1, abort);   // the epilogue has read O_i
+          ok = ok && mbar_wait_awake(p_full(i, tile), set_phase(tile), abort);
           if (!ok) break;
-          ++pcount;
           tc_fence_after();
           const uint64_t vd = sw128_mnmajor_desc(sbase + C::kRing + st * C::kTile);
-          const uint64_t pd = sw128_kmajor_desc(sbase + C::kP + i * 2 * N * 128);
+          const uint64_t pd = sw128_kmajor_desc(sbase + C::kP + (i * A + (int)(tile % A)) * C::kPSet);
+          if constexpr (kCodes) {
 #pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            mma_f16(o_col(i), vd + (2048 * k >> 4), pd + (((k >> 2) * (N * 128) + 32 * (k & 3)) >> 4), kIdescO, !first || k != 0);
+            for (int k = 0; k < kKeys / 32; ++k) mma_f8f6f4(o_col(i), vd + (4096 * k >> 4), pd + 2 * k, kIdescO, j != 0 || k != 0);
+          } else {
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+              mma_f16(o_col(i), vd + (2048 * k >> 4), pd + (((k >> 2) * C::kPAtom + 32 * (k & 3)) >> 4), kIdescO, j != 0 || k != 0);
+          }
           mma_commit(empty_bar(st));
-          if (last) mma_commit(o_full(i));
+          if (A > 1) mma_commit(done_bar(i, tile));
+          if (j + 1 == n) mma_commit(o_full(i));
         }
-        if (i == 1 && n == 1) mma_commit(q_empty);   // no tile of its own
-        ++qcount;
+        if (n == 0) mma_commit(q_empty);         // no tile of its own
       }
       if (!ok) record_timeout(abort);
       // All MMAs complete before TMEM is freed.
@@ -445,18 +416,41 @@ __global__ void __launch_bounds__(kFewThreads<kCodes>, 1)
       volatile int never = 0;
       if (!mbar_wait(drain_bar(i), 0, &never, kWaitLimitNs)) atomicOr(&g_paged_err, kErrTimeout);
     }
-  } else if (warp == 14 || warp > 16) {
+  } else if (warp == 14) {
+    // ---------------------------------------------------------------- V rows that not all rows see
+    uint32_t entry[2] = {0, 0};
     bool ok = true;
     Units units(a, seqs, tiles, state);
     Item x;
+    while (ok && units.next(x)) {
+      constexpr int kKinds = kCodes ? 1 : 2;     // entries of a ring for each tile: V, or K and V
+#pragma unroll 1
+      for (int k = 0; ok && k < kKinds * x.n(); ++k) {
+        const int j = k / kKinds, i = j & 1;
+        const uint32_t e = i ? entry[1]++ : entry[0]++;
+        const int st = stage_of(true, i, e), key0 = (x.t0 + j) * kKeys;
+        ok = mbar_wait_lanes(full_bar(st), stage_phase(true, e), abort);
+        if (!ok) break;
+        if ((kCodes || (k & 1)) && key0 + kKeys > x.lim0) {
+          if (clear_rows<kF16, kCodes, C::kAtoms>(smem + C::kRing + st * C::kTile, lane, x.lim0 - key0, x.limit - key0)) *dirty = 1;
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive(clean_bar(st));
+      }
+    }
+    if (!ok && lane == 0) record_timeout(abort);
+  } else if (warp == 17) {
     if constexpr (kCodes) {
       // ---------------------------------------------------------------- queries as E4M3 terms
       // Row r's terms are rows r, N + r and 2 N + r of the operand, four dimensions a lane.
-      uint32_t qcount = 0, tiles_done = 0;
+      bool ok = true;
+      uint32_t qcount = 0;
       const float scale = a.scale_log2 * ld_f32(a.k_scale);
+      Units units(a, seqs, tiles, state);
+      Item x;
       while (ok && units.next(x)) {
         if (x.n() == 0) continue;
-        if (warp == 14) {
         ok = mbar_wait_lanes(q_empty, (qcount & 1) ^ 1, abort);
         if (!ok) break;
         const uint16_t* q = static_cast<const uint16_t*>(a.q) + (int64_t)x.row0 * a.q_l + (int64_t)x.hk * a.G * a.q_h + 4 * lane;
@@ -503,41 +497,21 @@ __global__ void __launch_bounds__(kFewThreads<kCodes>, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
-        }
-#pragma unroll 1
-        for (int t = x.t0 + 1; ok && t < x.t1; t += 2) ok = convert(x, 1, t, warp == 14 ? 0 : warp - 16, tiles_done++);
       }
-    } else {
-      // ---------------------------------------------------------------- V rows that not all rows see
-      uint32_t entry[2] = {0, 0};
-      while (ok && units.next(x)) {
-#pragma unroll 1
-        for (int k = 0; ok && k < 2 * x.n(); ++k) {   // K and V of a tile in turn
-          const int i = (k >> 1) & 1;
-          const uint32_t e = i ? entry[1]++ : entry[0]++;
-          const int st = i * R + (int)(e % R), key0 = (x.t0 + (k >> 1)) * kKeys;
-          ok = mbar_wait_lanes(full_bar(st), (e / R) & 1, abort);
-          if (!ok) break;
-          if ((k & 1) && key0 + kKeys > x.lim0) {
-            if (clear_rows<kF16, C::kAtoms>(smem + C::kRing + st * C::kTile, lane, x.lim0 - key0, x.limit - key0)) *dirty = 1;
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-          if (lane == 0) mbar_arrive(clean_bar(st));
-        }
-      }
+      if (!ok && lane == 0) record_timeout(abort);
     }
-    if (!ok && lane == 0) record_timeout(abort);
   } else if (warp < 8) {
     // ---------------------------------------------------------------- softmax: a thread a key
     const int i = warp >> 2;                     // group
     const int key_in = (warp & 3) * 32 + lane;
     const uint32_t quad = (uint32_t)((warp & 3) * 32) << 16;
     const int id = 1 + i;                        // the group's barrier
-    // where this key's column of P stands, row 0, before the swizzle
-    uint8_t* p_at = smem + C::kP + i * 2 * N * 128 + (key_in >> 6) * (N * 128) + (key_in & 7) * 2;
-    const int p_chunk = (key_in & 63) >> 3;
-    uint32_t scount = 0, icount = 0, items = 0;
+    // What a new maximum leaves room for: with codes its weight is 2^7.  It grows to 2^8 either way.
+    constexpr float kTop = kCodes ? 7.0f : 0.0f, kGrow = kLazyMax;
+    // where this key's column of P stands, row 0 of set 0, before the swizzle
+    uint8_t* p_at = smem + C::kP + i * A * C::kPSet + (kCodes ? key_in & 15 : (key_in >> 6) * C::kPAtom + (key_in & 7) * 2);
+    const int p_chunk = kCodes ? key_in >> 4 : (key_in & 63) >> 3;
+    uint32_t tile = 0, icount = 0, items = 0;
     // A warp whose wait gave up goes on to the group's next vote, so that no barrier
     // waits for it, and the group leaves together.
     bool ok = true, out = false;
@@ -555,10 +529,9 @@ __global__ void __launch_bounds__(kFewThreads<kCodes>, 1)
 #pragma unroll
       for (int r = 0; r < N; ++r) l[r] = 0.0f;
 #pragma unroll 1
-      for (int j = 0; j < n; ++j) {
+      for (int j = 0; j < n; ++j, ++tile) {
         const int key0 = (x.t0 + 2 * j + i) * kKeys;
-        ok = ok && mbar_wait_lanes(s_full(i), scount & 1, abort);
-        ++scount;
+        ok = ok && mbar_wait_lanes(s_full(i, tile), set_phase(tile), abort);
         float s[N];                              // scaled scores, in powers of two
         bool grow = !ok || j == 0;
         if (ok) {
@@ -572,11 +545,11 @@ __global__ void __launch_bounds__(kFewThreads<kCodes>, 1)
           for (int r0 = 0; r0 < N; r0 += 4) {
             if (r0 >= valid) break;
             uint32_t t[4];
-            tmem_ld_32x32b_x4(s_col(i) + quad + (kCodes ? 2 * N : 0) + r0, t);
+            tmem_ld_32x32b_x4(s_col(i, tile) + quad + (kCodes ? 2 * N : 0) + r0, t);
             if constexpr (kCodes) {              // t0 + (t1 + t2 / 16) / 16
               uint32_t t1[4], t0[4];
-              tmem_ld_32x32b_x4(s_col(i) + quad + N + r0, t1);
-              tmem_ld_32x32b_x4(s_col(i) + quad + r0, t0);
+              tmem_ld_32x32b_x4(s_col(i, tile) + quad + N + r0, t1);
+              tmem_ld_32x32b_x4(s_col(i, tile) + quad + r0, t0);
               tmem_ld_wait();
               const float4 f = *reinterpret_cast<const float4*>(row_factor + r0);
               const float ff[4] = {f.x, f.y, f.z, f.w};
@@ -597,10 +570,14 @@ __global__ void __launch_bounds__(kFewThreads<kCodes>, 1)
                 if (++head == a.G) head = 0, ++token;
               }
               // a row without a query has no say: what it holds must not decide on roundings
-              grow |= r0 + e < valid && (s[r0 + e] > mm[e] + kLazyMax || (mm[e] == -INFINITY && s[r0 + e] > -INFINITY));
+              grow |= r0 + e < valid && (s[r0 + e] > mm[e] + kGrow || (mm[e] == -INFINITY && s[r0 + e] > -INFINITY));
             }
           }
         }
+        // P's set has been read by the product of A tiles before (with one set that is complete
+        // as the scores are, which were started behind it).
+        if (A > 1 && tile >= A) ok = ok && mbar_wait_lanes(done_bar(i, tile), set_phase(tile - A), abort);
+        grow |= !ok;
         __syncwarp();
         if (group_any(id, grow)) {
           if (group_any(id, !ok)) {
@@ -619,49 +596,74 @@ __global__ void __launch_bounds__(kFewThreads<kCodes>, 1)
           if ((warp & 3) == 0 && lane < N) {
             const float* t = tops + i * 4 * N + lane;
             const float m = j > 0 ? run_m[i * N + lane] : -INFINITY;
-            const float m_new = fmaxf(fmaxf(fmaxf(m, t[0]), t[N]), fmaxf(t[2 * N], t[3 * N]));
+            const float m_new = fmaxf(m, fmaxf(fmaxf(t[0], t[N]), fmaxf(t[2 * N], t[3 * N])) - kTop);
             run_m[i * N + lane] = m_new;
             run_f[i * N + lane] = m_new == -INFINITY ? 1.0f : ex2(m - m_new);
           }
           group_sync(id);
-          // Scores of this tile are complete, so the group's product with the previous
-          // one is too (issued before them): O_i may be rescaled here.
+          // O_i may be rescaled when the group's product with the previous tile is complete
+          // (with one set it is as the scores are, which were started behind it).
           if (j > 0) {
+            if (A > 1) ok = mbar_wait_lanes(done_bar(i, tile - 1), set_phase(tile - 1), abort);
+            tc_fence_after();
 #pragma unroll
             for (int r0 = 0; r0 < N; r0 += 4) {
               if (r0 >= valid) break;
-              uint32_t o[4];
-              tmem_ld_32x32b_x4(o_col(i) + quad + r0, o);
-              tmem_ld_wait();
               const float4 f4 = *reinterpret_cast<const float4*>(run_f + i * N + r0);
               const float f[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                l[r0 + e] *= f[e];
-                o[e] = __float_as_uint(__uint_as_float(o[e]) * f[e]);
+              for (int e = 0; e < 4; ++e) l[r0 + e] *= f[e];
+#pragma unroll
+              for (int c = 0; c < C::kCols; c += N) {
+                uint32_t o[4];
+                tmem_ld_32x32b_x4(o_col(i) + quad + c + r0, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f[e]);
+                tmem_st_32x32b_x4(o_col(i) + quad + c + r0, o);
               }
-              tmem_st_32x32b_x4(o_col(i) + quad + r0, o);
             }
             tmem_st_wait();
           }
         }
+        uint8_t* p_set = p_at + (int)(tile % A) * C::kPSet;
 #pragma unroll
         for (int r0 = 0; r0 < N; r0 += 4) {
           if (r0 >= valid) break;
           const float4 m4 = *reinterpret_cast<const float4*>(run_m + i * N + r0);
           const float mm[4] = {m4.x, m4.y, m4.z, m4.w};
+          float p[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int r = r0 + e;
-            const float p = ex2(s[r] - (mm[e] == -INFINITY ? 0.0f : mm[e]));
-            l[r] += p;
-            *reinterpret_cast<uint16_t*>(p_at + r * 128 + ((p_chunk ^ (r & 7)) << 4)) = (uint16_t)cvt16x2(kP16, p, 0.0f);
+            p[e] = ex2(s[r0 + e] - (mm[e] == -INFINITY ? 0.0f : mm[e]));
+            l[r0 + e] += p[e];
+          }
+          if constexpr (kCodes) {
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; e += 2) {   // two rows' terms and what they leave
+                const int row = k * N + r0 + e;
+                const uint32_t c = cvt_e4m3x2(p[e], p[e + 1]);
+                p_set[row * 128 + ((p_chunk ^ (row & 7)) << 4)] = (uint8_t)c;
+                p_set[(row + 1) * 128 + ((p_chunk ^ ((row + 1) & 7)) << 4)] = (uint8_t)(c >> 8);
+                float y0, y1;
+                f16x2_to_f32(cvt_e4m3x2_to_f16x2((uint16_t)c), y0, y1);
+                p[e] = (p[e] - y0) * 16.0f;
+                p[e + 1] = (p[e + 1] - y1) * 16.0f;
+              }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int row = r0 + e;
+              *reinterpret_cast<uint16_t*>(p_set + row * 128 + ((p_chunk ^ (row & 7)) << 4)) = (uint16_t)cvt16x2(kF16, p[e], 0.0f);
+            }
           }
         }
         tc_fence_before();
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(i));
+        if (lane == 0) mbar_arrive(p_full(i, tile));
       }
       if (out) break;
       float mine = 0.0f;                         // lane r: row r's
@@ -686,13 +688,13 @@ __global__ void __launch_bounds__(kFewThreads<kCodes>, 1)
     }
     if (!ok && lane == 0) record_timeout(abort);
   } else {
-    // ---------------------------------------------------------------- epilogue (and conversion of V's codes)
+    // ---------------------------------------------------------------- epilogue
     const int d = (warp & 3) * 32 + lane;        // this thread's dimension
     const uint32_t quad = (uint32_t)((warp & 3) * 32) << 16;
     float inv_s = 1.0f, v_scale = 1.0f;
     if (a.s_out) inv_s = __frcp_rn(ld_f32(a.s_out));
     if constexpr (kCodes) v_scale = ld_f32(a.v_scale);
-    uint32_t icount[2] = {0, 0}, tiles_done = 0;
+    uint32_t icount[2] = {0, 0};
     bool ok = true;
 
     auto put = [&](int64_t at, float y) {
@@ -740,11 +742,6 @@ __global__ void __launch_bounds__(kFewThreads<kCodes>, 1)
         put_zeros(x);
         continue;
       }
-      if constexpr (kCodes) {
-#pragma unroll 1
-        for (int t = x.t0; ok && t < x.t1; t += 2) ok = convert(x, 0, t, warp & 3, tiles_done++);
-        if (!ok) break;
-      }
       const bool two = x.n() > 1;
       for (int i = 0; i < (two ? 2 : 1) && ok; ++i) {
         if (!mbar_wait_lanes(l_full(i), icount[i] & 1, abort) ||
@@ -783,16 +780,26 @@ __global__ void __launch_bounds__(kFewThreads<kCodes>, 1)
       int head = 0;
 #pragma unroll 1
       for (int r0 = 0; r0 < valid; r0 += 4) {
-        uint32_t o0[4], o1[4];
-        tmem_ld_32x32b_x4(o_col(0) + quad + r0, o0);
-        if (two) tmem_ld_32x32b_x4(o_col(1) + quad + r0, o1);
-        tmem_ld_wait();
+        float o[2][4];                           // of codes the three terms' sum
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (i == 1 && !two) break;
+          uint32_t t[3][4];
+#pragma unroll
+          for (int c = 0; c < C::kCols / N; ++c) tmem_ld_32x32b_x4(o_col(i) + quad + c * N + r0, t[c]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            o[i][e] = __uint_as_float(t[0][e]);
+            if (kCodes) o[i][e] = fmaf(fmaf(__uint_as_float(t[2][e]), 0.0625f, __uint_as_float(t[1][e])), 0.0625f, o[i][e]);
+          }
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int r = r0 + e;
           const float f0 = __shfl_sync(0xFFFFFFFFu, a0, r & 31), f1 = __shfl_sync(0xFFFFFFFFu, a1, r & 31);
-          float y = __uint_as_float(o0[e]) * f0;
-          if (two) y = fmaf(__uint_as_float(o1[e]), f1, y);
+          float y = o[0][e] * f0;
+          if (two) y = fmaf(o[1][e], f1, y);
           if (nan_rows >> r & 1) y = __uint_as_float(0x7FC00000u);
           if (r < valid && d < a.D) {
             if (x.part >= 0) a.part[((int64_t)x.part * N + r) * DP + d] = y;
@@ -824,7 +831,7 @@ __global__ void __launch_bounds__(kFewThreads<kCodes>, 1)
   }
   if (warp == 12) {
     tc_fence_after();
-    tmem_dealloc(tmem, kFewTmem);
+    tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 
@@ -895,7 +902,7 @@ cudaError_t launch_kernel(const PagedMaps& maps, const PagedArgs& a, int grid, c
   }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(kFewThreads<kCodes>, 1, 1);
+  cfg.blockDim = dim3(kFewThreads, 1, 1);
   cfg.dynamicSmemBytes = C::kAlloc;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
