@@ -212,14 +212,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return true;
   };
-  // The page of box `lane` of a tile, or one behind the last: a copy then writes zeros.
+  // The page of box `lane` of a tile as the table has it (checked when it is used:
+  // the load is in flight until then), or one behind the last: a copy then writes zeros.
   const auto ask_page = [&](const Item& x, int tile) {
     const int key = tile * kKeys + lane * a.box;
     int page = a.pages;
-    if (lane < a.boxes && key < x.limit) {
-      const int got = ld_i32(a.table + x.b * a.table_stride + quotient(key, a.by_page));
-      if (got >= 0 && got < a.pages) page = got;
-    }
+    if (lane < a.boxes && key < x.limit) page = ld_i32(a.table + x.b * a.table_stride + quotient(key, a.by_page));
     return page;
   };
 
@@ -230,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t filled[2] = {0, 0}, raws = 0, qcount[2] = {0, 0};
     bool ok = true;
     auto load_q = [&](const Item& x, int i) {
-      if (!mbar_wait_warp(q_empty(i), (qcount[i] & 1) ^ 1, abort, kWaitLimitNs)) return false;
+      if (!mbar_wait_lanes(q_empty(i), (qcount[i] & 1) ^ 1, abort)) return false;
       ++qcount[i];
       if (lane == 0) {
         mbar_arrive_expect_tx(q_full(i), C::kAtoms * q_bytes);
@@ -258,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t dst, full;
         if constexpr (kCodes) {
           const int r = (int)(raws % RW);
-          if (!mbar_wait_warp(raw_empty(r), ((raws / RW) & 1) ^ 1, abort, kWaitLimitNs)) return false;
+          if (!mbar_wait_lanes(raw_empty(r), ((raws / RW) & 1) ^ 1, abort)) return false;
           ++raws;
           full = raw_full(r);
           dst = sbase + C::kRaw + r * C::kRawTile + lane * a.box * DP;
@@ -266,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           const uint32_t e = filled[ring];
           const int st = stage_of(ring, e);
-          if (!mbar_wait_warp(empty_bar(st), phase_of(e) ^ 1, abort, kWaitLimitNs)) return false;
+          if (!mbar_wait_lanes(empty_bar(st), phase_of(e) ^ 1, abort)) return false;
           ++filled[ring];
           full = full_bar(st);
           dst = sbase + C::kRing + st * C::kTile + lane * a.box * 128;
@@ -274,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane < a.boxes) {
+          if (page[ring] < 0 || page[ring] > a.pages) page[ring] = a.pages;
           if constexpr (kCodes) {
             tma_load_4d(dst, is_v ? &maps.v : &maps.k, full, 0, x.hk, slot, page[ring]);
           } else {
@@ -329,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto take = [&](bool is_v) {
         const uint32_t e = entry++;
         const int st = stage_of(i, e);
-        ok = ok && mbar_wait(kCodes || is_v || !kShared ? clean_bar(st) : full_bar(st), phase_of(e), abort, kWaitLimitNs);
+        ok = ok && mbar_wait_awake(kCodes || is_v || !kShared ? clean_bar(st) : full_bar(st), phase_of(e), abort);
         tc_fence_after();
         return st;
       };
@@ -339,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = x.n();
         if (n == 0) continue;
         // also by a slot without a tile: its word on Q below belongs to this Q
-        ok = mbar_wait(q_full(kShared ? i : 0), qcount & 1, abort, kWaitLimitNs);
+        ok = mbar_wait_awake(q_full(kShared ? i : 0), qcount & 1, abort);
         if (!ok) break;
         tc_fence_after();
         for (int j = kShared ? 0 : i; ok && j < n; j += kShared ? 1 : 2) {
@@ -347,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // The slots take turns: a slot's scores are started when the other's
           // are complete.
           if (kShared && (i == 1 || pcount > 0))
-            ok = ok && mbar_wait(s_full(1 - i), (pcount - (1 - i)) & 1, abort, kWaitLimitNs);
+            ok = ok && mbar_wait_awake(s_full(1 - i), (pcount - (1 - i)) & 1, abort);
           int st = take(false);
           if (!ok) break;
           const uint64_t qd = sw128_kmajor_desc(sbase + C::kQ + (kShared ? i : 0) * C::kTile);
@@ -362,11 +361,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (last) mma_commit(q_empty(kShared ? i : 0));
 
           st = take(true);
-          if (first) ok = ok && mbar_wait(o_free(i), (icount++ & 1) ^ 1, abort, kWaitLimitNs);   // the epilogue has read O_i
+          if (first) ok = ok && mbar_wait_awake(o_free(i), (icount++ & 1) ^ 1, abort);   // the epilogue has read O_i
           const uint64_t vd = sw128_mnmajor_desc(sbase + C::kRing + st * C::kTile);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {          // 64 keys at a time, as the softmax hands them over
-            ok = ok && mbar_wait(h ? p_full(i) : p_half(i), pcount & 1, abort, kWaitLimitNs);
+            ok = ok && mbar_wait_awake(h ? p_full(i) : p_half(i), pcount & 1, abort);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -399,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t e = ring ? seen_tiles[1]++ : seen_tiles[0]++;
           const int st = stage_of(ring, e);
           const bool pass = kShared && !is_v;
-          if (!pass && !mbar_wait_warp(full_bar(st), phase_of(e), abort, kWaitLimitNs)) return false;
+          if (!pass && !mbar_wait_lanes(full_bar(st), phase_of(e), abort)) return false;
           const int key0 = tile * kKeys;
           if (is_v && key0 + kKeys > x.lim0) {
             if (clear_rows<kF16, false, C::kAtoms>(smem + C::kRing + st * C::kTile, lane, x.lim0 - key0, x.limit - key0)) *dirty = 1;
@@ -434,7 +433,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       // raised (its scores may be another sequence's): what it holds must not decide on the other rows' roundings.
       const bool mine = row / a.G < a.rows_l && token < x.left;
       const int limit = mine ? seen(a, x.pos0, x.len, token + 1) : 0;
+      // A warp without a query leaves its weights as they are: they reach its own rows alone.
+      const bool busy = __any_sync(0xFFFFFFFFu, mine);
       for (int j = 0; j < n; ++j) {
+        if (!busy) {
+          if (!mbar_wait_lanes(s_full(i), scount & 1, abort)) {
+            ok = false;
+            break;
+          }
+          ++scount;
+          if (lane == 0) {
+            mbar_arrive(p_half(i));
+            mbar_arrive(p_full(i));
+          }
+          continue;
+        }
         const int key0 = (x.t0 + (kShared ? j : 2 * j + i)) * kKeys;
         const bool masked = key0 + kKeys > x.lim0;
         if (!mbar_wait_lanes(s_full(i), scount & 1, abort)) {
@@ -518,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // the epilogue has read the previous item's sums
-      if (!mbar_wait_warp(o_free(i), (icount & 1) ^ 1, abort, kWaitLimitNs)) {
+      if (!mbar_wait_lanes(o_free(i), (icount & 1) ^ 1, abort)) {
         ok = false;
         break;
       }
@@ -654,8 +667,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rs = (int)(raws % (RW ? RW : 1));
       const uint32_t e = filled[ring];
       const int st = stage_of(ring, e);
-      if (!mbar_wait_warp(raw_full(rs), (raws / (RW ? RW : 1)) & 1, abort, kWaitLimitNs) ||
-          !mbar_wait_warp(empty_bar(st), phase_of(e) ^ 1, abort, kWaitLimitNs))
+      if (!mbar_wait_lanes(raw_full(rs), (raws / (RW ? RW : 1)) & 1, abort) ||
+          !mbar_wait_lanes(empty_bar(st), phase_of(e) ^ 1, abort))
         return false;
       ++raws;
       ++filled[ring];
@@ -707,8 +720,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             put_zeros(row_at);
             continue;
           }
-          if (!mbar_wait_warp(l_full(i), icount[i] & 1, abort, kWaitLimitNs) ||
-              !mbar_wait_warp(o_full(i), icount[i] & 1, abort, kWaitLimitNs)) {
+          if (!mbar_wait_lanes(l_full(i), icount[i] & 1, abort) ||
+              !mbar_wait_lanes(o_full(i), icount[i] & 1, abort)) {
             ok = false;
             break;
           }
@@ -775,8 +788,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         for (int i = 0; i < (n1 > 0 ? 2 : 1) && ok; ++i) {
-          if (!mbar_wait_warp(l_full(i), icount[i] & 1, abort, kWaitLimitNs) ||
-              !mbar_wait_warp(o_full(i), icount[i] & 1, abort, kWaitLimitNs))
+          if (!mbar_wait_lanes(l_full(i), icount[i] & 1, abort) ||
+              !mbar_wait_lanes(o_full(i), icount[i] & 1, abort))
             ok = false;
           ++icount[i];
         }
@@ -928,12 +941,12 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedArgs a, int 
 // ------------------------------------------------------------------ host side
 
 struct Plan {
-  int few;          // rows of a unit where they are few (paged_few.cu), else 0
+  bool few;         // at most kFewRows rows a unit (paged_few.cu)
   bool shared;      // 256 rows a unit, else 128 rows over even and odd tiles
   bool may_cut;
   int DP, G, rows_l, blocks, ctas;
   int64_t items;
-  int unit_rows() const { return few ? few : shared ? 2 * kRows : kRows; }
+  int unit_rows() const { return few ? kFewRows : shared ? 2 * kRows : kRows; }
   int64_t part_rows() const { return may_cut ? 2ll * ctas * unit_rows() : 0; }
 };
 
@@ -944,8 +957,8 @@ Plan make_plan(const PagedAttnProblem& p, const PagedCache& c, int sms) {
   x.DP = p.D <= 64 ? 64 : 128;
   x.G = p.Hq / p.Hkv;
   const int64_t rows = (int64_t)p.max_q * x.G;
-  x.few = rows <= 16 ? 16 : rows <= 32 ? 32 : 0;
-  x.rows_l = (x.few ? x.few : kRows) / x.G;
+  x.few = rows <= kFewRows;
+  x.rows_l = (x.few ? kFewRows : kRows) / x.G;
   const int slots = (p.max_q + x.rows_l - 1) / x.rows_l;
   x.shared = slots > 1;
   x.blocks = x.shared ? (slots + 1) / 2 : 1;
@@ -1096,7 +1109,7 @@ cudaError_t launch_paged_attention(const PagedAttnProblem& p, const PagedCache& 
     *tmap_err = 1;
     return cudaSuccess;
   }
-  if (x.few) return launch_paged_few(maps, a, x.few, x.DP, p.f16, c.codes, x.ctas, st);
+  if (x.few) return launch_paged_few(maps, a, x.DP, p.f16, c.codes, x.ctas, st);
   if (x.DP == 64) return p.f16 ? launch_type<64, true>(maps, a, c.codes, x.shared, x.ctas, st) : launch_type<64, false>(maps, a, c.codes, x.shared, x.ctas, st);
   return p.f16 ? launch_type<128, true>(maps, a, c.codes, x.shared, x.ctas, st) : launch_type<128, false>(maps, a, c.codes, x.shared, x.ctas, st);
 }

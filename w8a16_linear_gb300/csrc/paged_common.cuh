@@ -186,6 +186,15 @@ __device__ __forceinline__ void record_timeout(volatile int* abort) {
 }
 }
 
+// mbar_wait that asks some times before it lets the thread sleep: a sleeping
+// thread is woken late, and every hand-over between roles is on a tile's way.
+__device__ __forceinline__ bool mbar_wait_awake(uint32_t bar, uint32_t parity, volatile int* abort) {
+#pragma unroll 1
+  for (int k = 0; k < 256; ++k)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, abort, kWaitLimitNs);
+}
+
 // Whether a half of one of the words (two 16-bit values each) is not finite.
 template <bool kF16>
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
@@ -398,9 +407,9 @@ inline cudaError_t read_paged_error(cudaStream_t st, uint32_t* err) {
 // Units of few rows: cutting costs the time of about 5 tiles.
 constexpr Cutting kCutFew{2, 1.0f, 5.0f};
 
-// Units of at most 16 or 32 rows (paged_few.cu).
-cudaError_t launch_paged_few(const PagedMaps& maps, const PagedArgs& a, int rows, int DP, bool f16, bool codes, int grid,
-                             cudaStream_t st);
+// Units of at most kFewRows rows (paged_few.cu).
+constexpr int kFewRows = 16;
+cudaError_t launch_paged_few(const PagedMaps& maps, const PagedArgs& a, int DP, bool f16, bool codes, int grid, cudaStream_t st);
 cudaError_t paged_few_read_error(cudaStream_t st, uint32_t* err);
 
 }  // namespace w8

@@ -1,4 +1,4 @@
-// Attention over a paged cache for units of at most N = 16 or 32 query rows (the
+// Attention over a paged cache for units of at most N = 16 query rows (the
 // new token, or a few, of a sequence, times the query heads of a key head): the
 // formula, units and pages of paged_attention.cu with the operands the other way round.
 //
@@ -39,17 +39,19 @@
 namespace w8 {
 namespace {
 
-template <int DP, bool kCodes, int N>
+constexpr int N = kFewRows;
+
+template <int DP, bool kCodes>
 struct Few {
   static constexpr int kAtoms = kCodes ? 1 : DP / 64;    // 128-byte spans of a row of K and V
   static constexpr int kTile = kAtoms * kAtom;           // bytes of 128 rows of them
   // Stages of a group's ring: of K and V in turn, or of E4M3 cells of each (of 16 bits
   // there is no room for two whole rings).
   static constexpr int kR = kCodes ? 0 : DP == 128 ? 3 : 5;
-  static constexpr int kRK = kCodes ? (N == 16 ? 3 : 2) : 0, kRV = kCodes ? 2 : 0;
+  static constexpr int kRK = kCodes ? 3 : 0, kRV = kCodes ? 2 : 0;
   static constexpr int kStages = kCodes ? kRK + kRV : kR;
   static constexpr int kCols = kCodes ? 3 * N : N;       // rows of Q and P, columns of S^T and O^T
-  static constexpr int kAhead = kCodes && N == 16 ? 2 : 1;   // sets of S^T and P of a group
+  static constexpr int kAhead = kCodes ? 2 : 1;   // sets of S^T and P of a group
   static constexpr int kRing = 0;                        // codes: K's stages, then V's, of each group
   static constexpr int kQAtom = kCols * 128;
   static constexpr int kQ = kRing + 2 * kStages * kTile;
@@ -80,15 +82,6 @@ struct Few {
 // Warps: 0-7 softmax, 8-11 epilogue, 12 and 15 MMA issue, 13 and 16 copies of K and V,
 // 14 clearing, 17 the queries' terms.
 constexpr int kFewThreads = 18 * 32;
-
-// mbar_wait that asks some times before it lets the thread sleep: a sleeping
-// thread is woken late, and every hand-over between roles is on a tile's way.
-__device__ __forceinline__ bool mbar_wait_awake(uint32_t bar, uint32_t parity, volatile int* abort) {
-#pragma unroll 1
-  for (int k = 0; k < 256; ++k)
-    if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait(bar, parity, abort, kWaitLimitNs);
-}
 
 // Whether any of the 128 threads of a group says so (named barrier `id`).
 __device__ __forceinline__ bool group_any(int id, bool mine) {
@@ -186,10 +179,10 @@ __device__ __forceinline__ void share_out_few(const PagedArgs& a, Seq* seqs, uin
   info[6] = (int)total;
 }
 
-template <int DP, bool kF16, bool kCodes, int N>
+template <int DP, bool kF16, bool kCodes>
 __global__ void __launch_bounds__(kFewThreads, 1)
     paged_few_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant__ PagedArgs a) {
-  using C = Few<DP, kCodes, N>;
+  using C = Few<DP, kCodes>;
   constexpr int R = C::kR, RK = C::kRK, RV = C::kRV, S = C::kStages, A = C::kAhead;
   constexpr uint32_t kFmt = kCodes || kF16 ? 0 : 1;  // E4M3 of its kind, binary16 of the other
   constexpr uint32_t kIdescS = make_idesc(kFmt, kFmt, kKeys, C::kCols);
@@ -837,7 +830,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
 // Joining cut units: as paged_join_kernel, with rows of DP floats; a thread
 // takes four columns of a row.
-template <int DP, bool kF16, int N>
+template <int DP, bool kF16>
 __global__ void __launch_bounds__(256) few_join_kernel(const PagedArgs a) {
   griddep_wait();
   constexpr int kBlocks = N * DP / 4 / 256;     // of a cut
@@ -886,10 +879,10 @@ __global__ void __launch_bounds__(256) few_join_kernel(const PagedArgs a) {
   }
 }
 
-template <int DP, bool kF16, bool kCodes, int N>
+template <int DP, bool kF16, bool kCodes>
 cudaError_t launch_kernel(const PagedMaps& maps, const PagedArgs& a, int grid, cudaStream_t st) {
-  using C = Few<DP, kCodes, N>;
-  auto* k = paged_few_kernel<DP, kF16, kCodes, N>;
+  using C = Few<DP, kCodes>;
+  auto* k = paged_few_kernel<DP, kF16, kCodes>;
   static std::atomic<uint64_t> allowed{0};   // devices on which the kernel may use its shared memory
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -915,27 +908,21 @@ cudaError_t launch_kernel(const PagedMaps& maps, const PagedArgs& a, int grid, c
     cfg.gridDim = dim3((unsigned)((grid - 1) * (N * DP / 4 / 256)), 1, 1);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.dynamicSmemBytes = 0;
-    if ((e = cudaLaunchKernelEx(&cfg, few_join_kernel<DP, kF16, N>, a)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, few_join_kernel<DP, kF16>, a)) != cudaSuccess) return e;
   }
   return cudaGetLastError();
 }
 
-template <int DP, bool kF16, bool kCodes>
-cudaError_t launch_rows(const PagedMaps& maps, const PagedArgs& a, int rows, int grid, cudaStream_t st) {
-  return rows == 16 ? launch_kernel<DP, kF16, kCodes, 16>(maps, a, grid, st) : launch_kernel<DP, kF16, kCodes, 32>(maps, a, grid, st);
-}
-
 template <int DP>
-cudaError_t launch_dims(const PagedMaps& maps, const PagedArgs& a, int rows, bool f16, bool codes, int grid, cudaStream_t st) {
-  if (codes) return f16 ? launch_rows<DP, true, true>(maps, a, rows, grid, st) : launch_rows<DP, false, true>(maps, a, rows, grid, st);
-  return f16 ? launch_rows<DP, true, false>(maps, a, rows, grid, st) : launch_rows<DP, false, false>(maps, a, rows, grid, st);
+cudaError_t launch_dims(const PagedMaps& maps, const PagedArgs& a, bool f16, bool codes, int grid, cudaStream_t st) {
+  if (codes) return f16 ? launch_kernel<DP, true, true>(maps, a, grid, st) : launch_kernel<DP, false, true>(maps, a, grid, st);
+  return f16 ? launch_kernel<DP, true, false>(maps, a, grid, st) : launch_kernel<DP, false, false>(maps, a, grid, st);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_few(const PagedMaps& maps, const PagedArgs& a, int rows, int DP, bool f16, bool codes, int grid,
-                             cudaStream_t st) {
-  return DP == 64 ? launch_dims<64>(maps, a, rows, f16, codes, grid, st) : launch_dims<128>(maps, a, rows, f16, codes, grid, st);
+cudaError_t launch_paged_few(const PagedMaps& maps, const PagedArgs& a, int DP, bool f16, bool codes, int grid, cudaStream_t st) {
+  return DP == 64 ? launch_dims<64>(maps, a, f16, codes, grid, st) : launch_dims<128>(maps, a, f16, codes, grid, st);
 }
 
 cudaError_t paged_few_read_error(cudaStream_t st, uint32_t* err) { return read_paged_error(st, err); }
