@@ -436,43 +436,59 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   } else if (warp == 17) {
     if constexpr (kCodes) {
       // ---------------------------------------------------------------- queries as E4M3 terms
-      // Row r's terms are rows r, N + r and 2 N + r of the operand, four dimensions a lane.
+      // Row r's terms are rows r, N + r and 2 N + r of the operand.  Four rows at a
+      // time, eight lanes a row, sixteen dimensions a lane; rows without a query are
+      // left as they are, four at a time.
       bool ok = true;
       uint32_t qcount = 0;
       const float scale = a.scale_log2 * ld_f32(a.k_scale);
+      const int part = lane & 7;
       Units units(a, seqs, tiles, state);
       Item x;
       while (ok && units.next(x)) {
         if (x.n() == 0) continue;
+        const int valid = x.left * a.G;
+        uint4 w[2];
+        auto load = [&](int r) {
+          w[0] = w[1] = make_uint4(0, 0, 0, 0);
+          if (r >= valid || 16 * part >= a.D) return;
+          const int l = r / a.G, h = r - l * a.G;
+          const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (int64_t)(x.row0 + l) * a.q_l +
+                                                          (int64_t)(x.hk * a.G + h) * a.q_h + 16 * part);
+          w[0] = q[0];
+          w[1] = q[1];
+        };
+        load(lane >> 3);
         ok = mbar_wait_lanes(q_empty, (qcount & 1) ^ 1, abort);
         if (!ok) break;
-        const uint16_t* q = static_cast<const uint16_t*>(a.q) + (int64_t)x.row0 * a.q_l + (int64_t)x.hk * a.G * a.q_h + 4 * lane;
-        const int valid = x.left * a.G;
-#pragma unroll 4
-        for (int r = 0; r < N; ++r) {
-          const int l = r / a.G, h = r - l * a.G;
-          float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          if (r < valid && 4 * lane < a.D) {
-            const uint2 w = *reinterpret_cast<const uint2*>(q + l * a.q_l + h * a.q_h);
-            const F2 lo = unpack16<kF16>(w.x), hi = unpack16<kF16>(w.y);
-            v[0] = lo.x, v[1] = lo.y, v[2] = hi.x, v[3] = hi.y;
-          }
-          float top = max_nan(max_nan(fabsf(v[0]), fabsf(v[1])), max_nan(fabsf(v[2]), fabsf(v[3])));
-          // bits of values of one sign are in the values' order, NaN last
-          const uint32_t bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));
-          // 2^-e takes the largest value to [128, 256) (less where it is below 2^-120); not finite: the row becomes NaN
-          const int e = (int)(bits >> 23) - 127 - 7;
-          const bool bad = bits >= 0x7F800000u;
-          const float down = bad ? 1.0f : pow2i(-e > 127 ? 127 : -e);
-          uint32_t t[3] = {0, 0, 0};
+#pragma unroll 1
+        for (int r0 = 0; r0 < valid; r0 += 4) {
+          const int r = r0 + (lane >> 3);
+          const uint32_t words[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+          F2 v[8];
+          float top = 0.0f;
 #pragma unroll
-          for (int k = 0; k < 4; k += 2) {
-            float x0 = v[k] * down, x1 = v[k + 1] * down;
+          for (int k = 0; k < 8; ++k) {
+            v[k] = unpack16<kF16>(words[k]);
+            top = max_nan(top, max_nan(fabsf(v[k].x), fabsf(v[k].y)));
+          }
+          load(r + 4);
+#pragma unroll
+          for (int o = 4; o >= 1; o /= 2) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+          // 2^-e takes the largest value to [128, 256) (less where it is below 2^-120); not finite: the row becomes NaN
+          const uint32_t bits = __float_as_uint(top);
+          const bool bad = bits >= 0x7F800000u;
+          const int e = (int)(bits >> 23) - 127 - 7;
+          const float down = bad ? 1.0f : pow2i(-e > 127 ? 127 : -e);
+          uint32_t t[3][4] = {};
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float x0 = v[k].x * down, x1 = v[k].y * down;
             if (bad) x0 = x1 = __uint_as_float(0x7FC00000u);
 #pragma unroll
             for (int s = 0; s < 3; ++s) {
               const uint32_t c = cvt_e4m3x2(x0, x1);
-              t[s] |= c << (8 * k);
+              t[s][k >> 1] |= c << (16 * (k & 1));
               float y0, y1;
               f16x2_to_f32(cvt_e4m3x2_to_f16x2((uint16_t)c), y0, y1);
               x0 = (x0 - y0) * 16.0f;
@@ -482,9 +498,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
           for (int s = 0; s < 3; ++s) {
             const int row = s * N + r;
-            *reinterpret_cast<uint32_t*>(smem + C::kQ + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + 4 * (lane & 3)) = t[s];
+            *reinterpret_cast<uint4*>(smem + C::kQ + row * 128 + ((part ^ (row & 7)) << 4)) = make_uint4(t[s][0], t[s][1], t[s][2], t[s][3]);
           }
-          if (lane == 0) factor[(qcount & 1) * N + r] = scale / down;
+          if (part == 0) factor[(qcount & 1) * N + r] = scale / down;
         }
         ++qcount;
         fence_proxy_async_smem();
