@@ -107,6 +107,68 @@ __device__ __forceinline__ float warp_max(float v) {
   return __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF));
 }
 
+// A CTA's units, in the order in which each of its roles goes through them: as
+// Units has them, where a sequence is one unit of each key head.
+struct FewUnits {
+  const PagedArgs& a;
+  const Seq* seqs;            // in shared memory, or null
+  const uint32_t* tiles;
+  uint32_t cur, end, step;    // the next item, or cut: the next tile and the share's end
+  int b, hk, t;               // cut: where that tile is
+  int part;
+  bool cut;
+
+  __device__ __forceinline__ FewUnits(const PagedArgs& args, const Seq* s, const uint32_t* tl, const volatile int* st)
+      : a(args), seqs(s), tiles(tl) {
+    cut = a.may_cut && st[kShares] > 0;
+    part = 2 * blockIdx.x;
+    cur = cut ? (uint32_t)st[kBegin] : blockIdx.x;
+    end = cut ? (uint32_t)st[kEnd] : (uint32_t)a.items;
+    if (cut) b = st[kAtB], hk = st[kAtHk], t = st[kAtTile];
+  }
+  __device__ __forceinline__ bool next(Item& x) {
+    Seq s;
+    do {
+      if (cur >= end) return false;
+      if (!cut) {
+        b = quotient((int)cur, a.by_hkv);
+        hk = (int)cur - b * a.Hkv;
+        cur += gridDim.x;
+      }
+      s = seqs ? seqs[b] : load_seq(a, b);
+    } while (s.tokens == 0);   // where units are cut it is one with tiles
+    x.b = b;
+    x.hk = hk;
+    x.left = s.tokens;
+    x.row0 = s.row0;
+    x.pos0 = s.base;
+    x.len = s.len;
+    x.limit = seen(a, s.base, s.len, s.tokens);
+    x.lim0 = seen(a, s.base, s.len, 1);
+    x.t0 = 0;
+    x.t1 = (x.limit + kKeys - 1) / kKeys;
+    x.part = -1;
+    if (cut) {
+      const int all = x.t1;
+      x.t0 = t;
+      x.t1 = (int)min((uint32_t)all, (uint32_t)t + (end - cur));
+      if (x.n() < all) x.part = part;
+      part = 2 * blockIdx.x + 1;
+      cur += (uint32_t)x.n();
+      t = x.t1;
+      if (t == all) {
+        t = 0;
+        if (++hk == a.Hkv) {
+          hk = 0;
+          while (++b < a.B - 1 && tiles[b] == 0) {
+          }
+        }
+      }
+    }
+    return true;
+  }
+};
+
 // The sequences to shared memory and, where units may be cut, how the work is
 // shared out (see share_out): by one warp, since a sequence is one unit of a key head.
 __device__ __forceinline__ void share_out_few(const PagedArgs& a, Seq* seqs, uint32_t* tiles, uint32_t* first, int* state) {
@@ -263,6 +325,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  griddep_launch_dependents();   // the next kernel may start its prologue
   const uint32_t tmem = *tmem_slot;
   const auto s_col = [&](int i, uint32_t t) { return tmem + (uint32_t)(i * (A + 1) * C::kCols) + (t % A) * C::kCols; };
   const auto o_col = [&](int i) { return tmem + (uint32_t)((i * (A + 1) + A) * C::kCols); };
@@ -296,7 +359,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     uint32_t entry[2] = {!kCodes && is_v ? 1u : 0u, !kCodes && is_v ? 1u : 0u}, qcount = 0;
     const uint32_t ring = sbase + C::kRing + lane * a.box * 128;
     bool ok = true;
-    Units units(a, seqs, tiles, state);
+    FewUnits units(a, seqs, tiles, state);
     Item x;
     while (ok && units.next(x)) {
       if (x.n() == 0) continue;
@@ -365,7 +428,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         mma_commit(empty_bar(st));
         return true;
       };
-      Units units(a, seqs, tiles, state);
+      FewUnits units(a, seqs, tiles, state);
       Item x;
       while (ok && units.next(x)) {
         if (x.n() == 0) continue;
@@ -413,7 +476,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     // ---------------------------------------------------------------- V rows that not all rows see
     uint32_t entry[2] = {0, 0};
     bool ok = true;
-    Units units(a, seqs, tiles, state);
+    FewUnits units(a, seqs, tiles, state);
     Item x;
     while (ok && units.next(x)) {
       constexpr int kKinds = kCodes ? 1 : 2;     // entries of a ring for each tile: V, or K and V
@@ -443,7 +506,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       uint32_t qcount = 0;
       const float scale = a.scale_log2 * ld_f32(a.k_scale);
       const int part = lane & 7;
-      Units units(a, seqs, tiles, state);
+      FewUnits units(a, seqs, tiles, state);
       Item x;
       while (ok && units.next(x)) {
         if (x.n() == 0) continue;
@@ -524,7 +587,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     // A warp whose wait gave up goes on to the group's next vote, so that no barrier
     // waits for it, and the group leaves together.
     bool ok = true, out = false;
-    Units units(a, seqs, tiles, state);
+    FewUnits units(a, seqs, tiles, state);
     Item x;
     while (!out && units.next(x)) {
       if (x.n() == 0) continue;
@@ -744,7 +807,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         put_zeros(x);
       }
     }
-    Units units(a, seqs, tiles, state);
+    FewUnits units(a, seqs, tiles, state);
     Item x;
     while (ok && units.next(x)) {
       if (x.n() == 0) {
@@ -848,6 +911,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 // takes four columns of a row.
 template <int DP, bool kF16>
 __global__ void __launch_bounds__(256) few_join_kernel(const PagedArgs a) {
+  griddep_launch_dependents();
   griddep_wait();
   constexpr int kBlocks = N * DP / 4 / 256;     // of a cut
   const int c = 1 + (int)blockIdx.x / kBlocks;
