@@ -213,32 +213,53 @@ __device__ __forceinline__ uint32_t finite(uint32_t w) {
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
 // V rows of a tile in shared memory that not every row of a unit sees (one warp;
-// eight lanes to a row's 128 bytes, four rows at a time): rows `to` and on, which none
-// sees, are cleared; of rows from .. to - 1 the values that are not finite.  Whether this
-// lane met one of those.
+// eight lanes to a row's 128 bytes): rows `to` and on, which none sees, are cleared;
+// of rows from .. to - 1 the values that are not finite.  Whether this lane met one of
+// those.  It stands between the tile's copy and its product: 16 rows' loads are under way at a time.
 template <bool kF16, bool kCells8, int kAtoms>
 __device__ __forceinline__ bool clear_rows(uint8_t* tile, int lane, int from, int to) {
-  const auto bad_of = [](uint32_t w) { return kCells8 ? nan_codes(w) : not_finite<kF16>(w); };
+  const auto bad_of = [](const uint4& w) {
+    return kCells8 ? nan_codes(w.x) | nan_codes(w.y) | nan_codes(w.z) | nan_codes(w.w)
+                   : not_finite<kF16>(w.x) | not_finite<kF16>(w.y) | not_finite<kF16>(w.z) | not_finite<kF16>(w.w);
+  };
   const auto kept = [](uint32_t w) { return kCells8 ? w & ~((nan_codes(w) >> 7) * 0xFFu) : finite<kF16>(w); };
-  bool bad = false;
   uint8_t* v = tile + (lane & 7) * 16;
+  const int sub = lane >> 3;
+  bool bad = false;
+  from = max(from, 0);
 #pragma unroll 1
-  for (int r0 = max(from, 0) & ~3; r0 < kKeys; r0 += 4) {
-    const int r = r0 + (lane >> 3);
+  for (int r0 = from & ~3; r0 < min(to, kKeys); r0 += 16) {
+    uint4 w[4][kAtoms];
+    uint32_t any = 0;
 #pragma unroll
-    for (int at = 0; at < kAtoms; ++at) {
-      uint4* p = reinterpret_cast<uint4*>(v + at * kAtom + r * 128);
-      if (r >= to) {
-        *p = make_uint4(0, 0, 0, 0);
-      } else if (r >= from) {
-        const uint4 w = *p;
-        if (bad_of(w.x) | bad_of(w.y) | bad_of(w.z) | bad_of(w.w)) {
-          *p = make_uint4(kept(w.x), kept(w.y), kept(w.z), kept(w.w));
-          bad = true;
-        }
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int at = 0; at < kAtoms; ++at)   // rows of 128 at most: the tile's last ones stand for those behind it
+        w[k][at] = *reinterpret_cast<const uint4*>(v + at * kAtom + min(r0 + 4 * k + sub, kKeys - 1) * 128);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = r0 + 4 * k + sub;
+#pragma unroll
+      for (int at = 0; at < kAtoms; ++at)
+        if (r >= from && r < to) any |= bad_of(w[k][at]);
+    }
+    if (__builtin_expect(any != 0, 0)) {
+      bad = true;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = r0 + 4 * k + sub;
+#pragma unroll
+        for (int at = 0; at < kAtoms; ++at)
+          if (r >= from && r < min(to, kKeys))
+            *reinterpret_cast<uint4*>(v + at * kAtom + r * 128) =
+                make_uint4(kept(w[k][at].x), kept(w[k][at].y), kept(w[k][at].z), kept(w[k][at].w));
       }
     }
   }
+#pragma unroll 2
+  for (int r = max(to, 0) + sub; r < kKeys; r += 4)
+#pragma unroll
+    for (int at = 0; at < kAtoms; ++at) *reinterpret_cast<uint4*>(v + at * kAtom + r * 128) = make_uint4(0, 0, 0, 0);
   return bad;
 }
 
