@@ -873,28 +873,27 @@ def _refuse_rows(t, name, dtypes, device, shape):
         raise W8Error(1, f"{name}: must be a CUDA tensor on the other operands' device")
     if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
         raise W8Error(2, f"{name}: shape {tuple(t.shape)}, expected {['any' if w is None else w for w in shape]}")
-    raise W8Error(4, f"{name}: the head's dimensions must be contiguous")
+    raise W8Error(4, f"{name}: the last dimension must be contiguous")
 
 
-def _rows(t, name, dtypes, device, M, H, D):
-    """(row, head) strides of ``t``, [M, H, D] with dense D."""
-    if t.dtype not in dtypes or t.device != device or not t.is_cuda or t.shape != (M, H, D):
-        _refuse_rows(t, name, dtypes, device, (M, H, D))
+# Of the tensors of a call the first is asked whether it is on a CUDA device, the
+# others whether they are on the same one.
+
+def _rows(t, name, dtype, device, shape):
+    """(row, head) strides of ``t``, of ``shape`` [M, H, D] with dense D."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
+        _refuse_rows(t, name, (dtype,), device, shape)
     sr, sh, sd = t.stride()
-    if sd != 1 and D > 1:
-        _refuse_rows(t, name, dtypes, device, (M, H, D))
+    if sd != 1 and shape[2] > 1:
+        _refuse_rows(t, name, (dtype,), device, shape)
     return sr, sh
 
 
 def _ints(t, name, n, device):
     """data_ptr of ``t``, n dense int32 values on ``device``."""
-    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous() or t.device != device or not t.is_cuda:
+    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous() or t.device != device:
         _refuse(t, name, (torch.int32,), device, numel=n)
     return t.data_ptr()
-
-
-def _weight(t, name, dtype, D, device):
-    return None if t is None else _like(t, name, (dtype,), (D,), device)
 
 
 def _rotation(turns, positions, axes, M, device):
@@ -903,18 +902,24 @@ def _rotation(turns, positions, axes, M, device):
         if positions is not None or axes is not None:
             raise W8Error(11, "positions and axes belong to a rotation (turns)")
         return 0, 1, (0, 0, 0), None, None, 0
-    if turns.dtype is not torch.int64 or turns.dim() != 1 or not turns.is_contiguous() or turns.device != device \
-            or not turns.is_cuda:
+    pairs = turns.numel()
+    if turns.dtype is not torch.int64 or turns.shape != (pairs,) or not turns.is_contiguous() or turns.device != device:
         _refuse(turns, "turns", (torch.int64,), device, shape=("pairs",))
-    pairs = turns.shape[0]
-    axes = (pairs,) if axes is None else tuple(axes)
+    if axes is None or len(axes) == 1:
+        axes = (pairs, 0, 0) if axes is None else (*axes, 0, 0)
+        if positions is None:
+            return 2 * pairs, 1, axes, turns.data_ptr(), None, 0
+        if positions.dtype is torch.int32 and positions.shape == (M,) and positions.device == device \
+                and (M < 2 or positions.stride(0) == 1):
+            return 2 * pairs, 1, axes, turns.data_ptr(), positions.data_ptr(), 0
+        axes = axes[:1]
+    axes = tuple(axes)
     if not 1 <= len(axes) <= 3:
         raise W8Error(2, f"axes: {axes}, expected 1 to 3 numbers of pairs")
     p_pos, pitch = None, 0
     if positions is not None:
         shape = (M,) if len(axes) == 1 and positions.dim() == 1 else (len(axes), M)
-        if positions.dtype is not torch.int32 or positions.shape != shape or positions.device != device \
-                or not positions.is_cuda:
+        if positions.dtype is not torch.int32 or positions.shape != shape or positions.device != device:
             _refuse_rows(positions, "positions", (torch.int32,), device, shape)
         if M > 1 and positions.stride(-1) != 1:
             raise W8Error(4, "positions: an axis's positions must be contiguous")
@@ -941,65 +946,62 @@ def qk_norm_rope(q, k, positions=None, turns=None, q_weight=None, k_weight=None,
         if not q.is_cuda:
             raise W8Error(1, "q: must be a CUDA tensor")
         raise W8Error(2, f"q: expected [tokens, heads, D], got {tuple(q.shape)}")
-    M, Hq, D = q.shape
-    same = (dtype,)
+    shape = q.shape
+    M, Hq, D = shape
     Hk = 0
     sk = sko = (0, 0)
-    p_k = p_ko = None
+    p_k = p_ko = p_wq = p_wk = None
     if k is not None:
         Hk = k.shape[1] if k.dim() == 3 else -1
-        sk = _rows(k, "k", same, device, M, Hk, D)
+        k_shape = (M, Hk, D)
+        sk = _rows(k, "k", dtype, device, k_shape)
         p_k = k.data_ptr()
         if k_out is None:
-            k_out = _empty((M, Hk, D), dtype, device, stream)
-        sko = _rows(k_out, "k_out", same, device, M, Hk, D)
+            k_out = _empty(k_shape, dtype, device, stream)
+        sko = _rows(k_out, "k_out", dtype, device, k_shape)
         p_ko = k_out.data_ptr()
     elif k_out is not None or k_weight is not None:
         raise W8Error(1, "k_out or k_weight without k")
+    if q_weight is not None:
+        p_wq = _like(q_weight, "q_weight", (dtype,), (D,), device)
+    if k_weight is not None:
+        p_wk = _like(k_weight, "k_weight", (dtype,), (D,), device)
     rot, n_axes, axes, p_turns, p_pos, pitch = _rotation(turns, positions, axes, M, device)
-    if turns is not None and positions is None:
+    if positions is None and turns is not None:
         raise W8Error(1, "positions: a rotation needs them")
     if q_out is None:
-        q_out = _empty((M, Hq, D), dtype, device, stream)
-    desc = _rope_desc(M, Hq, Hk, D, *_rows(q, "q", same, device, M, Hq, D), *sk, 0, 0,
-                      *_rows(q_out, "q_out", same, device, M, Hq, D), *sko, pitch, dt, rot, bool(interleaved), n_axes, *axes,
-                      eps, amplitude)
-    _check(lib().qk_norm_rope(desc, q.data_ptr(), p_k, p_pos, p_turns, _weight(q_weight, "q_weight", dtype, D, device),
-                              _weight(k_weight, "k_weight", dtype, D, device), q_out.data_ptr(), p_ko,
-                              _raw_stream(stream, device)))
+        q_out = _empty(shape, dtype, device, stream)
+    desc = _rope_desc(M, Hq, Hk, D, *_rows(q, "q", dtype, device, shape), *sk, 0, 0, *_rows(q_out, "q_out", dtype, device, shape),
+                      *sko, pitch, dt, rot, interleaved, n_axes, *axes, eps, amplitude)
+    status = lib().qk_norm_rope(desc, q.data_ptr(), p_k, p_pos, p_turns, p_wq, p_wk, q_out.data_ptr(), p_ko,
+                                          _raw_stream(stream, device))
+    if status:
+        _check(status)
     return q_out, k_out
 
 
-def _cells(t, name, kinds, device):
-    """(page, position, head) strides of a cache [pages, page_size, heads, D]."""
-    if t.dim() != 4 or t.dtype not in kinds or t.device != device or not t.is_cuda:
-        _refuse_rows(t, name, kinds, device, (None,) * 4)
-    sp, sl, sh, sd = t.stride()
-    if sd != 1 and t.shape[3] > 1:
-        _refuse_rows(t, name, kinds, device, (None,) * 4)
-    return sp, sl, sh
-
-
-def _paged(dtype, device, k_cache, v_cache, page_table):
+def _paged(dtype, dt, device, k_cache, v_cache, page_table):
     """(descriptor of a paged cache beside tensors of ``dtype``, sequences, heads, D, page table's pointer)."""
-    codes = k_cache.dtype in _CODES
-    kinds = _CODES if codes else (dtype,)
-    sk = _cells(k_cache, "k_cache", kinds, device)
-    sv = sk if v_cache is None else _cells(v_cache, "v_cache", kinds, device)
-    if v_cache is not None and v_cache.shape != k_cache.shape:
-        raise W8Error(2, f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} differ")
-    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.device != device or not page_table.is_cuda:
+    cells, shape = k_cache.dtype, k_cache.shape
+    codes = cells is not dtype
+    if (codes and cells not in _CODES) or len(shape) != 4 or k_cache.device != device:
+        _refuse_rows(k_cache, "k_cache", (dtype, *_CODES), device, (None,) * 4)
+    sk = sv = k_cache.stride()
+    if v_cache is not None:
+        if v_cache.shape != shape or v_cache.device != device or (v_cache.dtype is not cells and not (codes and v_cache.dtype in _CODES)):
+            _refuse_rows(v_cache, "v_cache", _CODES if codes else (dtype,), device, shape)
+        sv = v_cache.stride()
+    if (sk[3] != 1 or sv[3] != 1) and shape[3] > 1:
+        raise W8Error(4, "k_cache, v_cache: the head's dimensions must be contiguous")
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.device != device:
         _refuse_rows(page_table, "page_table", (torch.int32,), device, (None, None))
     B, cols = page_table.shape
-    if cols > 1 and page_table.stride(1) != 1:
+    pitch, step = page_table.stride()
+    if step != 1 and cols > 1:
         raise W8Error(4, "page_table: a sequence's pages must be contiguous")
-    pages, size, Hk, D = k_cache.shape
-    desc = _paged_desc(B, pages, size, cols, page_table.stride(0), Hk, D, *sk, *sv, DTYPE_E4M3 if codes else _DTYPE16[dtype])
-    return desc, B, Hk, D, page_table.data_ptr()
-
-
-def _scale_ptr(t, name, device):
-    return None if t is None else _floats(t, name, 1, device)
+    desc = _paged_desc(B, shape[0], shape[1], cols, pitch, shape[2], shape[3], sk[0], sk[1], sk[2], sv[0], sv[1], sv[2],
+                       DTYPE_E4M3 if codes else dt)
+    return desc, B, shape[2], shape[3], page_table.data_ptr()
 
 
 def paged_kv_append(k, v, k_cache, v_cache, page_table, q_start, kv_len, turns=None, q=None, q_weight=None, k_weight=None,
@@ -1023,47 +1025,54 @@ def paged_kv_append(k, v, k_cache, v_cache, page_table, q_start, kv_len, turns=N
         raise W8Error(5, f"k: expected bfloat16 or float16, got {dtype}")
     if not k.is_cuda:
         raise W8Error(1, "k: must be a CUDA tensor")
-    cache, B, Hk, D, p_table = _paged(dtype, device, k_cache, v_cache, page_table)
+    cache, B, Hk, D, p_table = _paged(dtype, dt, device, k_cache, v_cache, page_table)
     T = k.shape[0] if k.dim() else 0
-    same = (dtype,)
-    sk, sv = _rows(k, "k", same, device, T, Hk, D), _rows(v, "v", same, device, T, Hk, D)
-    Hq, sq, sqo, p_q, p_qo = 0, (0, 0), (0, 0), None, None
+    shape = (T, Hk, D)
+    sk, sv = _rows(k, "k", dtype, device, shape), _rows(v, "v", dtype, device, shape)
+    Hq, sq, sqo, p_q, p_qo, p_wq, p_wk = 0, (0, 0), (0, 0), None, None, None, None
     if q is not None:
         Hq = q.shape[1] if q.dim() == 3 else -1
-        sq = _rows(q, "q", same, device, T, Hq, D)
+        shape = (T, Hq, D)
+        sq = _rows(q, "q", dtype, device, shape)
         if q_out is None:
-            q_out = _empty((T, Hq, D), dtype, device, stream)
-        sqo = _rows(q_out, "q_out", same, device, T, Hq, D)
+            q_out = _empty(shape, dtype, device, stream)
+        sqo = _rows(q_out, "q_out", dtype, device, shape)
         p_q, p_qo = q.data_ptr(), q_out.data_ptr()
+        if q_weight is not None:
+            p_wq = _like(q_weight, "q_weight", (dtype,), (D,), device)
     elif q_out is not None or q_weight is not None:
         raise W8Error(1, "q_out or q_weight without q")
+    if k_weight is not None:
+        p_wk = _like(k_weight, "k_weight", (dtype,), (D,), device)
     rot, n_axes, axes, p_turns, p_pos, pitch = _rotation(turns, positions, axes, T, device)
-    desc = _rope_desc(T, Hq, Hk, D, *sq, *sk, *sv, *sqo, 0, 0, pitch, dt, rot, bool(interleaved), n_axes, *axes, eps,
-                      amplitude)
-    p_start = None if q_start is None else _ints(q_start, "q_start", B + 1, device)
-    _check(lib().paged_kv_append(desc, cache, p_q, k.data_ptr(), v.data_ptr(), p_pos, p_turns,
-                                 _weight(q_weight, "q_weight", dtype, D, device), _weight(k_weight, "k_weight", dtype, D, device),
-                                 k_cache.data_ptr(), v_cache.data_ptr(), p_table, p_start, _ints(kv_len, "kv_len", B, device),
-                                 _scale_ptr(k_scale, "k_scale", device), _scale_ptr(v_scale, "v_scale", device), p_qo,
-                                 _raw_stream(stream, device)))
+    desc = _rope_desc(T, Hq, Hk, D, *sq, *sk, *sv, *sqo, 0, 0, pitch, dt, rot, interleaved, n_axes, *axes, eps, amplitude)
+    status = lib().paged_kv_append(
+        desc, cache, p_q, k.data_ptr(), v.data_ptr(), p_pos, p_turns, p_wq, p_wk, k_cache.data_ptr(), v_cache.data_ptr(), p_table,
+        None if q_start is None else _ints(q_start, "q_start", B + 1, device), _ints(kv_len, "kv_len", B, device),
+        None if k_scale is None else _floats(k_scale, "k_scale", 1, device),
+        None if v_scale is None else _floats(v_scale, "v_scale", 1, device), p_qo, _raw_stream(stream, device))
+    if status:
+        _check(status)
     return q_out
 
 
-def _paged_queries(q, k_cache, v_cache, page_table, max_q, causal, scale, o_stride=None):
-    dtype, device = q.dtype, q.device
+def _paged_queries(q, k_cache, v_cache, page_table, max_q, causal, scale, out=None):
+    """(the two descriptors, sequences, page table's pointer)."""
+    dtype, device, shape = q.dtype, q.device, q.shape
     dt = _DTYPE16.get(dtype)
-    if dt is None:
-        raise W8Error(5, f"q: expected bfloat16 or float16, got {dtype}")
-    if q.dim() != 3:
-        raise W8Error(2, f"q: expected [tokens, heads, D], got {tuple(q.shape)}")
-    if not q.is_cuda:
+    if dt is None or len(shape) != 3 or not q.is_cuda:
+        if dt is None:
+            raise W8Error(5, f"q: expected bfloat16 or float16, got {dtype}")
+        if len(shape) != 3:
+            raise W8Error(2, f"q: expected [tokens, heads, D], got {tuple(shape)}")
         raise W8Error(1, "q: must be a CUDA tensor")
-    cache, B, _, D, p_table = _paged(dtype, device, k_cache, v_cache, page_table)
-    T, H = q.shape[0], q.shape[1]
-    sq = _rows(q, "q", (dtype,), device, T, H, D)
-    if max_q is None:
-        max_q = max(T, 1)
-    desc = _paged_attention_desc(T, H, max_q, *sq, *(o_stride or (H * D, D)), dt, bool(causal),
+    T, H, D = shape
+    cache, B, _, d, p_table = _paged(dtype, dt, device, k_cache, v_cache, page_table)
+    if d != D:
+        raise W8Error(2, f"q: heads of {D} dimensions, the cache's have {d}")
+    sq = _rows(q, "q", dtype, device, shape)
+    so = (H * D, D) if out is None else _rows(out, "out", out.dtype, device, shape)
+    desc = _paged_attention_desc(T, H, max(T, 1) if max_q is None else max_q, *sq, *so, dt, causal,
                                  D ** -0.5 if scale is None else scale)
     return desc, cache, B, p_table
 
@@ -1086,16 +1095,15 @@ def paged_attention(q, k_cache, v_cache, page_table, q_start, kv_len, max_q=None
     one sequence (default T; of a longer one the tokens from there on are left as they were, like those of no
     sequence).  ``scale`` defaults to D ** -0.5; ``k_scale`` and ``v_scale`` are
     those of E4M3 cells.  Returns [T, Hq, D] in q's dtype, or with ``s_out`` E4M3 codes."""
-    device, shape = q.device, q.shape
-    kinds = (q.dtype,) if s_out is None else _CODES
+    device = q.device
+    p_s = None
+    if s_out is not None:
+        p_s = _floats(s_out, "s_out", 1, device)
     if out is None:
-        out = _empty(shape, kinds[0], device, stream)
-    if len(shape) != 3 or out.shape != shape or out.dtype not in kinds or out.device != device:
-        _refuse_rows(out, "out", kinds, device, shape)
-    if out.stride(2) != 1 and shape[2] > 1:
-        _refuse_rows(out, "out", kinds, device, shape)
-    desc, cache, B, p_table = _paged_queries(q, k_cache, v_cache, page_table, max_q, causal, scale, out.stride()[:2])
-    p_start = None if q_start is None else _ints(q_start, "q_start", B + 1, device)
+        out = _empty(q.shape, q.dtype if s_out is None else torch.uint8, device, stream)
+    elif out.dtype is not q.dtype if s_out is None else out.dtype not in _CODES:
+        _refuse_rows(out, "out", (q.dtype,) if s_out is None else _CODES, device, q.shape)
+    desc, cache, B, p_table = _paged_queries(q, k_cache, v_cache, page_table, max_q, causal, scale, out)
     L = lib()
     p_ws, n_ws = None, 0
     if ws is None:
@@ -1106,10 +1114,14 @@ def paged_attention(q, k_cache, v_cache, page_table, q_start, kv_len, max_q=None
     if ws is not None:
         n_ws = ws.numel()
         p_ws = _floats(ws, "ws", n_ws, device)
-    _check(L.paged_attention(desc, cache, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), p_table, p_start,
-                             _ints(kv_len, "kv_len", B, device), _scale_ptr(k_scale, "k_scale", device),
-                             _scale_ptr(v_scale, "v_scale", device), _scale_ptr(s_out, "s_out", device), out.data_ptr(), p_ws,
-                             n_ws, _raw_stream(stream, device)))
+    status = L.paged_attention(
+        desc, cache, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), p_table,
+        None if q_start is None else _ints(q_start, "q_start", B + 1, device), _ints(kv_len, "kv_len", B, device),
+        None if k_scale is None else _floats(k_scale, "k_scale", 1, device),
+        None if v_scale is None else _floats(v_scale, "v_scale", 1, device), p_s, out.data_ptr(), p_ws, n_ws,
+        _raw_stream(stream, device))
+    if status:
+        _check(status)
     return out
 
 
