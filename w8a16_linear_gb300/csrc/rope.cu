@@ -31,7 +31,7 @@ namespace w8 {
 namespace {
 
 constexpr int kWarps = 4;          // of a block
-constexpr int kAhead = 2;          // chunks of heads that are loaded ahead
+constexpr int kAhead = 4;          // chunks of heads that are copied ahead
 
 struct RopeArgs {
   RopeProblem p;
@@ -40,11 +40,17 @@ struct RopeArgs {
   float inv_d;
 };
 
-// Four 16-bit values as two packed words.
-__device__ __forceinline__ uint2 ld8_once(const uint16_t* p) {
-  uint2 v;
-  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
-  return v;
+// Copies of 16 and 8 bytes to shared memory that the thread waits for by groups.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
 // kLanes: lanes of a head (a power of two), of eight dimensions each: 8 u .. 8 u + 7
@@ -67,11 +73,6 @@ __global__ void __launch_bounds__(32 * kWarps, 8) norm_rope_kernel(const __grid_
   const bool turned = 8 * sub < p.rot;
   const bool split_pairs = !kInterleaved && turned;
   const int d0 = split_pairs ? 4 * sub : 8 * sub, d1 = split_pairs ? (p.rot >> 1) + 4 * sub : 8 * sub + 4;
-  auto load = [&](const uint16_t* from) {
-    if (kInterleaved) return ld16_once(from + 8 * sub);
-    const uint2 lo = ld8_once(from + d0), hi = ld8_once(from + d1);
-    return make_uint4(lo.x, lo.y, hi.x, hi.y);
-  };
   // The token's heads, kHeads of a kind at a time: queries, keys and, into a cache, values.
   const int q_chunks = (p.Hq + kHeads - 1) / kHeads, k_chunks = (p.Hkv + kHeads - 1) / kHeads;
   const int chunks = q_chunks + k_chunks * (kPaged ? 2 : 1);
@@ -79,23 +80,30 @@ __global__ void __launch_bounds__(32 * kWarps, 8) norm_rope_kernel(const __grid_
   const uint16_t* k_at = static_cast<const uint16_t*>(p.k) + t * p.ks[0] + head0 * p.ks[1];
   const uint16_t* v_at = static_cast<const uint16_t*>(p.v) + t * p.vs[0] + head0 * p.vs[1];
   const int end = min(chunks, (part + 1) * a.per);
-  uint4 next[kAhead];
-  auto fetch = [&](int first) {
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int c = first + u, ck = c - q_chunks, cv = ck - k_chunks;
-      next[u] = make_uint4(0, 0, 0, 0);
-      if (!on || c >= end) continue;
-      if (c < q_chunks) {
-        if (c * kHeads + head0 < p.Hq) next[u] = load(q_at + c * kHeads * p.qs[1]);
-      } else if (ck < k_chunks) {
-        if (ck * kHeads + head0 < p.Hkv) next[u] = load(k_at + ck * kHeads * p.ks[1]);
-      } else if (kPaged && cv < k_chunks) {
-        if (cv * kHeads + head0 < p.Hkv) next[u] = load(v_at + cv * kHeads * p.vs[1]);
+  // A lane's own 16 bytes of each chunk that is under way.
+  __shared__ uint4 ring[kWarps][kAhead][32];
+  uint4* mine = &ring[threadIdx.x >> 5][0][lane];
+  auto fetch = [&](int c) {
+    const int ck = c - q_chunks, cv = ck - k_chunks;
+    const bool is_q = c < q_chunks, is_v = kPaged && cv >= 0;
+    const int h = (is_q ? c : is_v ? cv : ck) * kHeads;
+    if (c < end && on && h + head0 < (is_q ? p.Hq : p.Hkv)) {
+      const uint16_t* from = is_q ? q_at + h * p.qs[1] : is_v ? v_at + h * p.vs[1] : k_at + h * p.ks[1];
+      const uint32_t to = smem_u32(mine + (c % kAhead) * 32);
+      if (kInterleaved) {
+        copy16(to, from + d0);
+      } else {
+        copy8(to, from + d0);
+        copy8(to + 8, from + d1);
       }
     }
+    copy_commit();
   };
-  fetch(part * a.per);   // before the places and angles, which they do not need
+  // before the places and angles, which they do not need
+#pragma unroll 1
+  for (int k = 0; k < kAhead - 1; ++k) fetch(part * a.per + k);
+
+  auto leave = [] { copy_wait<0>(); };   // no copy may outlive its thread's block
 
   // Where the token stands: its sequence, its position there, and that one's page.
   int64_t pos = 0;
@@ -110,16 +118,16 @@ __global__ void __launch_bounds__(32 * kWarps, 8) norm_rope_kernel(const __grid_
       begin = __shfl_sync(0xFFFFFFFFu, start, b);
       end = __shfl_sync(0xFFFFFFFFu, start, min(b + 1, c.B));
       kv = __shfl_sync(0xFFFFFFFFu, len, min(b, c.B - 1));
-      if (b >= c.B || t < begin || t >= end) return;        // of no sequence
+      if (b >= c.B || t < begin || t >= end) return leave();   // of no sequence
     } else if (c.q_start) {
       int n = 0;   // sequences that begin at t or before it, the first aside
       for (int k = lane + 1; k <= c.B; k += 32) n += ld_i32(c.q_start + k) <= t;
       b = __reduce_add_sync(0xFFFFFFFFu, n);
-      if (b >= c.B) return;
+      if (b >= c.B) return leave();
       begin = ld_i32(c.q_start + b);
       end = ld_i32(c.q_start + b + 1);
       kv = ld_i32(c.kv_len + b);
-      if (t < begin || t >= end) return;
+      if (t < begin || t >= end) return leave();
     } else {
       const int per = (int)(p.M / c.B);
       b = (int)t / per;
@@ -161,85 +169,94 @@ __global__ void __launch_bounds__(32 * kWarps, 8) norm_rope_kernel(const __grid_
     }
   };
   uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
-  if (on && p.norm_q) wq = load(static_cast<const uint16_t*>(p.q_weight));
-  if (on && p.norm_k) wk = load(static_cast<const uint16_t*>(p.k_weight));
+  auto weight = [&](const void* w) {
+    const uint2 lo = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + d0));
+    const uint2 hi = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + d1));
+    return make_uint4(lo.x, lo.y, hi.x, hi.y);
+  };
+  if (on && p.norm_q) wq = weight(p.q_weight);
+  if (on && p.norm_k) wk = weight(p.k_weight);
 
-  for (int first = part * a.per; first < end; first += kAhead) {
-    uint4 x[kAhead];
+  float inv_ks = 1.0f, inv_vs = 1.0f;
+  if (kPaged && a.c.codes) {
+    inv_ks = __frcp_rn(ld_f32(a.c.k_scale));
+    inv_vs = __frcp_rn(ld_f32(a.c.v_scale));
+  }
+
+#pragma unroll 1
+  for (int c = part * a.per; c < end; ++c) {
+    fetch(c + kAhead - 1);   // to the place of the chunk before
+    copy_wait<kAhead - 1>();
+    // kinds and counts of a chunk are the same for the whole warp
+    const int ck = c - q_chunks, cv = ck - k_chunks;
+    const bool is_q = c < q_chunks, is_v = kPaged && cv >= 0;
+    const int h = (is_q ? c : is_v ? cv : ck) * kHeads + head0;
+    const bool there = on && h < (is_q ? p.Hq : p.Hkv);
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (there) x = mine[(c % kAhead) * 32];
+    const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+    uint32_t out[4] = {xw[0], xw[1], xw[2], xw[3]};
+    F2 v[4];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) x[u] = next[u];
-    fetch(first + kAhead);
+    for (int e = 0; e < 4; ++e) v[e] = unpack16<kF16>(xw[e]);
+    if (!is_v) {
+      if (is_q ? p.norm_q : p.norm_k) {
+        F2 s2 = mul2(v[0], v[0]);
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      // kinds and counts of a chunk are the same for the whole warp
-      const int c = first + u, ck = c - q_chunks, cv = ck - k_chunks;
-      if (c >= end) break;
-      const bool is_q = c < q_chunks, is_v = kPaged && cv >= 0;
-      const int h = (is_q ? c : is_v ? cv : ck) * kHeads + head0;
-      const bool there = on && h < (is_q ? p.Hq : p.Hkv);
-      const uint32_t xw[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-      uint32_t out[4] = {xw[0], xw[1], xw[2], xw[3]};
-      F2 v[4];
+        for (int e = 1; e < 4; ++e) s2 = fma2(v[e], v[e], s2);
+        float ss = __fadd_rn(s2.x, s2.y);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = unpack16<kF16>(xw[e]);
-      if (!is_v) {
-        if (is_q ? p.norm_q : p.norm_k) {
-          F2 s2 = mul2(v[0], v[0]);
+        for (int o = kLanes / 2; o >= 1; o /= 2) ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, o));
+        const F2 inv = splat(rsqrtf(fmaf(ss, a.inv_d, p.eps)));
+        const uint32_t ww[4] = {is_q ? wq.x : wk.x, is_q ? wq.y : wk.y, is_q ? wq.z : wk.z, is_q ? wq.w : wk.w};
 #pragma unroll
-          for (int e = 1; e < 4; ++e) s2 = fma2(v[e], v[e], s2);
-          float ss = __fadd_rn(s2.x, s2.y);
-#pragma unroll
-          for (int o = kLanes / 2; o >= 1; o /= 2) ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, o));
-          const F2 inv = splat(rsqrtf(fmaf(ss, a.inv_d, p.eps)));
-          const uint32_t ww[4] = {is_q ? wq.x : wk.x, is_q ? wq.y : wk.y, is_q ? wq.z : wk.z, is_q ? wq.w : wk.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = mul2(mul2(v[e], unpack16<kF16>(ww[e])), inv);
-        }
-        if (turned) {
-          if (kInterleaved) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              v[e] = fma2(v[e], splat(cs[e]), mul2(F2{v[e].y, v[e].x}, F2{-sn[e], sn[e]}));
-          } else {   // pairs of v[0], v[1] and v[2], v[3]
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const F2 c2 = F2{cs[2 * e], cs[2 * e + 1]}, s2 = F2{sn[2 * e], sn[2 * e + 1]};
-              const F2 lo = v[e], hi = v[e + 2];
-              v[e] = fma2(lo, c2, mul2(neg(hi), s2));
-              v[e + 2] = fma2(hi, c2, mul2(lo, s2));
-            }
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) out[e] = cvt16x2(kF16, v[e].x, v[e].y);
+        for (int e = 0; e < 4; ++e) v[e] = mul2(mul2(v[e], unpack16<kF16>(ww[e])), inv);
       }
-      if (!there) continue;
-      if (is_q) {
-        put(static_cast<uint16_t*>(p.q_out) + t * p.qos[0] + h * p.qos[1], out[0], out[1], out[2], out[3]);
-      } else if (!kPaged) {
-        put(static_cast<uint16_t*>(p.k_out) + t * p.kos[0] + h * p.kos[1], out[0], out[1], out[2], out[3]);
-      } else {
-        if (page < 0 || page >= a.c.pages) continue;        // a position without a page
-        const int64_t* cs3 = is_v ? a.c.vs : a.c.ks;
-        const int64_t at = page * cs3[0] + slot * cs3[1] + h * cs3[2];
-        void* cache = is_v ? a.c.v : a.c.k;
-        if (a.c.codes) {
-          const F2 f = splat(__frcp_rn(ld_f32(is_v ? a.c.v_scale : a.c.k_scale)));
-          uint32_t q[4];
+      if (turned) {
+        if (kInterleaved) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const F2 y = mul2(v[e], f);
-            q[e] = cvt_e4m3x2(y.x, y.y);
+          for (int e = 0; e < 4; ++e)
+            v[e] = fma2(v[e], splat(cs[e]), mul2(F2{v[e].y, v[e].x}, F2{-sn[e], sn[e]}));
+        } else {   // pairs of v[0], v[1] and v[2], v[3]
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const F2 c2 = F2{cs[2 * e], cs[2 * e + 1]}, s2 = F2{sn[2 * e], sn[2 * e + 1]};
+            const F2 lo = v[e], hi = v[e + 2];
+            v[e] = fma2(lo, c2, mul2(neg(hi), s2));
+            v[e + 2] = fma2(hi, c2, mul2(lo, s2));
           }
-          uint8_t* to = static_cast<uint8_t*>(cache) + at;
-          *reinterpret_cast<uint32_t*>(to + d0) = q[0] | (q[1] << 16);
-          *reinterpret_cast<uint32_t*>(to + d1) = q[2] | (q[3] << 16);
-        } else {
-          put(static_cast<uint16_t*>(cache) + at, out[0], out[1], out[2], out[3]);
         }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[e] = cvt16x2(kF16, v[e].x, v[e].y);
+    }
+    if (!there) continue;
+    if (is_q) {
+      put(static_cast<uint16_t*>(p.q_out) + t * p.qos[0] + h * p.qos[1], out[0], out[1], out[2], out[3]);
+    } else if (!kPaged) {
+      put(static_cast<uint16_t*>(p.k_out) + t * p.kos[0] + h * p.kos[1], out[0], out[1], out[2], out[3]);
+    } else {
+      if (page < 0 || page >= a.c.pages) continue;        // a position without a page
+      const int64_t* cs3 = is_v ? a.c.vs : a.c.ks;
+      const int64_t at = page * cs3[0] + slot * cs3[1] + h * cs3[2];
+      void* cache = is_v ? a.c.v : a.c.k;
+      if (a.c.codes) {
+        const F2 f = splat(is_v ? inv_vs : inv_ks);
+        uint32_t q[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const F2 y = mul2(v[e], f);
+          q[e] = cvt_e4m3x2(y.x, y.y);
+        }
+        uint8_t* to = static_cast<uint8_t*>(cache) + at;
+        *reinterpret_cast<uint32_t*>(to + d0) = q[0] | (q[1] << 16);
+        *reinterpret_cast<uint32_t*>(to + d1) = q[2] | (q[3] << 16);
+      } else {
+        put(static_cast<uint16_t*>(cache) + at, out[0], out[1], out[2], out[3]);
       }
     }
   }
+  copy_wait<0>();
 }
 
 template <bool kF16, int kLanes, bool kInterleaved>
