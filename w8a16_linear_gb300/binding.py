@@ -140,11 +140,12 @@ class W8Error(RuntimeError):
 
 
 _lib = None
+_marshal = None   # csrc/marshal.cpp, where it has been built
 
 
 def lib():
     """The loaded library; raises if it has not been built."""
-    global _lib
+    global _lib, _marshal
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise ImportError(f"{LIB_PATH} is missing: build it with "
@@ -155,6 +156,14 @@ def lib():
             f.restype = res
             f.argtypes = args
         _lib = l
+        if os.path.exists(os.path.join(_HERE, "_marshal.so")):
+            try:
+                from . import _marshal as m
+            except ImportError:   # of another PyTorch
+                return _lib
+            m.bind(*(ctypes.cast(getattr(l, n), ctypes.c_void_p).value for n in (
+                "qk_norm_rope", "paged_kv_append", "paged_attention", "paged_attention_workspace")))
+            _marshal = m
     return _lib
 
 
@@ -896,6 +905,10 @@ def _ints(t, name, n, device):
     return t.data_ptr()
 
 
+# The three calls below go by way of csrc/marshal.cpp where it takes the arguments as
+# they are; what follows in Python allocates outputs, takes other streams and
+# says what it refuses.
+
 def _rotation(turns, positions, axes, M, device):
     """(rot, axes' number and pairs, pointers of turns and positions, positions' pitch)."""
     if turns is None:
@@ -938,6 +951,12 @@ def qk_norm_rope(q, k, positions=None, turns=None, q_weight=None, k_weight=None,
     many pairs each of up to three axes rotates, ``positions`` is [axes, M].
     ``amplitude`` scales cosine and sine.  Returns ``(q_out, k_out)``, which may be
     ``q`` and ``k`` themselves."""
+    if _marshal is not None and stream is None:
+        status = _marshal.rope(q, k, positions, turns, q_weight, k_weight, eps, interleaved, axes, amplitude, q_out, k_out)
+        if status == 0:
+            return q_out, k_out
+        if status > 0:
+            _check(status)
     dtype, device = q.dtype, q.device
     dt = _DTYPE16.get(dtype)
     if dt is None or not q.is_cuda or q.dim() != 3:
@@ -1019,6 +1038,13 @@ def paged_kv_append(k, v, k_cache, v_cache, page_table, q_start, kv_len, turns=N
     multiples of 8 (E4M3 cells: 16) with contiguous D.  Positions without a page are not
     written, tokens of no sequence left out.  Returns ``q_out`` (None without ``q``),
     which may be ``q``."""
+    if _marshal is not None and stream is None:
+        status = _marshal.append(k, v, k_cache, v_cache, page_table, q_start, kv_len, turns, q, q_weight, k_weight, eps, interleaved,
+                                 positions, axes, amplitude, k_scale, v_scale, q_out)
+        if status == 0:
+            return q_out
+        if status > 0:
+            _check(status)
     dtype, device = k.dtype, k.device
     dt = _DTYPE16.get(dtype)
     if dt is None:
@@ -1095,6 +1121,13 @@ def paged_attention(q, k_cache, v_cache, page_table, q_start, kv_len, max_q=None
     one sequence (default T; of a longer one the tokens from there on are left as they were, like those of no
     sequence).  ``scale`` defaults to D ** -0.5; ``k_scale`` and ``v_scale`` are
     those of E4M3 cells.  Returns [T, Hq, D] in q's dtype, or with ``s_out`` E4M3 codes."""
+    if _marshal is not None and stream is None:
+        status = _marshal.attention(q, k_cache, v_cache, page_table, q_start, kv_len, max_q, causal, scale, k_scale, v_scale, s_out,
+                                    out, ws)
+        if status == 0:
+            return out
+        if status > 0:
+            _check(status)
     device = q.device
     p_s = None
     if s_out is not None:

@@ -20,6 +20,8 @@ LIB = os.path.join(HERE, "libw8lin.so")
 SOURCES = ["api.cu", "attention.cu", "elementwise.cu", "gemm.cu", "noalloc.cu", "paged_attention.cu", "paged_few.cu", "policy.cu",
            "rmsnorm.cu", "rope.cu"]
 
+MARSHAL = os.path.join(HERE, "_marshal.so")
+
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "-Xcompiler", "-fno-strict-aliasing", "--expt-relaxed-constexpr"]
@@ -53,11 +55,36 @@ def _compile(nvcc, src, obj, extra):
     return src, r.returncode, r.stdout + r.stderr
 
 
+def _marshal():
+    """Compile the CPython module of csrc/marshal.cpp; returns what the compiler
+    said where it failed (the binding then marshals in Python)."""
+    src = os.path.join(CSRC, "marshal.cpp")
+    if not _stale(MARSHAL, [src, os.path.join(ROOT, "include", "w8lin.h"), os.path.abspath(__file__)]):
+        return ""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    tmp = f"{MARSHAL}.{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += [f"-I{p}" for p in [*include_paths(), sysconfig.get_paths()["include"], cuda]]
+    cmd += [src, "-o", tmp, f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{libs}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode == 0:
+        os.replace(tmp, MARSHAL)
+        return ""
+    return r.stdout + r.stderr
+
+
 def build(verbose=False, extra_flags=()):
     """Compile and link; returns the path of the shared library."""
     nvcc = _nvcc()
     os.makedirs(OUT_DIR, exist_ok=True)
     hdrs = _headers()
+    pool = cf.ThreadPoolExecutor(max_workers=1)
+    marshal = pool.submit(_marshal)
     jobs = []
     objs = []
     for s in SOURCES:
@@ -80,6 +107,10 @@ def build(verbose=False, extra_flags=()):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}{r.stderr}")
+    failed = marshal.result()
+    pool.shutdown()
+    if failed:
+        print(f"csrc/marshal.cpp was not built; calls are marshalled in Python:\n{failed[-2000:]}", file=sys.stderr)
     return LIB
 
 
