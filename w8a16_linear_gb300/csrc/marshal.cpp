@@ -165,6 +165,16 @@ void paged(Call& c, w8_paged_desc& d, PyObject* k_cache, PyObject* v_cache, PyOb
   *p_table = static_cast<const int32_t*>(t->data_ptr());
 }
 
+// The library's call, which may wait for room in the launch queue, without the interpreter's lock.
+template <typename F>
+PyObject* status_of(F&& call) {
+  int status;
+  Py_BEGIN_ALLOW_THREADS
+  status = (int)call();
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(status);
+}
+
 PyObject* left() { return PyLong_FromLong(-1); }   // to the binding's Python
 
 // (q, k, positions, turns, q_weight, k_weight, eps, interleaved, axes, amplitude, q_out, k_out)
@@ -200,7 +210,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) try {
   d.amplitude = c.number(a[9]);
   void* stream = c.stream();
   if (!c.ok) return left();
-  return PyLong_FromLong(g_rope(&d, p_q, p_k, p_pos, p_turns, p_wq, p_wk, p_qo, p_ko, stream));
+  return status_of([&] { return g_rope(&d, p_q, p_k, p_pos, p_turns, p_wq, p_wk, p_qo, p_ko, stream); });
 } catch (...) {
   return left();
 }
@@ -245,8 +255,8 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) try {
   d.amplitude = c.number(a[15]);
   void* stream = c.stream();
   if (!c.ok || a[6] == Py_None) return left();
-  return PyLong_FromLong(g_append(&d, &p, p_q, p_k, p_v, p_pos, p_turns, p_wq, p_wk, p_kc, p_vc, p_table, p_start, p_len, p_ks,
-                                  p_vs, p_qo, stream));
+  return status_of([&] { return g_append(&d, &p, p_q, p_k, p_v, p_pos, p_turns, p_wq, p_wk, p_kc, p_vc, p_table, p_start, p_len, p_ks,
+                                  p_vs, p_qo, stream); });
 } catch (...) {
   return left();
 }
@@ -291,8 +301,8 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) try {
     int64_t need = 0;
     if (g_workspace(&d, &p, &need) != W8_OK || need > 0) return left();
   }
-  return PyLong_FromLong(g_attention(&d, &p, p_q, p_kc, p_vc, p_table, p_start, p_len, p_ks, p_vs, p_so, p_out, p_ws, floats,
-                                     stream));
+  return status_of([&] { return g_attention(&d, &p, p_q, p_kc, p_vc, p_table, p_start, p_len, p_ks, p_vs, p_so, p_out, p_ws, floats,
+                                     stream); });
 } catch (...) {
   return left();
 }

@@ -1,7 +1,8 @@
 """One transformer block's linear sites on one denoising step, in the
 precision the step policy picks: the call sequence of the step-scheduled
-stack, over the C ABI; and the site where a block attends to an encoder's
-states (CrossSite, at the end).
+stack, over the C ABI; the site where a block attends to an encoder's states
+(CrossSite); and the site where it attends to its own past in a paged cache
+(SelfSite, at the end).
 
 This module only orders calls, owns the buffers they write and the streams
 they overlap on; every value is computed by the library's kernels.
@@ -30,7 +31,7 @@ CrossSite makes them once and keeps them.
 """
 
 from dataclasses import dataclass
-from typing import List, Tuple
+from typing import List, Optional, Tuple
 
 import torch
 
@@ -207,3 +208,72 @@ class CrossSite:
         W.cross_attention(q, self.k, self.v, kv_len=kv_len, kv_mask=kv_mask, s_out=w.s_attn, out=self.attn, ws=self.ws)
         W.fp8_linear_w8a8(self.attn.view(self.B * self.L, -1), w.out[0], w.s_attn, w.out[1], out=self.y)
         return self.y, self.res
+
+
+@dataclass
+class SelfWeights:
+    """A self-attention site's norms (bfloat16; ``norm`` [H], of the queries' and keys' heads
+    [D] or None), E4M3 weights ``[N, K]`` with one float32 scale for each output channel,
+    the out-projection's weight with its own scale and static input scale, what a
+    position adds to the phase of each pair (rope_turns), and of a cache of E4M3 codes its scales."""
+    norm: torch.Tensor
+    q: Tuple[torch.Tensor, torch.Tensor]              # [heads * D, H], [heads * D]
+    k: Tuple[torch.Tensor, torch.Tensor]              # [kv_heads * D, H], [kv_heads * D]
+    v: Tuple[torch.Tensor, torch.Tensor]
+    out: Tuple[torch.Tensor, torch.Tensor]            # [H, heads * D], one scale
+    s_attn: torch.Tensor                              # input scale of the out-projection
+    turns: torch.Tensor                               # [rot / 2]
+    q_norm: Optional[torch.Tensor] = None
+    k_norm: Optional[torch.Tensor] = None
+    k_scale: Optional[torch.Tensor] = None
+    v_scale: Optional[torch.Tensor] = None
+
+
+class SelfSite:
+    """The site where a block's new tokens attend to their sequences' past: the
+    residual's addition and norm to E4M3 with a scale for each token, the three
+    projections on those codes, the heads' norms and rotation with the keys and
+    values on their way into a paged cache, softmax attention over that cache, written
+    as E4M3 codes, and the out-projection on them.
+
+    Made for at most ``tokens`` new tokens of ``batch`` sequences, at most ``max_q`` of
+    one, in a cache ``k_cache``, ``v_cache`` [pages, page_size, kv_heads, D] and a page
+    table of ``columns`` entries for each sequence.  All buffers are the site's own, so
+    that a pass of as many tokens can be captured in a CUDA graph; the lengths,
+    starts and pages are read when it runs, so the graph serves every step, and the
+    site has to live as long as it."""
+
+    def __init__(self, batch, tokens, max_q, hidden, heads, kv_heads, head_dim, k_cache, v_cache, columns, interleaved=False):
+        device = k_cache.device
+        self.heads, self.kv_heads, self.D, self.max_q = heads, kv_heads, head_dim, max_q
+        self.k_cache, self.v_cache, self.interleaved = k_cache, v_cache, interleaved
+        bf = dict(dtype=torch.bfloat16, device=device)
+        u8 = dict(dtype=torch.uint8, device=device)
+        self.codes = torch.empty((tokens, hidden), **u8)
+        self.s_tok = torch.empty((tokens,), dtype=torch.float32, device=device)
+        self.res = torch.empty((tokens, hidden), **bf)
+        self.q, self.k, self.v = (torch.empty((tokens, n, head_dim), **bf) for n in (heads, kv_heads, kv_heads))
+        self.attn = torch.empty((tokens, heads, head_dim), **u8)
+        self.y = torch.empty((tokens, hidden), **bf)
+        self.table = (batch, columns)
+        self.ws = {}                                  # tokens of a pass -> workspace
+
+    def run(self, W, w, x, residual, page_table, q_start, kv_len):
+        """One pass over the tokens ``x`` [T, hidden] on the current stream: returns the
+        out-projection's output and the sum of ``x`` and ``residual``, [T, hidden].
+        ``kv_len`` counts the new tokens."""
+        T = x.shape[0]
+        codes, s_tok, res, q, k, v, attn, y = (t[:T] for t in (self.codes, self.s_tok, self.res, self.q, self.k, self.v, self.attn,
+                                                               self.y))
+        if T not in self.ws:
+            shape = torch.empty(self.table, dtype=torch.int32, device=x.device)
+            self.ws[T] = W.paged_attention_workspace(q, self.k_cache, shape, max_q=self.max_q)
+        W.add_rms_norm_quant(x, residual, w.norm, out=codes, s_tok=s_tok, res_out=res)
+        W.fp8_linear_w8a8_pertoken_group(codes, s_tok, [w.q[0], w.k[0], w.v[0]], [w.q[1], w.k[1], w.v[1]],
+                                         outs=[t.view(T, -1) for t in (q, k, v)])
+        W.paged_kv_append(k, v, self.k_cache, self.v_cache, page_table, q_start, kv_len, turns=w.turns, q=q, q_weight=w.q_norm,
+                          k_weight=w.k_norm, interleaved=self.interleaved, k_scale=w.k_scale, v_scale=w.v_scale, q_out=q)
+        W.paged_attention(q, self.k_cache, self.v_cache, page_table, q_start, kv_len, max_q=self.max_q, k_scale=w.k_scale,
+                          v_scale=w.v_scale, s_out=w.s_attn, out=attn, ws=self.ws[T])
+        W.fp8_linear_w8a8(attn.view(T, -1), w.out[0], w.s_attn, w.out[1], out=y)
+        return y, res
