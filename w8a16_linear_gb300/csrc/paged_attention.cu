@@ -83,6 +83,18 @@ struct Cfg {
   static_assert(kAlloc <= 232448, "shared memory budget");
 };
 
+// With 128 rows a sequence is one unit of a key head.
+template <bool kShared>
+struct UnitsKind {
+  using type = Units;
+};
+template <>
+struct UnitsKind<false> {
+  using type = WholeUnits;
+};
+template <bool kShared>
+using UnitsOf = typename UnitsKind<kShared>::type;
+
 // kShared: both slots work on the same key tiles (256 query rows); otherwise
 // they take the even and odd tiles of the same 128 rows.
 template <int DP, bool kF16, bool kCodes, bool kShared>
@@ -170,16 +182,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_proxy_async_smem();
   }
   griddep_wait();   // from here on what earlier kernels wrote may be read
-  if (seqs) {
-    for (int b = threadIdx.x; b < a.B; b += kThreads) seqs[b] = load_seq(a, b);
-    if (a.may_cut) {
-      __syncthreads();
-      share_out(a, seqs, tiles, reinterpret_cast<uint32_t*>(smem + C::kFirst), state, kShared ? kCutShared : kCutSplit);
+  uint32_t* tiles_first = reinterpret_cast<uint32_t*>(smem + C::kFirst);
+  if constexpr (kShared) {
+    if (seqs) {
+      for (int b = threadIdx.x; b < a.B; b += kThreads) seqs[b] = load_seq(a, b);
+      if (a.may_cut) {
+        __syncthreads();
+        share_out(a, seqs, tiles, tiles_first, state, kCutShared);
+      }
     }
+  } else if (warp == 0 && seqs) {
+    share_out_whole(a, seqs, tiles, tiles_first, state, kCutSplit);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // The next kernel (the joining one) may start its prologue.  Not with 256 rows: what is launched
+  // early there costs 3 to 5% (chunks 911 -> 936 us, prompts 75 -> 79).
+  if (!kShared) griddep_launch_dependents();
   const uint32_t tmem = *tmem_slot;
   const auto s_col = [&](int i) { return tmem + (uint32_t)(i * kKeys); };
   const auto o_col = [&](int i) { return tmem + 256u + (uint32_t)(i * DP); };
@@ -238,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       return true;
     };
-    Units units(a, seqs, tiles, state);
+    UnitsOf<kShared> units(a, seqs, tiles, state);
     Item x;
     while (ok && units.next(x)) {
       if (x.n() == 0) continue;
@@ -332,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         return st;
       };
-      Units units(a, seqs, tiles, state);
+      UnitsOf<kShared> units(a, seqs, tiles, state);
       Item x;
       while (ok && units.next(x)) {
         const int n = x.n();
@@ -391,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (!kCodes) {
       uint32_t seen_tiles[2] = {0, 0};
       bool ok = true;
-      Units units(a, seqs, tiles, state);
+      UnitsOf<kShared> units(a, seqs, tiles, state);
       Item x;
       while (ok && units.next(x)) {
         ok = walk(x, [&](bool is_v, int ring, int tile) {
@@ -423,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (kCodes) scale_log2 *= ld_f32(a.k_scale);
     uint32_t scount = 0, icount = 0;
     bool ok = true;
-    Units units(a, seqs, tiles, state);
+    UnitsOf<kShared> units(a, seqs, tiles, state);
     Item x;
     while (ok && units.next(x)) {
       const int n = slot_tiles(x.n(), i);
@@ -702,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < (kShared ? 2 : 1); ++i) put_zeros(out_row(x, i * a.rows_l + pos));
         }
     }
-    Units units(a, seqs, tiles, state);
+    UnitsOf<kShared> units(a, seqs, tiles, state);
     Item x;
     while (ok && units.next(x)) {
       kind = x.part < 0 ? out_kind : 2;
@@ -871,6 +891,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // order in which the parts were written (and have been left in L2).
 template <int DP, bool kF16>
 __global__ void __launch_bounds__(256) paged_join_kernel(const PagedArgs a, int unit_rows) {
+  griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
   constexpr int kChunks = DP / 16;

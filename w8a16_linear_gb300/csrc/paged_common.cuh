@@ -411,6 +411,141 @@ __device__ __forceinline__ void share_out(const PagedArgs& a, const Seq* seqs, u
   }
 }
 
+// A CTA's units, in the order in which each of its roles goes through them: as
+// Units has them, where a sequence is one unit of each key head.
+struct WholeUnits {
+  const PagedArgs& a;
+  const Seq* seqs;            // in shared memory, or null
+  const uint32_t* tiles;
+  uint32_t cur, end, step;    // the next item, or cut: the next tile and the share's end
+  int b, hk, t;               // cut: where that tile is
+  int part;
+  bool cut;
+
+  __device__ __forceinline__ WholeUnits(const PagedArgs& args, const Seq* s, const uint32_t* tl, const volatile int* st)
+      : a(args), seqs(s), tiles(tl) {
+    cut = a.may_cut && st[kShares] > 0;
+    part = 2 * blockIdx.x;
+    cur = cut ? (uint32_t)st[kBegin] : blockIdx.x;
+    end = cut ? (uint32_t)st[kEnd] : (uint32_t)a.items;
+    if (cut) b = st[kAtB], hk = st[kAtHk], t = st[kAtTile];
+  }
+  __device__ __forceinline__ bool next(Item& x) {
+    Seq s;
+    do {
+      if (cur >= end) return false;
+      if (!cut) {
+        b = quotient((int)cur, a.by_hkv);
+        hk = (int)cur - b * a.Hkv;
+        cur += gridDim.x;
+      }
+      s = seqs ? seqs[b] : load_seq(a, b);
+    } while (s.tokens == 0);   // where units are cut it is one with tiles
+    x.b = b;
+    x.hk = hk;
+    x.left = s.tokens;
+    x.row0 = s.row0;
+    x.pos0 = s.base;
+    x.len = s.len;
+    x.limit = seen(a, s.base, s.len, s.tokens);
+    x.lim0 = seen(a, s.base, s.len, 1);
+    x.t0 = 0;
+    x.t1 = (x.limit + kKeys - 1) / kKeys;
+    x.part = -1;
+    if (cut) {
+      const int all = x.t1;
+      x.t0 = t;
+      x.t1 = (int)min((uint32_t)all, (uint32_t)t + (end - cur));
+      if (x.n() < all) x.part = part;
+      part = 2 * blockIdx.x + 1;
+      cur += (uint32_t)x.n();
+      t = x.t1;
+      if (t == all) {
+        t = 0;
+        if (++hk == a.Hkv) {
+          hk = 0;
+          while (++b < a.B - 1 && tiles[b] == 0) {
+          }
+        }
+      }
+    }
+    return true;
+  }
+};
+
+// The sequences to shared memory and, where units may be cut, how the work is
+// shared out (see share_out): by one warp, since a sequence is one unit of a key head.
+__device__ __forceinline__ void share_out_whole(const PagedArgs& a, Seq* seqs, uint32_t* tiles, uint32_t* first, int* state,
+                                                const Cutting cost) {
+  const int lane = threadIdx.x & 31;
+  uint32_t total = 0, units = 0, longest = 0, zeros = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int b = b0 + lane;
+    uint32_t mine = 0;
+    if (b < a.B) {
+      const Seq s = load_seq(a, b);
+      seqs[b] = s;
+      if (s.tokens > 0) {
+        mine = (uint32_t)(seen(a, s.base, s.len, s.tokens) + kKeys - 1) / kKeys;
+        ++units;
+        zeros |= mine == 0;
+      }
+      tiles[b] = mine;
+    }
+    if (!a.may_cut) continue;
+    longest = max(longest, mine);
+    mine *= (uint32_t)a.Hkv;
+    uint32_t to = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, to, o);
+      if (lane >= o) to += v;
+    }
+    if (b < a.B) first[b] = total + to - mine;
+    total += __shfl_sync(0xFFFFFFFFu, to, 31);
+  }
+  if (!a.may_cut) return;
+  __syncwarp();
+  units = __reduce_add_sync(0xFFFFFFFFu, units) * (uint32_t)a.Hkv;
+  longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+  zeros = __reduce_or_sync(0xFFFFFFFFu, zeros);
+  const uint32_t ctas = gridDim.x;
+  const uint32_t share = max((total + ctas - 1) / ctas, (uint32_t)cost.least);
+  const float even = (float)total / (float)ctas;
+  const float whole = units <= ctas ? (float)longest : fmaxf((float)longest, even + 0.5f * (float)longest);
+  const bool cut = cost.slope * (float)share + cost.plus < whole;
+  const uint32_t shares = cut ? (total + share - 1) / share : 0;
+  if (lane == 0) {
+    a.info[blockIdx.x * kInfo] = (int)shares;
+    state[kShares] = (int)shares;
+    state[kZeros] = (int)zeros;
+  }
+  if (blockIdx.x >= shares) {
+    if (lane == 0) state[kBegin] = state[kEnd] = (int)total;
+    return;
+  }
+  const uint32_t p = share_begin(total, blockIdx.x, shares);
+  int n = 0;                                 // sequences that begin at tile p or before it, the first aside
+  for (int k = lane + 1; k < a.B; k += 32) n += first[k] <= p;
+  const int b = __reduce_add_sync(0xFFFFFFFFu, n);
+  if (lane != 0) return;
+  const Seq s = seqs[b];
+  const uint32_t at = p - first[b], hk = at / tiles[b], t = at - hk * tiles[b];
+  state[kBegin] = (int)p;
+  state[kEnd] = (int)share_begin(total, blockIdx.x + 1, shares);
+  state[kAtB] = b;
+  state[kAtHk] = (int)hk;
+  state[kAtBlk] = 0;
+  state[kAtTile] = (int)t;
+  int* info = a.info + blockIdx.x * kInfo;
+  info[1] = (int)t;
+  info[2] = (int)tiles[b];
+  info[3] = (int)hk;
+  info[4] = s.row0;
+  info[5] = s.tokens;
+  info[6] = (int)total;
+}
+
 // Reads and clears this translation unit's error word.
 namespace {
 inline cudaError_t read_paged_error(cudaStream_t st, uint32_t* err) {
