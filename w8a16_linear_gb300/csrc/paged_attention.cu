@@ -71,7 +71,8 @@ struct Cfg {
   static constexpr int kSeq = kSum + 4 * kRows * 4;      // row0, tokens, base, len of each sequence
   static constexpr int kTiles = kSeq + kMaxSeqs * 16;    // tiles of one key head's units
   static constexpr int kFirst = kTiles + kMaxSeqs * 4;   // where they begin in the row of all tiles
-  static constexpr int kState = kFirst + (kMaxSeqs + 4) * 4;
+  static constexpr int kOrder = kFirst + (kMaxSeqs + 4) * 4;   // sequences by their units
+  static constexpr int kState = kOrder + kMaxSeqs * 2;
   static constexpr int kBar = kState + 16 * 4;
   // full[S], empty[S], clean[S], raw_full[R], raw_empty[R], q_full[2], q_empty[2], s_full[2], p_full[2],
   // o_full[2], l_full[2], o_free[2], p_half[2], drain[2]
@@ -134,6 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Seq* seqs = a.B <= kMaxSeqs ? reinterpret_cast<Seq*>(smem + C::kSeq) : nullptr;
   uint32_t* tiles = reinterpret_cast<uint32_t*>(smem + C::kTiles);
   int* state = reinterpret_cast<int*>(smem + C::kState);
+  uint16_t* order = reinterpret_cast<uint16_t*>(smem + C::kOrder);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -186,10 +188,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (kShared) {
     if (seqs) {
       for (int b = threadIdx.x; b < a.B; b += kThreads) seqs[b] = load_seq(a, b);
-      if (a.may_cut) {
-        __syncthreads();
-        share_out(a, seqs, tiles, tiles_first, state, kCutShared);
-      }
+      __syncthreads();
+      order_units(a, seqs, order);
+      if (a.may_cut) share_out(a, seqs, tiles, tiles_first, state, kCutShared);
     }
   } else if (warp == 0 && seqs) {
     share_out_whole(a, seqs, tiles, tiles_first, state, kCutSplit);
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       return true;
     };
-    UnitsOf<kShared> units(a, seqs, tiles, state);
+    UnitsOf<kShared> units(a, seqs, tiles, state, order);
     Item x;
     while (ok && units.next(x)) {
       if (x.n() == 0) continue;
@@ -352,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         return st;
       };
-      UnitsOf<kShared> units(a, seqs, tiles, state);
+      UnitsOf<kShared> units(a, seqs, tiles, state, order);
       Item x;
       while (ok && units.next(x)) {
         const int n = x.n();
@@ -411,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (!kCodes) {
       uint32_t seen_tiles[2] = {0, 0};
       bool ok = true;
-      UnitsOf<kShared> units(a, seqs, tiles, state);
+      UnitsOf<kShared> units(a, seqs, tiles, state, order);
       Item x;
       while (ok && units.next(x)) {
         ok = walk(x, [&](bool is_v, int ring, int tile) {
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!pass && !mbar_wait_lanes(full_bar(st), phase_of(e), abort)) return false;
           const int key0 = tile * kKeys;
           if (is_v && key0 + kKeys > x.lim0) {
-            if (clear_rows<kF16, false, C::kAtoms>(smem + C::kRing + st * C::kTile, lane, x.lim0 - key0, x.limit - key0)) *dirty = 1;
+            if (clear_rows<kF16, false, C::kAtoms>(smem + C::kRing + st * C::kTile, lane, x.lim0 - key0, x.limit - key0, a.box)) *dirty = 1;
             fence_proxy_async_smem();
             __syncwarp();
           }
@@ -443,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (kCodes) scale_log2 *= ld_f32(a.k_scale);
     uint32_t scount = 0, icount = 0;
     bool ok = true;
-    UnitsOf<kShared> units(a, seqs, tiles, state);
+    UnitsOf<kShared> units(a, seqs, tiles, state, order);
     Item x;
     while (ok && units.next(x)) {
       const int n = slot_tiles(x.n(), i);
@@ -722,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < (kShared ? 2 : 1); ++i) put_zeros(out_row(x, i * a.rows_l + pos));
         }
     }
-    UnitsOf<kShared> units(a, seqs, tiles, state);
+    UnitsOf<kShared> units(a, seqs, tiles, state, order);
     Item x;
     while (ok && units.next(x)) {
       kind = x.part < 0 ? out_kind : 2;

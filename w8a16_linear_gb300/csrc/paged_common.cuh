@@ -99,26 +99,50 @@ __device__ __forceinline__ int seen(const PagedArgs& a, int base, int len, int e
   return a.causal ? min(max(base + end, 0), len) : len;
 }
 
+// The sequences in the order of their numbers of units, the most first (all threads).
+__device__ __forceinline__ void order_units(const PagedArgs& a, const Seq* seqs, uint16_t* order) {
+  for (int b = threadIdx.x; b < a.B; b += kThreads) {
+    const int mine = (seqs[b].tokens + a.per - 1) / a.per;
+    int before = 0;
+    for (int k = 0; k < a.B; ++k) {
+      const int n = (seqs[k].tokens + a.per - 1) / a.per;
+      before += n > mine || (n == mine && k < b);
+    }
+    order[before] = (uint16_t)b;
+  }
+}
+
 // A CTA's units, in the order in which each of its roles goes through them.
+//
+// Whole units: block by block from the last (the longest, where causal), of the
+// sequences that have it, and dealt out to the CTAs to and fro.  (Counted over all blocks
+// of all sequences instead, prompts of 539 to 1077 tokens gave one CTA 30 tiles
+// where 18 are the average.)
 struct Units {
   const PagedArgs& a;
   const Seq* seqs;            // in shared memory, or null
   const uint32_t* tiles;
-  const volatile int* state;
-  uint32_t cur, end;          // the next item, or cut: the next tile and the share's end
-  int b, hk, blk, t;          // cut: where that tile is
+  const uint16_t* order;
+  uint32_t cur, end;          // cut: the next tile and the share's end
+  int b, hk, blk, t;          // cut: where that tile is; whole: the block
   uint32_t begin;
+  int count;                  // whole: sequences that have the block
+  int at, turn;               // the next unit among theirs; whether the last round went back
   bool cut;
 
-  __device__ __forceinline__ Units(const PagedArgs& args, const Seq* s, const uint32_t* tl, const volatile int* st)
-      : a(args), seqs(s), tiles(tl), state(st) {
-    cut = a.may_cut && state[kShares] > 0;
+  __device__ __forceinline__ Units(const PagedArgs& args, const Seq* s, const uint32_t* tl, const volatile int* st,
+                                   const uint16_t* ord)
+      : a(args), seqs(s), tiles(tl), order(ord) {
+    cut = a.may_cut && st[kShares] > 0;
     if (cut) {
-      begin = cur = (uint32_t)state[kBegin];
-      end = (uint32_t)state[kEnd];
-      b = state[kAtB], hk = state[kAtHk], blk = state[kAtBlk], t = state[kAtTile];
+      begin = cur = (uint32_t)st[kBegin];
+      end = (uint32_t)st[kEnd];
+      b = st[kAtB], hk = st[kAtHk], blk = st[kAtBlk], t = st[kAtTile];
     } else {
-      cur = blockIdx.x;
+      blk = a.blocks - 1;
+      count = seqs ? 0 : a.B;
+      at = (int)blockIdx.x;
+      turn = 0;
     }
   }
   // The unit of block `at`; false where the sequence has no such tokens.
@@ -139,12 +163,19 @@ struct Units {
   __device__ __forceinline__ bool next(Item& x) {
     x.part = -1;
     if (!cut) {
-      while (cur < (uint32_t)a.items) {
-        const int q = quotient((int)cur, a.by_bh), r = (int)cur - q * (a.B * a.Hkv);
-        x.b = quotient(r, a.by_hkv);
-        x.hk = r - x.b * a.Hkv;
-        cur += gridDim.x;
-        if (fill(x, a.blocks - 1 - q)) return true;   // the longest first
+      for (; blk >= 0; --blk) {
+        while (seqs && count < a.B && seqs[order[count]].tokens > blk * a.per) ++count;
+        const int n = count * a.Hkv;
+        if (at >= n) {
+          at -= n;
+          continue;
+        }
+        const int k = quotient(at, a.by_hkv);
+        x.b = seqs ? order[k] : k;
+        x.hk = at - k * a.Hkv;
+        at += turn ? 1 + 2 * (int)blockIdx.x : 2 * ((int)gridDim.x - (int)blockIdx.x) - 1;
+        turn ^= 1;
+        if (fill(x, blk)) return true;
       }
       return false;
     }
@@ -213,11 +244,12 @@ __device__ __forceinline__ uint32_t finite(uint32_t w) {
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
 // V rows of a tile in shared memory that not every row of a unit sees (one warp;
-// eight lanes to a row's 128 bytes): rows `to` and on, which none sees, are cleared;
-// of rows from .. to - 1 the values that are not finite.  Whether this lane met one of
+// eight lanes to a row's 128 bytes): rows `to` and on, which none sees, are cleared up to
+// the end of their copy of `box` rows (the copies behind it wrote zeros); of rows from .. to - 1 the
+// values that are not finite.  Whether this lane met one of
 // those.  It stands between the tile's copy and its product: 16 rows' loads are under way at a time.
 template <bool kF16, bool kCells8, int kAtoms>
-__device__ __forceinline__ bool clear_rows(uint8_t* tile, int lane, int from, int to) {
+__device__ __forceinline__ bool clear_rows(uint8_t* tile, int lane, int from, int to, int box) {
   const auto bad_of = [](const uint4& w) {
     return kCells8 ? nan_codes(w.x) | nan_codes(w.y) | nan_codes(w.z) | nan_codes(w.w)
                    : not_finite<kF16>(w.x) | not_finite<kF16>(w.y) | not_finite<kF16>(w.z) | not_finite<kF16>(w.w);
@@ -257,7 +289,7 @@ __device__ __forceinline__ bool clear_rows(uint8_t* tile, int lane, int from, in
     }
   }
 #pragma unroll 2
-  for (int r = max(to, 0) + sub; r < kKeys; r += 4)
+  for (int r = max(to, 0) + sub; r < min((max(to, 0) + box - 1) & -box, kKeys); r += 4)
 #pragma unroll
     for (int at = 0; at < kAtoms; ++at) *reinterpret_cast<uint4*>(v + at * kAtom + r * 128) = make_uint4(0, 0, 0, 0);
   return bad;
@@ -422,7 +454,8 @@ struct WholeUnits {
   int part;
   bool cut;
 
-  __device__ __forceinline__ WholeUnits(const PagedArgs& args, const Seq* s, const uint32_t* tl, const volatile int* st)
+  __device__ __forceinline__ WholeUnits(const PagedArgs& args, const Seq* s, const uint32_t* tl, const volatile int* st,
+                                        const uint16_t* = nullptr)
       : a(args), seqs(s), tiles(tl) {
     cut = a.may_cut && st[kShares] > 0;
     part = 2 * blockIdx.x;

@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         ok = mbar_wait_lanes(full_bar(st), stage_phase(true, e), abort);
         if (!ok) break;
         if ((kCodes || (k & 1)) && key0 + kKeys > x.lim0) {
-          if (clear_rows<kF16, kCodes, C::kAtoms>(smem + C::kRing + st * C::kTile, lane, x.lim0 - key0, x.limit - key0)) *dirty = 1;
+          if (clear_rows<kF16, kCodes, C::kAtoms>(smem + C::kRing + st * C::kTile, lane, x.lim0 - key0, x.limit - key0, a.box)) *dirty = 1;
           fence_proxy_async_smem();
           __syncwarp();
         }
