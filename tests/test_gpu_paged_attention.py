@@ -218,6 +218,19 @@ def test_nothing_is_written_behind_the_workspace(W, new, lens, H, Hk, D):
         assert e.value.status == 2
 
 
+@pytest.mark.parametrize("B", [256, 257, 300])
+@pytest.mark.parametrize("most,H,Hk,D", [(1, 8, 2, 64), (3, 10, 1, 64), (40, 10, 2, 128), (300, 2, 2, 64)])
+@pytest.mark.parametrize("codes", [False, True])
+def test_many_sequences_of_all_lengths(W, B, most, H, Hk, D, codes):
+    """About as many as are kept in shared memory: some without a token, some without a past."""
+    new = [most * (7 * i % 11) // 10 for i in range(B)]
+    lens = [n + (37 * i % 101) * (i % 3) for i, n in enumerate(new)]
+    b = batch(new, lens, 16, Hk, D, codes=codes)
+    q = queries(b, H, D)
+    for causal in (True, False):
+        check(call(W, b, q, causal=causal, max_q=most), *exact_attention(b, q, causal))
+
+
 @pytest.mark.parametrize("new,lens", [([1] * 4, [3000, 50, 2000, 1]), ([300, 40], [3000, 100])])
 @pytest.mark.parametrize("codes", [False, True])
 def test_equal_calls_give_equal_bits(W, new, lens, codes):

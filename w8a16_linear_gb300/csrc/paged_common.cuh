@@ -163,11 +163,12 @@ struct Units {
   __device__ __forceinline__ bool next(Item& x) {
     x.part = -1;
     if (!cut) {
-      for (; blk >= 0; --blk) {
+      while (blk >= 0) {
         while (seqs && count < a.B && seqs[order[count]].tokens > blk * a.per) ++count;
         const int n = count * a.Hkv;
         if (at >= n) {
           at -= n;
+          --blk;
           continue;
         }
         const int k = quotient(at, a.by_hkv);
@@ -175,7 +176,7 @@ struct Units {
         x.hk = at - k * a.Hkv;
         at += turn ? 1 + 2 * (int)blockIdx.x : 2 * ((int)gridDim.x - (int)blockIdx.x) - 1;
         turn ^= 1;
-        if (fill(x, blk)) return true;
+        if (fill(x, blk)) return true;   // without a table of sequences one may lack the block
       }
       return false;
     }
