@@ -22,6 +22,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -31,7 +32,8 @@ namespace w8 {
 namespace {
 
 constexpr int kWarps = 4;          // of a block
-constexpr int kAhead = 4;          // chunks of heads that are copied ahead
+constexpr int kAhead = 4;          // chunks of heads that are copied ahead of the two that are worked on
+constexpr int kRing = 8;           // places for them
 
 struct RopeArgs {
   RopeProblem p;
@@ -57,7 +59,7 @@ __device__ __forceinline__ void copy_wait() {
 // in lane u, or where pairs are half-split four of either half, 4 u .. and rot / 2 + 4 u ..,
 // so that a pair is in one lane.  kPaged: k and v go into the cache; else k to k_out.
 template <bool kF16, int kLanes, bool kInterleaved, bool kPaged>
-__global__ void __launch_bounds__(32 * kWarps, 8) norm_rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, 6) norm_rope_kernel(const __grid_constant__ RopeArgs a) {
   griddep_launch_dependents();
   constexpr int kHeads = 32 / kLanes;                       // heads that a warp has at a time
   const RopeProblem& p = a.p;
@@ -81,7 +83,7 @@ __global__ void __launch_bounds__(32 * kWarps, 8) norm_rope_kernel(const __grid_
   const uint16_t* v_at = static_cast<const uint16_t*>(p.v) + t * p.vs[0] + head0 * p.vs[1];
   const int end = min(chunks, (part + 1) * a.per);
   // A lane's own 16 bytes of each chunk that is under way.
-  __shared__ uint4 ring[kWarps][kAhead][32];
+  __shared__ uint4 ring[kWarps][kRing][32];
   uint4* mine = &ring[threadIdx.x >> 5][0][lane];
   auto fetch = [&](int c) {
     const int ck = c - q_chunks, cv = ck - k_chunks;
@@ -89,7 +91,7 @@ __global__ void __launch_bounds__(32 * kWarps, 8) norm_rope_kernel(const __grid_
     const int h = (is_q ? c : is_v ? cv : ck) * kHeads;
     if (c < end && on && h + head0 < (is_q ? p.Hq : p.Hkv)) {
       const uint16_t* from = is_q ? q_at + h * p.qs[1] : is_v ? v_at + h * p.vs[1] : k_at + h * p.ks[1];
-      const uint32_t to = smem_u32(mine + (c % kAhead) * 32);
+      const uint32_t to = smem_u32(mine + (c % kRing) * 32);
       if (kInterleaved) {
         copy16(to, from + d0);
       } else {
@@ -101,7 +103,7 @@ __global__ void __launch_bounds__(32 * kWarps, 8) norm_rope_kernel(const __grid_
   };
   // before the places and angles, which they do not need
 #pragma unroll 1
-  for (int k = 0; k < kAhead - 1; ++k) fetch(part * a.per + k);
+  for (int k = 0; k < kAhead; ++k) fetch(part * a.per + k);
 
   auto leave = [] { copy_wait<0>(); };   // no copy may outlive its thread's block
 
@@ -160,102 +162,119 @@ __global__ void __launch_bounds__(32 * kWarps, 8) norm_rope_kernel(const __grid_
       sn[j] *= p.amplitude;
     }
   }
-  auto put = [&](uint16_t* to, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+  auto put = [&](uint16_t* to, const uint32_t (&w)[4]) {
     if (kInterleaved) {
-      *reinterpret_cast<uint4*>(to + 8 * sub) = make_uint4(w0, w1, w2, w3);
+      *reinterpret_cast<uint4*>(to + d0) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
-      *reinterpret_cast<uint2*>(to + d0) = make_uint2(w0, w1);
-      *reinterpret_cast<uint2*>(to + d1) = make_uint2(w2, w3);
+      *reinterpret_cast<uint2*>(to + d0) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2*>(to + d1) = make_uint2(w[2], w[3]);
     }
   };
-  uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
-  auto weight = [&](const void* w) {
-    const uint2 lo = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + d0));
-    const uint2 hi = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + d1));
-    return make_uint4(lo.x, lo.y, hi.x, hi.y);
-  };
-  if (on && p.norm_q) wq = weight(p.q_weight);
-  if (on && p.norm_k) wk = weight(p.k_weight);
+  const bool codes = kPaged && a.c.codes, placed = page >= 0 && page < a.c.pages;   // else a position without a page
 
-  float inv_ks = 1.0f, inv_vs = 1.0f;
-  if (kPaged && a.c.codes) {
-    inv_ks = __frcp_rn(ld_f32(a.c.k_scale));
-    inv_vs = __frcp_rn(ld_f32(a.c.v_scale));
-  }
-
+  // The chunks lo .. hi - 1, of one kind (0 queries, 1 keys, 2 values), which begin with chunk
+  // c0: two at a time, so that one's reduction is under way with the other's.
+  auto section = [&](auto kind, int c0, int lo, int hi) {
+    constexpr int kKind = decltype(kind)::value;
+    constexpr bool kCache = kPaged && kKind > 0;
+    const int H = kKind == 0 ? p.Hq : p.Hkv;
+    const bool norm = kKind == 0 ? p.norm_q : kKind == 1 && p.norm_k;
+    F2 w[4] = {};
+    if (norm && on) {
+      const uint16_t* from = static_cast<const uint16_t*>(kKind == 0 ? p.q_weight : p.k_weight);
+      const uint2 w0 = __ldg(reinterpret_cast<const uint2*>(from + d0)), w1 = __ldg(reinterpret_cast<const uint2*>(from + d1));
+      w[0] = unpack16<kF16>(w0.x), w[1] = unpack16<kF16>(w0.y), w[2] = unpack16<kF16>(w1.x), w[3] = unpack16<kF16>(w1.y);
+    }
+    const int64_t* cell = kKind == 2 ? a.c.vs : a.c.ks;
+    const int64_t* row = kKind == 0 ? p.qos : p.kos;
+    const int64_t head = kCache ? cell[2] : row[1];
+    const int64_t first = kCache ? page * cell[0] + slot * cell[1] : t * row[0];
+    void* to = kKind == 0 ? p.q_out : !kPaged ? p.k_out : kKind == 1 ? a.c.k : a.c.v;
+    float inv_s = 1.0f;
+    if (kCache && codes) inv_s = __frcp_rn(ld_f32(kKind == 1 ? a.c.k_scale : a.c.v_scale));
 #pragma unroll 1
-  for (int c = part * a.per; c < end; ++c) {
-    fetch(c + kAhead - 1);   // to the place of the chunk before
-    copy_wait<kAhead - 1>();
-    // kinds and counts of a chunk are the same for the whole warp
-    const int ck = c - q_chunks, cv = ck - k_chunks;
-    const bool is_q = c < q_chunks, is_v = kPaged && cv >= 0;
-    const int h = (is_q ? c : is_v ? cv : ck) * kHeads + head0;
-    const bool there = on && h < (is_q ? p.Hq : p.Hkv);
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (there) x = mine[(c % kAhead) * 32];
-    const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-    uint32_t out[4] = {xw[0], xw[1], xw[2], xw[3]};
-    F2 v[4];
+    for (int c = lo; c < hi; c += 2) {
+      fetch(c + kAhead);
+      if (c + 1 < hi) fetch(c + kAhead + 1);
+      copy_wait<kAhead>();
+      F2 v[2][4];
+      uint32_t out[2][4];
+      bool there[2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = unpack16<kF16>(xw[e]);
-    if (!is_v) {
-      if (is_q ? p.norm_q : p.norm_k) {
-        F2 s2 = mul2(v[0], v[0]);
+      for (int u = 0; u < 2; ++u) {
+        there[u] = on && c + u < hi && (c + u - c0) * kHeads + head0 < H;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (there[u]) x = mine[((c + u) % kRing) * 32];
+        out[u][0] = x.x, out[u][1] = x.y, out[u][2] = x.z, out[u][3] = x.w;
 #pragma unroll
-        for (int e = 1; e < 4; ++e) s2 = fma2(v[e], v[e], s2);
-        float ss = __fadd_rn(s2.x, s2.y);
-#pragma unroll
-        for (int o = kLanes / 2; o >= 1; o /= 2) ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, o));
-        const F2 inv = splat(rsqrtf(fmaf(ss, a.inv_d, p.eps)));
-        const uint32_t ww[4] = {is_q ? wq.x : wk.x, is_q ? wq.y : wk.y, is_q ? wq.z : wk.z, is_q ? wq.w : wk.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = mul2(mul2(v[e], unpack16<kF16>(ww[e])), inv);
+        for (int e = 0; e < 4; ++e) v[u][e] = unpack16<kF16>(out[u][e]);
       }
-      if (turned) {
-        if (kInterleaved) {
+      if (kKind < 2) {
+        if (norm) {
+          float ss[2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            v[e] = fma2(v[e], splat(cs[e]), mul2(F2{v[e].y, v[e].x}, F2{-sn[e], sn[e]}));
-        } else {   // pairs of v[0], v[1] and v[2], v[3]
+          for (int u = 0; u < 2; ++u) {
+            F2 s2 = mul2(v[u][0], v[u][0]);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const F2 c2 = F2{cs[2 * e], cs[2 * e + 1]}, s2 = F2{sn[2 * e], sn[2 * e + 1]};
-            const F2 lo = v[e], hi = v[e + 2];
-            v[e] = fma2(lo, c2, mul2(neg(hi), s2));
-            v[e + 2] = fma2(hi, c2, mul2(lo, s2));
+            for (int e = 1; e < 4; ++e) s2 = fma2(v[u][e], v[u][e], s2);
+            ss[u] = __fadd_rn(s2.x, s2.y);
+          }
+#pragma unroll
+          for (int o = kLanes / 2; o >= 1; o /= 2)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) ss[u] = __fadd_rn(ss[u], __shfl_xor_sync(0xFFFFFFFFu, ss[u], o));
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const F2 inv = splat(rsqrtf(fmaf(ss[u], a.inv_d, p.eps)));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[u][e] = mul2(mul2(v[u][e], w[e]), inv);
           }
         }
-      }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) out[e] = cvt16x2(kF16, v[e].x, v[e].y);
-    }
-    if (!there) continue;
-    if (is_q) {
-      put(static_cast<uint16_t*>(p.q_out) + t * p.qos[0] + h * p.qos[1], out[0], out[1], out[2], out[3]);
-    } else if (!kPaged) {
-      put(static_cast<uint16_t*>(p.k_out) + t * p.kos[0] + h * p.kos[1], out[0], out[1], out[2], out[3]);
-    } else {
-      if (page < 0 || page >= a.c.pages) continue;        // a position without a page
-      const int64_t* cs3 = is_v ? a.c.vs : a.c.ks;
-      const int64_t at = page * cs3[0] + slot * cs3[1] + h * cs3[2];
-      void* cache = is_v ? a.c.v : a.c.k;
-      if (a.c.codes) {
-        const F2 f = splat(is_v ? inv_vs : inv_ks);
-        uint32_t q[4];
+        for (int u = 0; u < 2; ++u) {
+          if (turned) {
+            if (kInterleaved) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const F2 y = mul2(v[e], f);
-          q[e] = cvt_e4m3x2(y.x, y.y);
+              for (int e = 0; e < 4; ++e)
+                v[u][e] = fma2(v[u][e], splat(cs[e]), mul2(F2{v[u][e].y, v[u][e].x}, F2{-sn[e], sn[e]}));
+            } else {   // pairs of v[0], v[1] and v[2], v[3]
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const F2 c2 = F2{cs[2 * e], cs[2 * e + 1]}, s2 = F2{sn[2 * e], sn[2 * e + 1]};
+                const F2 x0 = v[u][e], x1 = v[u][e + 2];
+                v[u][e] = fma2(x0, c2, mul2(neg(x1), s2));
+                v[u][e + 2] = fma2(x1, c2, mul2(x0, s2));
+              }
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) out[u][e] = cvt16x2(kF16, v[u][e].x, v[u][e].y);
         }
-        uint8_t* to = static_cast<uint8_t*>(cache) + at;
-        *reinterpret_cast<uint32_t*>(to + d0) = q[0] | (q[1] << 16);
-        *reinterpret_cast<uint32_t*>(to + d1) = q[2] | (q[3] << 16);
-      } else {
-        put(static_cast<uint16_t*>(cache) + at, out[0], out[1], out[2], out[3]);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (!there[u] || (kCache && !placed)) continue;
+        const int64_t at = first + ((c + u - c0) * kHeads + head0) * head;
+        if (kCache && codes) {
+          uint32_t q[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const F2 y = mul2(v[u][e], splat(inv_s));
+            q[e] = cvt_e4m3x2(y.x, y.y);
+          }
+          uint8_t* cells = static_cast<uint8_t*>(to) + at;
+          *reinterpret_cast<uint32_t*>(cells + d0) = q[0] | (q[1] << 16);
+          *reinterpret_cast<uint32_t*>(cells + d1) = q[2] | (q[3] << 16);
+        } else {
+          put(static_cast<uint16_t*>(to) + at, out[u]);
+        }
       }
     }
-  }
+  };
+  const int begin = part * a.per, k0 = q_chunks, v0 = q_chunks + k_chunks;
+  section(std::integral_constant<int, 0>{}, 0, begin, min(end, k0));
+  section(std::integral_constant<int, 1>{}, k0, max(begin, k0), min(end, v0));
+  if (kPaged) section(std::integral_constant<int, 2>{}, v0, max(begin, v0), end);
   copy_wait<0>();
 }
 
