@@ -99,6 +99,8 @@ def exact_attention(b, q, causal=True, scale=None, max_q=None):
         e = A * E + h * (oi.abs() + A * E) + smallest_half(q.dtype)
         if h < 2.0 ** -10:
             e = e + x * 2.0 ** -25 * vf.abs().max()
+        if b.codes:   # weights beside E4M3 cells: see test_gpu_paged_attention.py
+            e = e + x * 2.0 ** -24 * vf.abs().max()
         # a value that is not finite and counts spoils its own column
         spoiled = torch.einsum("hlt,thd->lhd", (ok & (s > float("-inf"))).double(), (~torch.isfinite(v)).double()) > 0
         o[t0:t0 + m], err[t0:t0 + m] = torch.where(spoiled, float("nan"), oi), e

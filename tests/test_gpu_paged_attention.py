@@ -6,7 +6,12 @@ A = sum_j P_j |v_j|,
     E = h + 2 (2 D 2^-24 scale max sum|q k| + 2^-22 max|s log2 e| + 2^-22) + 4 (x + 64) 2^-24
 for x positions and h = half a step of the 16-bit type, and for f16, whose P is subnormal below 2^-14,
 another x 2^-25 max|v|.  E4M3 cells are exact in 16 bits; their scales are one more rounding of the score's factor
-and of the output's, which the 64 in E covers.
+and of the output's, which the 64 in E covers.  Beside them P is binary16, which is
+off by 2^-25 below 2^-14 where the row's largest weight is 1 or more, or three E4M3 terms t0 + t1 / 16 +
+t2 / 256: each rounds what the one before leaves, by 2^-4 of it or by half of
+the smallest step, 2^-10, so that 2^-12 of a weight (less than h) or 2^-10 / 256 = 2^-18 is left, where the
+row's largest weight is 2^6 or more.  Either is within 2^-24 of the largest weight, for
+x positions x 2^-24 max|v|.
 """
 
 import pytest
@@ -141,6 +146,16 @@ def test_pages_that_are_none_and_positions_beyond_the_table(W):
     q = queries(b, 4, 64)
     for causal in (True, False):
         check(call(W, b, q, causal=causal), *exact_attention(b, q, causal))
+
+
+@pytest.mark.parametrize("new", [1, 20, 200])
+def test_a_table_without_columns(W, new):
+    b = batch([new, 2], [50, 60], 16, 2, 64)
+    b.table, b.cols = b.table[:, :0].contiguous(), 0
+    q = queries(b, 4, 64)
+    out = torch.full_like(q, 5.0)
+    call(W, b, q, out=out)
+    assert not out.any()
 
 
 def test_uniform_batches_without_starts_and_shared_pages(W):

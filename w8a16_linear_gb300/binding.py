@@ -991,7 +991,7 @@ def qk_norm_rope(q, k, positions=None, turns=None, q_weight=None, k_weight=None,
     if q_out is None:
         q_out = _empty(shape, dtype, device, stream)
     desc = _rope_desc(M, Hq, Hk, D, *_rows(q, "q", dtype, device, shape), *sk, 0, 0, *_rows(q_out, "q_out", dtype, device, shape),
-                      *sko, pitch, dt, rot, interleaved, n_axes, *axes, eps, amplitude)
+                      *sko, pitch, dt, rot, bool(interleaved), n_axes, *axes, eps, amplitude)
     status = lib().qk_norm_rope(desc, q.data_ptr(), p_k, p_pos, p_turns, p_wq, p_wk, q_out.data_ptr(), p_ko,
                                           _raw_stream(stream, device))
     if status:
@@ -1071,7 +1071,7 @@ def paged_kv_append(k, v, k_cache, v_cache, page_table, q_start, kv_len, turns=N
     if k_weight is not None:
         p_wk = _like(k_weight, "k_weight", (dtype,), (D,), device)
     rot, n_axes, axes, p_turns, p_pos, pitch = _rotation(turns, positions, axes, T, device)
-    desc = _rope_desc(T, Hq, Hk, D, *sq, *sk, *sv, *sqo, 0, 0, pitch, dt, rot, interleaved, n_axes, *axes, eps, amplitude)
+    desc = _rope_desc(T, Hq, Hk, D, *sq, *sk, *sv, *sqo, 0, 0, pitch, dt, rot, bool(interleaved), n_axes, *axes, eps, amplitude)
     status = lib().paged_kv_append(
         desc, cache, p_q, k.data_ptr(), v.data_ptr(), p_pos, p_turns, p_wq, p_wk, k_cache.data_ptr(), v_cache.data_ptr(), p_table,
         None if q_start is None else _ints(q_start, "q_start", B + 1, device), _ints(kv_len, "kv_len", B, device),
@@ -1098,7 +1098,7 @@ def _paged_queries(q, k_cache, v_cache, page_table, max_q, causal, scale, out=No
         raise W8Error(2, f"q: heads of {D} dimensions, the cache's have {d}")
     sq = _rows(q, "q", dtype, device, shape)
     so = (H * D, D) if out is None else _rows(out, "out", out.dtype, device, shape)
-    desc = _paged_attention_desc(T, H, max(T, 1) if max_q is None else max_q, *sq, *so, dt, causal,
+    desc = _paged_attention_desc(T, H, max(T, 1) if max_q is None else max_q, *sq, *so, dt, bool(causal),
                                  D ** -0.5 if scale is None else scale)
     return desc, cache, B, p_table
 
