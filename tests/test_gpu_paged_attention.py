@@ -312,3 +312,11 @@ def test_nothing_to_do(W):
     torch.cuda.synchronize()
     assert (out == 5).all()
     assert DT["bf16"] == q.dtype
+
+
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("lens", [[1280], [1281], [1408], [1409], [1792], [1793], [1920], [1921], [1281] * 3, [1793, 1, 1281, 0, 2049]])
+def test_single_tokens_around_the_lengths_at_which_units_are_cut(W, lens, codes):
+    b = batch([min(x, 1) for x in lens], lens, 16, 2, 128, codes=codes)
+    q = queries(b, 8, 128)
+    check(call(W, b, q, max_q=1), *exact_attention(b, q))

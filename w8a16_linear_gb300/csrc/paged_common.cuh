@@ -594,8 +594,12 @@ inline cudaError_t read_paged_error(cudaStream_t st, uint32_t* err) {
 }
 }  // namespace
 
-// Units of few rows: cutting costs the time of about 5 tiles.
-constexpr Cutting kCutFew{2, 1.0f, 5.0f};
+// Units of few rows: cutting costs the time of 8 tiles, or of 12 of E4M3 cells, which are half
+// the bytes and take less.  Measured, 32/8 heads of 128, us with 5 / 8 / 12: one token over
+// 1024 and 1536 positions 12.0 / 11.8 / 11.8 and 12.9 / 12.9 / 15.0, 8 over up to 1500 and
+// 2500 18.7 / 17.9 / 15.9 and 23.4 / 23.4 / 23.8; over E4M3 cells, 16 up to 2500 and 4133
+// 28.1 / 22.5 / 22.5 and 32.7 / 32.7 / 28.8, one over 1536 13.4 / 12.5 / 11.1.
+constexpr Cutting kCutFew{2, 1.0f, 8.0f}, kCutFewCodes{2, 1.0f, 12.0f};
 
 // Units of at most kFewRows rows (paged_few.cu).
 constexpr int kFewRows = 16;

@@ -22,7 +22,21 @@
 // 3 N, and the softmax and epilogue threads add the three results.  A group's scores of a tile
 // are started before the products of the one before: two sets of S^T and P.
 //
-// Bound by the bytes of K and V.  Roundings below 32 bits: P (its sum l is taken
+// Bound by the bytes of K and V.  Measured (GB300, a replayed graph), 32 query and 8 key
+// heads of 128: 8 single tokens over 10335 to 20670 positions 90 us = 5.6 TB/s (0.84 of the
+// measured copy; by the 128-row kernel, as that was then, 115 us), 16 of them 160 us = 6.3 TB/s, 16 over
+// E4M3 cells 90 to 100 us = 5.1-5.7 TB/s (by the 128-row kernel 347; with V converted here 140, with its
+// codes as they are 115, with rows without a query left out of Q's terms 99).  One token over 512
+// positions: 8.4 us, a chain of latencies.  What runs once is mostly the
+// fetching of instructions: loops are not unrolled and rows without a query left out, four at
+// a time, where that makes the code shorter.
+//
+// Up to 16 rows.  A form of 32 against the 128-row kernel, both as they were then: 25 rows over 4133
+// positions 32.2 against 25.1 us, 32 rows over 4133 51.9 against 41.7, 32 over 512 20.4 against
+// 16.0; 20 rows over 20670 106 against 116, over E4M3 cells 283 against 331.  It won where few
+// rows meet a long cache and lost elsewhere, and spilled registers: left out.
+//
+// Roundings below 32 bits: P (its sum l is taken
 // before) and the output.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -187,7 +201,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     fence_proxy_async_smem();
   }
   griddep_wait();   // from here on what earlier kernels wrote may be read
-  if (warp == 0 && seqs) share_out_whole(a, seqs, tiles, reinterpret_cast<uint32_t*>(smem + C::kFirst), state, kCutFew);
+  if (warp == 0 && seqs) share_out_whole(a, seqs, tiles, reinterpret_cast<uint32_t*>(smem + C::kFirst), state,
+                                             kCodes ? kCutFewCodes : kCutFew);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
