@@ -562,7 +562,8 @@ typedef struct {
  *              the phase is position * turns[i] modulo 2^64, whose upper 32 bits
  *              are the angle.  NULL where rot is 0
  *   q_weight, k_weight   [D] of dtype, device, or NULL: no norm of q / of k
- *   q_out, k_out  by their strides, device, written; may be q and k themselves
+ *   q_out, k_out  by their strides, device, written; may be q and k themselves (the
+ *              same memory and strides); else they share no memory with an input
  * A norm or a rotation is wanted.  M == 0 launches nothing.
  * Errors: NULL, SHAPE, STRIDE, DTYPE, PARAM (eps, amplitude, nothing to do),
  * ALIGN (16 bytes; positions 4, turns 8), ARCH, CUDA.
@@ -634,7 +635,8 @@ typedef struct {
  *   s_out      NULL: out is of dtype.  Device float scalar (at least 2^-126): out
  *              is E4M3_satRNE(o / s_out) as for cross_attention
  *   out        [T, Hq, D] by o_stride, device, written for the first max_q tokens
- *              of each sequence; the other rows are left as they were
+ *              of each sequence; the other rows are left as they were.  It shares no
+ *              memory with the inputs
  *   ws         ws_floats floats, device, of which paged_attention_workspace() says
  *              how many the call needs; its contents need no set-up and mean
  *              nothing afterwards.  Calls that may run at the same time need one each
