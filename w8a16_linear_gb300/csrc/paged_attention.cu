@@ -12,7 +12,7 @@
 //
 // Sequences.  Starts, lengths and pages are the device's.  A unit of work is a
 // block of tokens of one sequence and key head; it has the key tiles up to its last
-// token's position.  A block takes whole units, the longest first, or, where the
+// token's position.  A block takes whole units, the longest first, dealt out to and fro, or, where the
 // lengths make that uneven or leave SMs idle, all tiles of all units stand in
 // one row of which each CTA takes an even share; every CTA decides that for itself from the
 // lengths, alike, and a second kernel joins the partial results.
@@ -1076,7 +1076,6 @@ cudaError_t launch_paged_attention(const PagedAttnProblem& p, const PagedCache& 
   a.blocks = x.blocks;
   a.items = (int)x.items;
   auto by = [](int64_t d) { return d == 1 ? 0ull : ~0ull / (uint64_t)d + 1; };
-  a.by_bh = by((int64_t)c.B * p.Hkv);
   a.by_hkv = by(p.Hkv);
   a.by_page = by(c.page_size);
   a.causal = p.causal;

@@ -31,7 +31,7 @@ struct PagedArgs {
   int max_q;
   int blocks;                 // units of a sequence and key head at most
   int items;                  // B * Hkv * blocks
-  uint64_t by_bh, by_hkv, by_page;   // 2^64 / d rounded up, 0 for d = 1
+  uint64_t by_hkv, by_page;          // 2^64 / d rounded up, 0 for d = 1
   int causal;
   int may_cut;
   int pages, page_size, cols, box, boxes;   // rows of a copy, copies of a tile and 64 dimensions
