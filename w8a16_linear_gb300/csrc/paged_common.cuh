@@ -381,6 +381,7 @@ __device__ __forceinline__ void share_out(const PagedArgs& a, const Seq* seqs, u
       if (b < a.B) first[b] = total + to - mine;
       total += __shfl_sync(0xFFFFFFFFu, to, 31);
     }
+    __syncwarp();   // first[] is read by other lanes than wrote it, and shuffles do not order memory
     items = __reduce_add_sync(0xFFFFFFFFu, items);
     longest = __reduce_max_sync(0xFFFFFFFFu, longest);
     zeros = __reduce_or_sync(0xFFFFFFFFu, zeros);
