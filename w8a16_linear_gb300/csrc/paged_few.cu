@@ -45,6 +45,7 @@
 #include <cstdint>
 
 #include "attention_common.cuh"
+#include "few_ring.h"
 #include "internal.h"
 #include "paged_common.cuh"
 #include "ptx.cuh"
@@ -161,6 +162,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   Seq* seqs = a.B <= kMaxSeqs ? reinterpret_cast<Seq*>(smem + C::kSeq) : nullptr;
   uint32_t* tiles = reinterpret_cast<uint32_t*>(smem + C::kTiles);
   int* state = reinterpret_cast<int*>(smem + C::kState);
+  int* copied = state + 8;                                     // [2][2]: the next filling by K's and V's copies of each group; passes' Q
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -279,7 +281,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         page = next;
       }
     }
-    if (!ok && lane == 0) record_timeout(abort);
+    if (lane == 0) {
+      copied[2 * is_v] = (int)entry[0];
+      copied[2 * is_v + 1] = (int)entry[1];
+      if (!is_v) copied[4] = (int)qcount;
+      if (!ok) record_timeout(abort);
+    }
   } else if (warp == 12 || warp == 15) {
     // ---------------------------------------------------------------- MMA issue, a thread for each group
     if (elect_one()) {
@@ -775,12 +782,22 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  // Every copy has landed: each was waited for by those that read it, unless they gave
-  // up.  Then the block stays for 5 ms, in which any copy under way lands.
+  // Every copy has landed before the block ends: each was waited for by those that read
+  // it, unless they gave up, and then here.
   if (*abort && threadIdx.x == 0) {
-    const uint64_t t0 = globaltimer_ns();
-    while (globaltimer_ns() - t0 < 5000000ull) {
-    }
+    volatile int never = 0;
+    auto landed = [&](uint32_t b, uint32_t parity) {
+      if (!mbar_wait(b, parity, &never, kWaitLimitNs)) atomicOr(&g_paged_err, kErrTimeout);
+    };
+    for (int v = 0; v < 2; ++v)
+      for (int i = 0; i < 2; ++i) {
+        const int ring = !kCodes ? R : v ? RV : RK;
+        for (int j = 1; j <= ring; ++j) {
+          const int e = unread_filling(copied[2 * v + i], copied[2 * (1 - v) + i], kCodes ? 1 : 2, ring, j);
+          if (e >= 0) landed(full_bar(stage_of(v, i, (uint32_t)e)), stage_phase(v, (uint32_t)e));
+        }
+      }
+    if (!kCodes && copied[4] > 0) landed(q_full, (uint32_t)(copied[4] - 1) & 1);
   }
   if (warp == 12) {
     tc_fence_after();
