@@ -765,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float sum = sum_l[i * kRows + row];
           const float f = sum == 0.0f ? 0.0f : __frcp_rn(sum) * v_scale;
           put_lse(x, i * kRows + row, sum_m[i * kRows + row], sum);
-          const bool spoilt = *dirty != 0;
+          const bool spoilt = __any_sync(0xFFFFFFFFu, *dirty != 0);   // a later tile may say so just now: the warp as one
           // A bulk copy writes whole rows of a warp: only where all of them are the sequence's.
           const bool bulk = a.tma_out && !spoilt && l_warp + warp_l <= x.left;
           __syncwarp();   // together again for the TMEM loads
@@ -842,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float f = sum == 0.0f ? 0.0f : __frcp_rn(sum) * v_scale;
         a0 *= f;
         a1 *= f;
-        const bool spoilt = *dirty != 0;
+        const bool spoilt = __any_sync(0xFFFFFFFFu, *dirty != 0);
         __syncwarp();   // together again for the TMEM loads
 #pragma unroll 1
         for (int c = 0; c < DP / 32; ++c) {
