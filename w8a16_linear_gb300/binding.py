@@ -859,8 +859,9 @@ def rope_frequencies(dim, base=10000.0, factor=1.0, trained=None, fast=32.0, slo
         return f / factor
     # the (fractional) pair that turns n times over the trained length
     pair = [half * math.log(trained / (2 * math.pi * n)) / math.log(base) for n in (fast, slow)]
-    low, high = max(math.floor(pair[0]), 0), min(math.ceil(pair[1]), half - 1)
-    keep = 1.0 - ((torch.arange(half, dtype=torch.float64) - low) / max(high - low, 1e-3)).clamp(0.0, 1.0)
+    # the ramp's ends, which may lie beyond the head's first and last pair
+    low, high = math.floor(pair[0]), math.ceil(pair[1])
+    keep = 1.0 - ((torch.arange(half, dtype=torch.float64) - low) / (high - low)).clamp(0.0, 1.0)
     return f * keep + f / factor * (1.0 - keep)
 
 
