@@ -44,3 +44,13 @@ def test_long_training_leaves_the_last_pair_on_the_ramp(b):
     assert math.isclose(float(r), 1 - 18 / 25 * 7 / 8, rel_tol=1e-12)   # the ramp goes from pair 45 to pair 70
     assert (b.rope_frequencies(64, 1e4, 8.0, 10 ** 9) == b.rope_frequencies(64, 1e4)).all()   # all are fast
     assert torch.allclose(b.rope_frequencies(64, 1e4, 8.0, 5), b.rope_frequencies(64, 1e4) / 8, rtol=1e-14)   # all are slow
+
+
+@pytest.mark.parametrize("bad", [dict(base=1.0), dict(base=0.5), dict(base=math.inf), dict(base=math.nan), dict(trained=math.inf),
+                                 dict(factor=math.inf), dict(fast=math.inf), dict(slow=0.0), dict(trained=-1)])
+def test_refusals_by_parts(b, bad):
+    """A base of 1 or less has no pair that turns a given number of times, or has them the other way round."""
+    with pytest.raises(b.W8Error) as e:
+        b.rope_frequencies(**dict(dict(dim=64, base=1e4, factor=4.0, trained=4096), **bad))
+    assert e.value.status == 11
+    assert len(b.rope_frequencies(64, base=1.0)) == 32 and len(b.rope_frequencies(64, base=0.5)) == 32

@@ -848,10 +848,12 @@ def rope_frequencies(dim, base=10000.0, factor=1.0, trained=None, fast=32.0, slo
     many times as long: all of them (positions are interpolated), or with
     ``trained``, the context length of the training, by parts: a pair that turns more
     than ``fast`` times over that length is kept, one that turns less than ``slow``
-    times is divided by ``factor``, with a linear ramp over the pairs between."""
+    times is divided by ``factor``, with a linear ramp over the pairs between (``base`` above 1)."""
     if dim < 2 or dim % 2:
         raise W8Error(2, f"dim={dim}: expected an even number of dimensions")
-    if not (base > 0 and factor > 0 and (trained is None or (trained > 0 and fast > slow > 0))):
+    # a base of 1 or less has no slow pairs at the head's end for a ramp to go to
+    if not (0 < base < math.inf and 0 < factor < math.inf
+            and (trained is None or (0 < trained < math.inf and math.inf > fast > slow > 0 and base > 1))):
         raise W8Error(11, f"base={base}, factor={factor}, trained={trained}, fast={fast}, slow={slow}")
     half = dim // 2
     f = torch.tensor([base ** (-i / half) for i in range(half)], dtype=torch.float64)
