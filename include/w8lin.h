@@ -650,7 +650,9 @@ w8_status paged_attention(const w8_paged_attention_desc* desc, const w8_paged_de
                           void* out, float* ws, int64_t ws_floats, void* stream);
 
 /* Floats of workspace that paged_attention needs for these sizes on the
- * current device.  Errors as above. */
+ * current device.  It goes by max_q (where that is below T), and fewer tokens may need more:
+ * up to 16 rows, max_q * Hq / Hkv of them, up to 128 and more are worked on in different ways.
+ * Errors as above. */
 w8_status paged_attention_workspace(const w8_paged_attention_desc* desc, const w8_paged_desc* cache, int64_t* floats);
 
 /*

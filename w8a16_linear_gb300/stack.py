@@ -238,10 +238,11 @@ class SelfSite:
 
     Made for at most ``tokens`` new tokens of ``batch`` sequences, at most ``max_q`` of
     one, in a cache ``k_cache``, ``v_cache`` [pages, page_size, kv_heads, D] and a page
-    table of ``columns`` entries for each sequence.  All buffers are the site's own, so
-    that a pass of as many tokens can be captured in a CUDA graph; the lengths,
+    table of ``columns`` entries for each sequence.  All buffers are made here and are the
+    site's own, so that a pass can be captured in a CUDA graph; the lengths,
     starts and pages are read when it runs, so the graph serves every step, and the
-    site has to live as long as it."""
+    site has to live as long as it.  Passes of one site, replayed ones among them, run one
+    after the other.  Tokens of no sequence have no output: what ``run`` returns for them means nothing."""
 
     def __init__(self, batch, tokens, max_q, hidden, heads, kv_heads, head_dim, k_cache, v_cache, columns, interleaved=False):
         device = k_cache.device
@@ -255,8 +256,22 @@ class SelfSite:
         self.q, self.k, self.v = (torch.empty((tokens, n, head_dim), **bf) for n in (heads, kv_heads, kv_heads))
         self.attn = torch.empty((tokens, heads, head_dim), **u8)
         self.y = torch.empty((tokens, hidden), **bf)
-        self.table = (batch, columns)
-        self.ws = {}                                  # tokens of a pass -> workspace
+        self.ws = self._workspace(batch, columns)
+
+    def _workspace(self, batch, columns):
+        """One for passes of any number of tokens.  The need goes by n = min(max_q, tokens of the pass): it
+        grows with n until every SM has a share, within up to 16 rows (n times the heads of a key
+        head), up to 128 and above, where other kernels take the call, and is 0 where the tiles are too many to be
+        shared out.  So the ends of these, and powers of two between."""
+        from . import binding as W
+        group, most = self.heads // self.kv_heads, min(self.max_q, max(self.q.shape[0], 1))
+        table = torch.empty((batch, columns), dtype=torch.int32, device=self.q.device)
+        ws = None
+        for n in {16 // group, 128 // group, most, *(1 << i for i in range(most.bit_length()))}:
+            if 1 <= n <= most:
+                more = W.paged_attention_workspace(self.q, self.k_cache, table, max_q=n)
+                ws = more if ws is None or more.numel() > ws.numel() else ws
+        return ws
 
     def run(self, W, w, x, residual, page_table, q_start, kv_len):
         """One pass over the tokens ``x`` [T, hidden] on the current stream: returns the
@@ -265,15 +280,12 @@ class SelfSite:
         T = x.shape[0]
         codes, s_tok, res, q, k, v, attn, y = (t[:T] for t in (self.codes, self.s_tok, self.res, self.q, self.k, self.v, self.attn,
                                                                self.y))
-        if T not in self.ws:
-            shape = torch.empty(self.table, dtype=torch.int32, device=x.device)
-            self.ws[T] = W.paged_attention_workspace(q, self.k_cache, shape, max_q=self.max_q)
         W.add_rms_norm_quant(x, residual, w.norm, out=codes, s_tok=s_tok, res_out=res)
         W.fp8_linear_w8a8_pertoken_group(codes, s_tok, [w.q[0], w.k[0], w.v[0]], [w.q[1], w.k[1], w.v[1]],
                                          outs=[t.view(T, -1) for t in (q, k, v)])
         W.paged_kv_append(k, v, self.k_cache, self.v_cache, page_table, q_start, kv_len, turns=w.turns, q=q, q_weight=w.q_norm,
                           k_weight=w.k_norm, interleaved=self.interleaved, k_scale=w.k_scale, v_scale=w.v_scale, q_out=q)
         W.paged_attention(q, self.k_cache, self.v_cache, page_table, q_start, kv_len, max_q=self.max_q, k_scale=w.k_scale,
-                          v_scale=w.v_scale, s_out=w.s_attn, out=attn, ws=self.ws[T])
+                          v_scale=w.v_scale, s_out=w.s_attn, out=attn, ws=self.ws)
         W.fp8_linear_w8a8(attn.view(T, -1), w.out[0], w.s_attn, w.out[1], out=y)
         return y, res
