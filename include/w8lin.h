@@ -623,7 +623,9 @@ typedef struct {
  *   o[i,h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q[i,h] . k_j - max)
  * with the key head h / (Hq / Hkv).  A row that sees no position is 0, and so is one whose
  * scores are all -inf.  What the cells of positions hold that a row does not see
- * (NaN included) has no effect on it.  With E4M3 cells k_j and v_j are the
+ * (NaN included) has no effect on it.  A value of V that is not finite and that a row sees
+ * gives it what the formula gives (an infinity, or NaN) where the value's p has not rounded to
+ * 0; where it has, one of the two.  With E4M3 cells k_j and v_j are the
  * codes' values times k_scale and v_scale.  Positions beyond the table do not
  * exist; a page outside 0 .. pages - 1 stands for zeros.  Scores, sums and
  * the accumulator are binary32, p is rounded to dtype for the product with V (beside

@@ -31,7 +31,7 @@
 // Positions that a row does not see have P = 0, but 0 * NaN would spoil the
 // product: V rows behind the unit's last position are cleared in shared memory.
 // Those that only some of a unit's rows see cannot be; if they hold a value that
-// is not finite, it is cleared too, and the rows that see it get their NaN at the end (spoil).
+// is not finite, it is cleared too, and added at the end to the rows that see it (restore).
 //
 // Measured (GB300, a replayed graph / one call among others): a chunk of 4096 tokens
 // over 20670 positions, 32 query and 8 key heads of 128, bf16: 921-937 / 926-956 us = 1.31-1.36
@@ -677,22 +677,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto put_lse = [&](const Item& x, int r, float m, float sum) {
       if (kind == 2) a.part_lse[(int64_t)x.part * kUnitRows + r] = sum == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) + log2f(sum);
     };
-    // The columns of this row in which a position that it sees, but not every row of the
-    // unit, has a value that is not finite (and was cleared): NaN.  Seldom called, and slow.
-    auto spoil = [&](const Item& x, int l, int row_group, uint8_t* row_at) {
-      if (pos >= a.rows_l || l >= x.left) return;
-      const int end = min(seen(a, x.pos0, x.len, l + 1), x.t1 * kKeys);
-      for (int j = max(x.lim0, x.t0 * kKeys); j < end; ++j) {
-        const int at = quotient(j, a.by_page), page = ld_i32(a.table + x.b * a.table_stride + at);
-        if (page < 0 || page >= a.pages) continue;
-        const uint8_t* v = a.v + page * a.vs[0] + (j - at * a.page_size) * a.vs[1] + x.hk * a.vs[2];
-        for (int d = 0; d < a.D; ++d) {
-          const bool bad = kCodes ? (v[d] & 0x7F) == 0x7F : (not_finite<kF16>(reinterpret_cast<const uint16_t*>(v)[d]) & 0x8000u) != 0;
-          if (!bad) continue;
-          if (kind == 2) reinterpret_cast<float*>(part_at(x, row_group, d >> 2))[d & 3] = __uint_as_float(0x7FC00000u);
-          else if (kind == 1) reinterpret_cast<uint16_t*>(row_at)[d] = kF16 ? 0x7E00 : 0x7FC0;
-          else row_at[d] = 0x7F;
+    // V's values that are not finite, at positions that this row (token l of the unit) sees
+    // but not every row of the unit, were cleared: they are added to its accumulator, as if
+    // their weights were 1, by the whole warp.  Seldom called, and slow.
+    auto restore = [&](const Item& x, int i, int l) {
+      const bool mine = pos < a.rows_l && l < x.left;
+      const int from = max(x.lim0, x.t0 * kKeys), end = mine ? min(seen(a, x.pos0, x.len, l + 1), x.t1 * kKeys) : 0;
+#pragma unroll 1
+      for (int d = 0; d < a.D; d += 4) {
+        float add[4] = {};
+        bool some = false;
+#pragma unroll 1
+        for (int j = from; j < end; ++j) {
+          if (!kShared && ((j / kKeys - x.t0) & 1) != i) continue;   // the other slot's tile
+          const int at = quotient(j, a.by_page), page = ld_i32(a.table + x.b * a.table_stride + at);
+          if (page < 0 || page >= a.pages) continue;
+          const uint8_t* v = a.v + page * a.vs[0] + (j - at * a.page_size) * a.vs[1] + x.hk * a.vs[2];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint16_t w;                                              // as it was in the tile, in P's type
+            if (kCodes) w = (v[d + e] & 0x7F) == 0x7F ? 0x7E00 : 0;
+            else w = reinterpret_cast<const uint16_t*>(v)[d + e];
+            if (!(not_finite<kP16>(w) & 0x8000u)) continue;
+            some = true;
+            add[e] += unpack16<kP16>(w).x;
+          }
         }
+        __syncwarp();
+        if (!__any_sync(0xFFFFFFFFu, some)) continue;
+        uint32_t o[4];
+        tmem_ld_32x32b_x4(o_col(i) + quad + d, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + add[e]);
+        tmem_st_32x32b_x4(o_col(i) + quad + d, o);
+        tmem_st_wait();
       }
     };
 
@@ -767,8 +786,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           put_lse(x, i * kRows + row, sum_m[i * kRows + row], sum);
           const bool spoilt = __any_sync(0xFFFFFFFFu, *dirty != 0);   // a later tile may say so just now: the warp as one
           // A bulk copy writes whole rows of a warp: only where all of them are the sequence's.
-          const bool bulk = a.tma_out && !spoilt && l_warp + warp_l <= x.left;
+          const bool bulk = a.tma_out && l_warp + warp_l <= x.left;
           __syncwarp();   // together again for the TMEM loads
+          if (__builtin_expect(spoilt, 0)) restore(x, i, l);
           // The accumulator goes to registers, packed, before anything is
           // stored: the next item's first product waits for it.
           auto free_o = [&] {
@@ -811,7 +831,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (bulk) put_bulk(x.row0 + l_warp, x.hk, w);
             else if (row_at) put_words(row_at, DP / 2, 2 * a.D, w);
           }
-          if (__builtin_expect(spoilt, 0)) spoil(x, l, 4 * i + (warp & 3), row_at);
           __syncwarp();
         }
       } else {
@@ -844,6 +863,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         a1 *= f;
         const bool spoilt = __any_sync(0xFFFFFFFFu, *dirty != 0);
         __syncwarp();   // together again for the TMEM loads
+        if (__builtin_expect(spoilt, 0)) {
+          restore(x, 0, pos);
+          if (n1 > 0) restore(x, 1, pos);
+        }
 #pragma unroll 1
         for (int c = 0; c < DP / 32; ++c) {
           uint32_t r[32];
@@ -881,7 +904,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
-        if (__builtin_expect(spoilt, 0)) spoil(x, pos, warp & 3, row_at);
         __syncwarp();
       }
     }

@@ -40,7 +40,7 @@ struct PagedArgs {
   const float *k_scale, *v_scale;           // of codes
   const void* q;              // queries and their element strides, where a kernel reads them itself
   int64_t q_l, q_h;
-  const uint8_t* v;           // the cache and its strides in bytes, for spoil()
+  const uint8_t* v;           // the cache and its strides in bytes, for values that are cleared in shared memory
   int64_t vs[3];
   float scale_log2;
   const float* s_out;         // not null: E4M3 output

@@ -666,22 +666,27 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       for (int t = 0; t < x.left; ++t)
         for (int h = 0; h < a.G; ++h) put((int64_t)(x.row0 + t) * a.o_l + (int64_t)(x.hk * a.G + h) * a.o_h + d, 0.0f);
     };
-    // Rows that see a position, which not every row of the unit sees, where dimension d
-    // is not finite (and was cleared).  Seldom called, and slow.
-    auto spoilt_rows = [&](const Item& x) {
-      uint32_t rows = 0;
-      if (d >= a.D) return rows;
+    // Rows that see a position, which not every row of the unit sees, where dimension d is +inf,
+    // and where it is -inf; NaN counts as both (it was cleared).  Seldom called, and slow.
+    auto spoilt_rows = [&](const Item& x, uint32_t (&rows)[2]) {
+      if (d >= a.D) return;
       const int end = min(x.limit, x.t1 * kKeys);
       for (int j = max(x.lim0, x.t0 * kKeys); j < end; ++j) {
         const int at = quotient(j, a.by_page), page = ld_i32(a.table + x.b * a.table_stride + at);
         if (page < 0 || page >= a.pages) continue;
         const uint8_t* v = a.v + page * a.vs[0] + (j - at * a.page_size) * a.vs[1] + x.hk * a.vs[2];
-        const bool bad = kCodes ? (v[d] & 0x7F) == 0x7F : (not_finite<kF16>(reinterpret_cast<const uint16_t*>(v)[d]) & 0x8000u) != 0;
-        if (!bad) continue;
+        bool plus, minus;
+        if (kCodes) {
+          plus = minus = (v[d] & 0x7F) == 0x7F;
+        } else {
+          const uint32_t w = reinterpret_cast<const uint16_t*>(v)[d], inf = kF16 ? 0x7C00u : 0x7F80u;
+          if ((w & inf) != inf) continue;
+          plus = w != (inf | 0x8000u);
+          minus = w != inf;
+        }
         for (int r = 0; r < x.left * a.G; ++r)
-          if (j < seen(a, x.pos0, x.len, r / a.G + 1)) rows |= 1u << r;
+          if (j < seen(a, x.pos0, x.len, r / a.G + 1)) rows[0] |= (uint32_t)plus << r, rows[1] |= (uint32_t)minus << r;
       }
-      return rows;
     };
     if (a.may_cut && state[kShares] > 0 && state[kZeros]) {   // units without a tile: their rows are zeros
       for (int it = blockIdx.x; it < a.B * a.Hkv; it += gridDim.x) {
@@ -733,7 +738,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         a0 *= f;
         a1 *= f;
       }
-      const uint32_t nan_rows = *dirty ? spoilt_rows(x) : 0;
+      uint32_t inf_rows[2] = {0, 0};
+      if (*dirty) spoilt_rows(x, inf_rows);
       __syncwarp();   // together again for the TMEM loads
       const int valid = x.left * a.G;
       int64_t at = (int64_t)x.row0 * a.o_l + (int64_t)x.hk * a.G * a.o_h + d;
@@ -760,7 +766,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           const float f0 = __shfl_sync(0xFFFFFFFFu, a0, r & 31), f1 = __shfl_sync(0xFFFFFFFFu, a1, r & 31);
           float y = o[0][e] * f0;
           if (two) y = fmaf(o[1][e], f1, y);
-          if (nan_rows >> r & 1) y = __uint_as_float(0x7FC00000u);
+          if (inf_rows[0] >> r & 1) y += INFINITY;
+          if (inf_rows[1] >> r & 1) y -= INFINITY;
           if (r < valid && d < a.D) {
             if (x.part >= 0) a.part[((int64_t)x.part * N + r) * DP + d] = y;
             else put(at, y);
