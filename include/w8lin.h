@@ -630,7 +630,8 @@ typedef struct {
  * exist; a page outside 0 .. pages - 1 stands for zeros.  Scores, sums and
  * the accumulator are binary32, p is rounded to dtype for the product with V (beside
  * E4M3 cells to 2^-11 of itself or 2^-24 of the row's largest; its sum is taken
- * before that); 2^8 times the sum of |v| over the positions has to stay within binary32.
+ * before that); beside E4M3 cells with at most 16 rows (max_q * Hq / Hkv) q is rounded by at most
+ * 2^-25 of its row's largest value.  2^8 times the sum of |v| over the positions has to stay within binary32.
  *   q          [T, Hq, D], device
  *   k_cache, v_cache, page_table, q_start, kv_len, k_scale, v_scale as for
  *              paged_kv_append; sequences may share pages

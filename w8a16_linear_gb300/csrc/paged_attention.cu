@@ -47,7 +47,8 @@
 // once each tile's copies waited for that load.  These two, and warps without rows left idle: prompts
 // 91.6 -> 75.4 us.
 //
-// Roundings below 32 bits: P (its sum l is taken before) and the output.
+// Roundings below 32 bits: P (its sum l is taken before), since the tensor core takes 32-bit weights
+// beside 32-bit values alone, which would be twice the bytes of V and half the rate; and the output.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

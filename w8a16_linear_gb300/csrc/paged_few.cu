@@ -15,10 +15,10 @@
 // with accumulators of their own, which the epilogue joins.
 //
 // E4M3 cells go to the tensor core as they are.  What stands beside them is split
-// into three E4M3 terms, x = (t0 + t1 / 16 + t2 / 256) 2^e, which leaves less than 2^-12 of
-// each value or 2^-18 in units of the terms: the queries, with 2^e from the row's largest
-// value (2^-27 of which is left of the smallest ones; nothing of a bf16 value), and P, whose largest
-// is kept between 2^6 and 2^8 (so that 2^-24 of it is left).  Terms are rows of their own,
+// into three E4M3 terms, x = (t0 + t1 / 16 + t2 / 256) 2^e, which leaves at most 2^-12 of
+// each value or 2^-18 in units of the terms: the queries, with the row's largest value in [2^7, 2^8)
+// of those (so that at most 2^-25 of it is left, and nothing of a bf16 value from 2^-17 of it on, of an f16
+// value from 2^-14 on), and P, whose largest is kept between 2^6 and 2^8 (so that 2^-24 of it is left).  Terms are rows of their own,
 // 3 N, and the softmax and epilogue threads add the three results.  A group's scores of a tile
 // are started before the products of the one before: two sets of S^T and P.
 //
@@ -36,8 +36,9 @@
 // 16.0; 20 rows over 20670 106 against 116, over E4M3 cells 283 against 331.  It won where few
 // rows meet a long cache and lost elsewhere, and spilled registers: left out.
 //
-// Roundings below 32 bits: P (its sum l is taken
-// before) and the output.
+// Roundings below 32 bits: P (its sum l is taken before), since the tensor core takes 32-bit weights
+// beside 32-bit values alone, which would be twice the bytes of V; beside E4M3 cells the terms
+// above; and the output.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
