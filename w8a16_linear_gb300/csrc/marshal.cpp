@@ -85,6 +85,15 @@ struct Call {
     }
     return (float)v;
   }
+  // What has no truth value raises in the binding's Python.
+  bool truth(PyObject* o) {
+    const int v = ok ? PyObject_IsTrue(o) : 0;
+    if (v < 0) {
+      PyErr_Clear();
+      ok = false;
+    }
+    return v == 1;
+  }
   // The current stream of the tensors' device, which has to be the current one.
   void* stream() {
     if (c10::cuda::current_device() != device.index()) ok = false;
@@ -207,7 +216,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) try {
   if (c.ok && p_turns && !p_pos) return left();
   d.dtype = c.dtype();
   d.eps = c.number(a[6]);
-  d.interleaved = PyObject_IsTrue(a[7]) == 1;
+  d.interleaved = c.truth(a[7]);
   d.amplitude = c.number(a[9]);
   void* stream = c.stream();
   if (!c.ok) return left();
@@ -252,7 +261,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) try {
   const float* p_vs = static_cast<const float*>(c.dense(a[17], at::kFloat, 1));
   d.dtype = c.dtype();
   d.eps = c.number(a[11]);
-  d.interleaved = PyObject_IsTrue(a[12]) == 1;
+  d.interleaved = c.truth(a[12]);
   d.amplitude = c.number(a[15]);
   void* stream = c.stream();
   if (!c.ok || a[6] == Py_None) return left();
@@ -294,7 +303,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) try {
     }
   }
   d.dtype = c.dtype();
-  d.causal = PyObject_IsTrue(a[7]) == 1;
+  d.causal = c.truth(a[7]);
   d.scale = a[8] == Py_None ? (float)std::pow((double)D, -0.5) : c.number(a[8]);
   void* stream = c.stream();
   if (!c.ok) return left();
