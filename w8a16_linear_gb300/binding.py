@@ -9,6 +9,7 @@ import ctypes
 import math
 import os
 import struct
+import sys
 from fractions import Fraction
 
 import torch
@@ -159,7 +160,10 @@ def lib():
         if os.path.exists(os.path.join(_HERE, "_marshal.so")):
             try:
                 from . import _marshal as m
-            except ImportError:   # of another PyTorch
+            except ImportError:   # of another PyTorch, whose names it lacks
+                return _lib
+            # of another whose names are the same, and tensors not: calls are marshalled in Python
+            if getattr(m, "built_for", None) != f"{torch.__version__} {sys.implementation.cache_tag}":
                 return _lib
             m.bind(*(ctypes.cast(getattr(l, n), ctypes.c_void_p).value for n in (
                 "qk_norm_rope", "paged_kv_append", "paged_attention", "paged_attention_workspace")))

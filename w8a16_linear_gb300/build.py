@@ -21,6 +21,7 @@ SOURCES = ["api.cu", "attention.cu", "elementwise.cu", "gemm.cu", "noalloc.cu", 
            "rmsnorm.cu", "rope.cu"]
 
 MARSHAL = os.path.join(HERE, "_marshal.so")
+MARSHAL_FOR = os.path.join(OUT_DIR, "marshal.txt")   # the PyTorch and Python that it was compiled with
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -55,25 +56,40 @@ def _compile(nvcc, src, obj, extra):
     return src, r.returncode, r.stdout + r.stderr
 
 
+def _marshal_stale(built_for):
+    """Whether csrc/marshal.cpp is newer than its module, or that is of another PyTorch or Python."""
+    src = os.path.join(CSRC, "marshal.cpp")
+    if _stale(MARSHAL, [src, os.path.join(ROOT, "include", "w8lin.h"), os.path.abspath(__file__)]):
+        return True
+    try:
+        with open(MARSHAL_FOR) as f:
+            return f.read() != built_for
+    except OSError:
+        return True
+
+
 def _marshal():
     """Compile the CPython module of csrc/marshal.cpp; returns what the compiler
     said where it failed (the binding then marshals in Python)."""
-    src = os.path.join(CSRC, "marshal.cpp")
-    if not _stale(MARSHAL, [src, os.path.join(ROOT, "include", "w8lin.h"), os.path.abspath(__file__)]):
+    import torch
+    built_for = f"{torch.__version__} {sys.implementation.cache_tag}"
+    if not _marshal_stale(built_for):
         return ""
     import sysconfig
 
-    import torch
     from torch.utils.cpp_extension import include_paths
+    src = os.path.join(CSRC, "marshal.cpp")
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
     tmp = f"{MARSHAL}.{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
     cmd += [f"-I{p}" for p in [*include_paths(), sysconfig.get_paths()["include"], cuda]]
-    cmd += [src, "-o", tmp, f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{libs}"]
+    cmd += [f'-DW8_BUILT_FOR="{built_for}"', src, "-o", tmp, f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{libs}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode == 0:
         os.replace(tmp, MARSHAL)
+        with open(MARSHAL_FOR, "w") as f:
+            f.write(built_for)
         return ""
     return r.stdout + r.stderr
 
