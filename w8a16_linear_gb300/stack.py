@@ -267,10 +267,11 @@ class SelfSite:
         group, most = self.heads // self.kv_heads, min(self.max_q, max(self.q.shape[0], 1))
         table = torch.empty((batch, columns), dtype=torch.int32, device=self.q.device)
         ws = None
-        for n in {16 // group, 128 // group, most, *(1 << i for i in range(most.bit_length()))}:
-            if 1 <= n <= most:
-                more = W.paged_attention_workspace(self.q, self.k_cache, table, max_q=n)
-                ws = more if ws is None or more.numel() > ws.numel() else ws
+        with torch.cuda.device(self.q.device):        # the need is that of the current device's SMs
+            for n in {16 // group, 128 // group, most, *(1 << i for i in range(most.bit_length()))}:
+                if 1 <= n <= most:
+                    more = W.paged_attention_workspace(self.q, self.k_cache, table, max_q=n)
+                    ws = more if ws is None or more.numel() > ws.numel() else ws
         return ws
 
     def run(self, W, w, x, residual, page_table, q_start, kv_len):
