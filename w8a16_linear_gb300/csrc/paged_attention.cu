@@ -34,13 +34,13 @@
 // is not finite, it is cleared too, and added at the end to the rows that see it (restore).
 //
 // Measured (GB300, a replayed graph / one call among others): a chunk of 4096 tokens
-// over 20670 positions, 32 query and 8 key heads of 128, bf16: 921-937 / 926-956 us = 1.31-1.36
+// over 20670 positions, 32 query and 8 key heads of 128, bf16: 911-942 / 953-961 us = 1.30-1.37
 // PFLOP/s; with 1024 tokens the tensor pipe is active in 53% of the cycles.  Over E4M3 cells
-// the chunk takes 1233 us: the conversion in shared memory is what differs.  Six prompts of
-// 629 to 1077 tokens, E4M3 out: 60.6 / 60.3 us; a tile of both slots takes 3450 cycles there (stamped in a
+// the chunk takes 1233-1268 us: the conversion in shared memory is what differs.  Six prompts of
+// 629 to 1077 tokens, E4M3 out: 59.1 / 58.9-59.2 us; a tile of both slots takes 3450 cycles there (stamped in a
 // copy of the kernel), the two products at the nominal rate 2048 of them, and the first tile of a
 // unit 1900 to 4100 more.  At most 25 rows (up to five tokens of seven sequences) over up to 4133
-// positions, 20/4 heads of 64, f16: 22.6 / 22.8-23.2 us, latency.
+// positions, 20/4 heads of 64, f16: 22.5-23.1 / 22.6-23.3 us, latency.
 //
 // Waits: a thread that sleeps on a barrier is woken about 1 us late, so the products' warp asks 256
 // times before it sleeps; page numbers are loaded raw and checked when they are used, since checked at
@@ -67,7 +67,8 @@ namespace w8 {
 namespace {
 
 // With 256 rows a unit cutting costs the time of about 10 tiles, with 128 rows about 8
-// (measured for cross attention, whose tiles these are).
+// (measured for cross attention, whose tiles these are; over E4M3 cells, where a tile takes a third
+// longer, not measured again).
 constexpr Cutting kCutShared{8, 1.0f, 10.0f}, kCutSplit{4, 1.4f, 8.0f};
 
 template <int DP, bool kCodes, bool kShared>

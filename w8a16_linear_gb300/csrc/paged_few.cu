@@ -23,7 +23,7 @@
 // are started before the products of the one before: two sets of S^T and P.
 //
 // Bound by the bytes of K and V.  Measured (GB300, a replayed graph), 32 query and 8 key
-// heads of 128: 8 single tokens over 10335 to 20670 positions 90 us = 5.6 TB/s (0.84 of the
+// heads of 128: 8 single tokens over 10335 to 20670 positions 87-92 us = 5.5-5.9 TB/s (0.83-0.88 of the
 // measured copy; by the 128-row kernel, as that was then, 115 us), 16 of them 160 us = 6.3 TB/s, 16 over
 // E4M3 cells 90 to 100 us = 5.1-5.7 TB/s (by the 128-row kernel 347; with V converted here 140, with its
 // codes as they are 115, with rows without a query left out of Q's terms 99).  One token over 512
