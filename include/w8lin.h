@@ -625,7 +625,7 @@ typedef struct {
  * scores are all -inf.  What the cells of positions hold that a row does not see
  * (NaN included) has no effect on it.  A value of V that is not finite and that a row sees
  * gives it what the formula gives (an infinity, or NaN) where the value's p has not rounded to
- * 0; where it has, one of the two.  With E4M3 cells k_j and v_j are the
+ * 0; where it has, what comes out is not specified.  With E4M3 cells k_j and v_j are the
  * codes' values times k_scale and v_scale.  Positions beyond the table do not
  * exist; a page outside 0 .. pages - 1 stands for zeros.  Scores, sums and
  * the accumulator are binary32, p is rounded to dtype for the product with V (beside
