@@ -38,7 +38,7 @@
 // over 20670 positions, 32 query and 8 key heads of 128, bf16: 911-942 / 953-961 us = 1.30-1.37
 // PFLOP/s; with 1024 tokens the tensor pipe is active in 53% of the cycles.  Over E4M3 cells
 // the chunk takes 1233-1268 us: the conversion in shared memory is what differs.  Six prompts of
-// 629 to 1077 tokens, E4M3 out: 59.1 / 58.9-59.2 us; a tile of both slots takes 3450 cycles there (stamped in a
+// 629 to 1077 tokens, E4M3 out: 58.8-59.2 / 58.9-59.6 us; a tile of both slots takes 3450 cycles there (stamped in a
 // copy of the kernel), the two products at the nominal rate 2048 of them, and the first tile of a
 // unit 1900 to 4100 more.  At most 25 rows (up to five tokens of seven sequences) over up to 4133
 // positions, 20/4 heads of 64, f16: 22.5-23.1 / 22.6-23.3 us, latency.
